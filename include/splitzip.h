@@ -406,6 +406,184 @@ sz_status sz_decode_blocks(const void *d_src, uint64_t src_pitch, const uint64_t
                            void *d_workspace, uint64_t workspace_bytes, int32_t *d_status,
                            hipStream_t stream);
 
+/* ---- operators on a paged cache ----------------------------------------
+ * What a server does with the pages of a BF16 KV cache besides shipping
+ * them (sz_encode_pages, sz_decode_pages): it puts the keys and values of
+ * new tokens into them and attends over them.  Not part of the explainers'
+ * method.  The calls below take one layer; they allocate nothing, never
+ * synchronise and may be captured into a graph.  `stream` must belong to
+ * the current device (SZ_ERR_INVALID_ARGUMENT otherwise).
+ *
+ * A head row is head_dim consecutive elements; head_dim is a multiple of 8,
+ * 8 .. 256.  Tensors of rows are described by sz_heads.  A tensor that a
+ * call writes must not overlap itself (rows lie inside one another's
+ * strides: tokens of heads, or heads of tokens) nor any other tensor of the
+ * call; two tensors may interleave with the same token stride (slices of
+ * one fused projection).  sz_qk_norm_rope and sz_kv_append may write a
+ * BF16 tensor in place: same data, strides and type as its source. */
+typedef enum {
+    SZ_TYPE_BF16 = 1,
+    SZ_TYPE_F32 = 2
+} sz_type;
+
+typedef struct {
+    void *data;            /* device address of token 0, head 0; 16-byte aligned */
+    uint64_t heads;        /* 1 .. 65535 */
+    uint64_t token_stride; /* elements from a token to the next; a multiple of 8, < 2^32 */
+    uint64_t head_stride;  /* elements from a head to the next; a multiple of 8, < 2^32 */
+    uint32_t type;         /* sz_type */
+} sz_heads;
+
+/* One layer's cache.  Sequence s keeps cached token c in page c /
+ * page_tokens of its row of the tables, d_k_pages[s * table_pitch + c /
+ * page_tokens] and the same of d_v_pages (device arrays of device
+ * addresses, 16-byte aligned), at element (c mod page_tokens) *
+ * token_stride + head * head_stride of the page.  With token_stride =
+ * kv_heads * head_dim and head_stride = head_dim a sequence's pages in
+ * table order are the tensor that sz_encode_pages reads.  A page spans
+ * (page_tokens - 1) * token_stride + (kv_heads - 1) * head_stride +
+ * head_dim BF16 words.  Table entries past a sequence's length, and those
+ * that no token of a call needs, are never used and may hold anything.
+ * Pages may be shared between sequences except where a call writes. */
+typedef struct {
+    const void *const *d_k_pages;
+    const void *const *d_v_pages;
+    uint64_t pages_per_seq; /* entries of a table row that may be used, >= 1 */
+    uint64_t table_pitch;   /* entries from a row to the next, >= pages_per_seq */
+    uint64_t token_stride;  /* elements; multiples of 8, < 2^32; rows must not overlap */
+    uint64_t head_stride;
+    uint32_t kv_heads;      /* 1 .. 65535 */
+    uint32_t head_dim;
+    uint32_t page_tokens;   /* a power of two, 16 .. 65536 */
+} sz_kv_cache;
+
+/* A ragged batch.  Sequence s has the new tokens d_starts[s] ..
+ * d_starts[s+1] - 1 of the call's token-major tensors, and d_lens[s]
+ * tokens in the cache, the new ones (its last) included.  Tokens before
+ * d_starts[0] and from d_starts[n_seqs] on belong to no sequence and are
+ * left as they are.  Both arrays are checked on the device. */
+typedef struct {
+    const int32_t *d_starts; /* n_seqs + 1 entries, ascending, 0 .. n_tokens */
+    const int32_t *d_lens;   /* n_seqs entries, 0 .. pages_per_seq * page_tokens */
+    uint64_t n_seqs;         /* 0 .. 65535 */
+    uint64_t n_tokens;       /* rows of the token-major tensors, < 2^31 */
+} sz_batch;
+
+/* Rotation of positions over the first rotary_dim elements of a head:
+ * pair i of rotary_dim / 2 turns by position * d_phases[i] / 2^64 turns,
+ * and cos and sin are multiplied by `magnitude`.  The product is taken
+ * modulo 2^64, so that no position loses accuracy. */
+typedef struct {
+    const uint64_t *d_phases; /* rotary_dim / 2 entries (sz_rope_phases) */
+    uint32_t rotary_dim;      /* a multiple of 8, 0 (no rotation) .. head_dim */
+    uint32_t interleaved;     /* 0: pair i is elements i, i + rotary_dim/2; 1: 2i, 2i + 1 */
+    float magnitude;
+} sz_rope;
+
+/* How sz_rope_frequencies stretches the frequencies f_i = base^(-2i/R),
+ * i < R/2, R = rotary_dim, by factor >= 1:
+ *  PLAIN   f_i
+ *  LINEAR  f_i / factor (position interpolation)
+ *  BASE    base becomes base * factor^(R/(R-2)) (R > 2)
+ *  RAMP    f_i where pair i turns more than `fast` times in original_len
+ *          positions, f_i / factor where fewer than `slow` times, and
+ *          between them a blend linear in i, from floor(i(fast)) to
+ *          ceil(i(slow)), i(t) = R ln(original_len / (2 pi t)) / (2 ln base);
+ *          *magnitude = 0.1 ln(factor) + 1 (YaRN)
+ *  BANDS   the same ends, and between them a blend linear in the turns */
+typedef enum {
+    SZ_ROPE_PLAIN = 0,
+    SZ_ROPE_LINEAR = 1,
+    SZ_ROPE_BASE = 2,
+    SZ_ROPE_RAMP = 3,
+    SZ_ROPE_BANDS = 4
+} sz_rope_stretch;
+
+/* Host-only: rotary_dim / 2 angles per position, in radians, to
+ * inv_freq[], and the magnitude (1 except RAMP).  rotary_dim even, base >
+ * 1, factor >= 1 (all but PLAIN), original_len >= 1 and fast > slow > 0
+ * (RAMP and BANDS); SZ_ERR_INVALID_ARGUMENT otherwise. */
+sz_status sz_rope_frequencies(uint32_t rotary_dim, double base, int stretch, double factor,
+                              double original_len, double slow, double fast, double *inv_freq,
+                              float *magnitude);
+
+/* Host-only: phases[i] = inv_freq[i] / (2 pi), its fraction in units of
+ * 2^-64 turns, from n angles per position in radians (finite). */
+sz_status sz_rope_phases(const double *inv_freq, uint64_t n, uint64_t *phases);
+
+/* Norm and rotation of queries and keys in one pass: for every token and
+ * head, y = x / sqrt(mean(x^2) + eps) * weight over the head's elements
+ * (weight NULL: y = x), then the rotation of the token's position, in FP32,
+ * rounded once to BF16.
+ *   q, q_out / k, k_out  source (BF16 or F32) and BF16 destination, each
+ *                        with n_tokens tokens; q or k (with its destination)
+ *                        may be NULL
+ *   d_q_weight, d_k_weight  optional device float[head_dim], 16-byte aligned
+ *   d_positions          device i32[n_tokens], any values
+ *   eps                  >= 0, finite (used with a weight)
+ *   rope                 NULL or rotary_dim 0: norm only */
+sz_status sz_qk_norm_rope(const sz_heads *q, const sz_heads *q_out, const float *d_q_weight,
+                          const sz_heads *k, const sz_heads *k_out, const float *d_k_weight,
+                          uint32_t head_dim, uint64_t n_tokens, const int32_t *d_positions,
+                          float eps, const sz_rope *rope, hipStream_t stream);
+
+/* Appends new tokens to the cache: token i of sequence s's n new ones goes
+ * to cache position c = d_lens[s] - n + i, its keys normed (with a weight)
+ * and rotated, its values as they are, both rounded to BF16; with q given,
+ * its queries are normed and rotated to q_out in the same launch.  The
+ * rotation's position is c, or d_positions[token] where given.  k and v
+ * have cache->kv_heads heads; every other argument as in sz_qk_norm_rope.
+ *   d_status  optional device i32[n_seqs]: SZ_OK, or
+ *             SZ_ERR_INVALID_ARGUMENT for a sequence whose starts are out
+ *             of order or range, whose length is below its new tokens' count
+ *             or past its pages, or one of whose written pages is NULL or
+ *             misaligned.  Of such a sequence the tokens that have no place
+ *             are not written and the others may be; nothing outside valid
+ *             pages is touched. */
+sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_weight,
+                       const sz_heads *q, const sz_heads *q_out, const float *d_q_weight,
+                       float eps, const sz_rope *rope, const int32_t *d_positions,
+                       const sz_kv_cache *cache, const sz_batch *batch, int32_t *d_status,
+                       hipStream_t stream);
+
+/* Attention of every new token over its sequence's cache.  Token i of
+ * sequence s's n new ones stands at position c = d_lens[s] - n + i; its
+ * query head h attends to the keys of KV head h / (q heads / kv_heads):
+ * those at j < d_lens[s], with `causal` j <= c, with window > 0 (causal
+ * only) j > c - window.  Scores are scale * q.k, with softcap > 0 softcap *
+ * tanh(scale * q.k / softcap).  A query that no key is visible to gives
+ * zeros and a log-sum of -infinity.  A key or value that a query does not
+ * see has no effect on it, whatever its bits.
+ * Scores, the softmax's maximum and sum, and the accumulated output are
+ * FP32; the weights are rounded to BF16 before they multiply the values.
+ *   q         BF16, batch->n_tokens tokens, heads a multiple of kv_heads
+ *   out       BF16 or F32, as many heads
+ *   d_lse     optional device float[n_tokens][q heads]: ln of the sum of
+ *             exp(score) over the visible keys
+ *   max_len   a host-side bound of d_lens (longer sequences are refused),
+ *             1 .. pages_per_seq * page_tokens; 0 means that product.  Work
+ *             is split for it, so it should not be far above the lengths.
+ *   scale     > 0, finite; softcap >= 0, finite (0: none)
+ *   d_workspace, workspace_bytes   256-byte aligned, at least
+ *             sz_attend_workspace_size(q->heads, cache, batch, max_len); any
+ *             content; NULL where that is 0.  Calls (or replays of graphs)
+ *             that may overlap need workspaces of their own.
+ *   d_status  optional device i32[n_seqs]: SZ_OK, or
+ *             SZ_ERR_INVALID_ARGUMENT for a sequence whose starts are out
+ *             of order or range, whose length is negative or above max_len,
+ *             or one of whose pages with a visible token is NULL or
+ *             misaligned.  The outputs of such a sequence are unspecified;
+ *             nothing outside valid pages is read.
+ * sz_attend_workspace_size reads n_seqs and n_tokens of the batch, not its
+ * arrays; 0 also for invalid arguments.  Host-only. */
+uint64_t sz_attend_workspace_size(uint64_t q_heads, const sz_kv_cache *cache,
+                                  const sz_batch *batch, uint64_t max_len);
+sz_status sz_attend_pages(const sz_heads *q, const sz_heads *out, float *d_lse,
+                          const sz_kv_cache *cache, const sz_batch *batch, uint64_t max_len,
+                          float scale, float softcap, int causal, uint64_t window,
+                          void *d_workspace, uint64_t workspace_bytes, int32_t *d_status,
+                          hipStream_t stream);
+
 /* ---- compressed transfer to and from host memory ----------------------
  * The explainers present the codec as a way to shrink the KV transfer
  * between prefill and decode servers (introduction and "Les Resultats").

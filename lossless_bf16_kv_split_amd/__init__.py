@@ -30,6 +30,9 @@ __all__ = [
     "sz_decode_workspace_size", "sz_decode_index", "sz_decode_tiles",
     "sz_encode_pages", "sz_decode_pages", "sz_blocks_workspace_size", "sz_encode_blocks",
     "sz_decode_blocks", "sz_blocks_decode_workspace_size", "sz_ship_to_host", "sz_ship_from_host", "ShipContext",
+    "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
+    "sz_attend_workspace_size", "sz_attend_pages", "Heads", "KVCache", "Batch", "Rope",
+    "rope_phases", "rope", "paged_cache", "qk_norm_rope", "kv_append", "attend_pages",
     "sz_status_string", "encode",
     "decode", "encode_blocks", "decode_blocks", "BlockContainers",
     "PREFIX_BYTES", "MAX_ELEMENTS", "NOALLOC_WORKSPACE_BYTES",
@@ -45,6 +48,15 @@ SZ_ERR_CAPACITY = 2
 SZ_ERR_TOO_LARGE = 3
 SZ_ERR_CORRUPT = 4
 SZ_ERR_HIP = 5
+
+SZ_TYPE_BF16 = 1
+SZ_TYPE_F32 = 2
+
+SZ_ROPE_PLAIN = 0
+SZ_ROPE_LINEAR = 1
+SZ_ROPE_BASE = 2
+SZ_ROPE_RAMP = 3
+SZ_ROPE_BANDS = 4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libsplitzip.so")
@@ -102,7 +114,18 @@ def _load() -> ctypes.CDLL:
     L.sz_ship_context_destroy.restype = None
     L.sz_ship_to_host_ctx.argtypes = [p, p, u64, p, u64, p, p]
     L.sz_ship_from_host_ctx.argtypes = [p, p, p, u64, p, p, p]
-    for name in ("sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
+    f32, f64, pd = ctypes.c_float, ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+    L.sz_rope_frequencies.argtypes = [ctypes.c_uint32, f64, i32, f64, f64, f64, f64, pd,
+                                      ctypes.POINTER(f32)]
+    L.sz_rope_phases.argtypes = [pd, u64, p]
+    # descriptors go as addresses (None = NULL)
+    L.sz_qk_norm_rope.argtypes = [p, p, p, p, p, p, ctypes.c_uint32, u64, p, f32, p, p]
+    L.sz_kv_append.argtypes = [p, p, p, p, p, p, f32, p, p, p, p, p, p]
+    L.sz_attend_workspace_size.argtypes = [u64, p, p, u64]
+    L.sz_attend_workspace_size.restype = u64
+    L.sz_attend_pages.argtypes = [p, p, p, p, p, u64, f32, f32, i32, u64, p, u64, p, p]
+    for name in ("sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
+                 "sz_attend_pages", "sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
                  "sz_encode_pack", "sz_encode_pack_ranked", "sz_encode_sample",
                  "sz_encode_first_pass", "sz_encode_finish",
                  "sz_decode_unpack", "sz_decode_scatter", "sz_decode_fused",
@@ -353,6 +376,234 @@ class ShipContext:
                "sz_ship_from_host_ctx")
 
 
+# ---- operators on a paged cache --------------------------------------------
+# Descriptors of tensors, cache, batch and rotation: made once, kept as long
+# as the buffers they describe (which they hold a reference to), and passed to
+# any number of calls.
+
+def _on_device(t, dtype, what: str, dim: int | None = None):
+    if not hasattr(t, "is_cuda") or not t.is_cuda or t.dtype != dtype or \
+            (dim is not None and t.dim() != dim) or (t.numel() > 0 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must be a CUDA tensor of {dtype}"
+                         + (f" with {dim} dimensions" if dim else "")
+                         + ", its last dimension contiguous")
+    return t
+
+
+class _Descriptor(ctypes.Structure):
+    def _set(self, device, *keep):
+        self._keep, self._device, self._at = keep, device, ctypes.addressof(self)
+
+
+class Heads(_Descriptor):
+    """sz_heads of a CUDA tensor [tokens, heads, head_dim] of bfloat16 or
+    float32 with a contiguous last dimension (any view of one whose strides
+    and address are multiples of 8 elements and 16 bytes)."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_uint64),
+                ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+                ("type", ctypes.c_uint32)]
+
+    def __init__(self, t):
+        import torch
+        if not hasattr(t, "is_cuda") or not t.is_cuda or t.dim() != 3 or \
+                t.dtype not in (torch.bfloat16, torch.float32) or \
+                (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError("head rows must be a CUDA tensor [tokens, heads, head_dim] of "
+                             "bfloat16 or float32, its last dimension contiguous")
+        strides = [t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
+        super().__init__(t.data_ptr(), t.shape[1], strides[0], strides[1],
+                         SZ_TYPE_F32 if t.dtype == torch.float32 else SZ_TYPE_BF16)
+        self.tokens, self.head_dim = t.shape[0], t.shape[2]
+        self._set(t.device, t)
+
+
+class KVCache(_Descriptor):
+    """sz_kv_cache: k_pages and v_pages are int64 CUDA tensors [sequences,
+    pages] of page addresses, of the same shape and row stride; strides in
+    elements of a page (default: [token][head][dim])."""
+    _fields_ = [("d_k_pages", ctypes.c_void_p), ("d_v_pages", ctypes.c_void_p),
+                ("pages_per_seq", ctypes.c_uint64), ("table_pitch", ctypes.c_uint64),
+                ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+                ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32)]
+
+    def __init__(self, k_pages, v_pages, kv_heads: int, head_dim: int, page_tokens: int,
+                 token_stride: int | None = None, head_stride: int | None = None, keep=None):
+        import torch
+        for t in (k_pages, v_pages):
+            _on_device(t, torch.int64, "a page table", 2)
+        pitch = [t.stride(0) if t.shape[0] > 1 else t.shape[1] for t in (k_pages, v_pages)]
+        if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device or \
+                pitch[0] != pitch[1]:
+            raise ValueError("the page tables must have the same shape, strides and device")
+        super().__init__(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[1], pitch[0],
+                         kv_heads * head_dim if token_stride is None else token_stride,
+                         head_dim if head_stride is None else head_stride,
+                         kv_heads, head_dim, page_tokens)
+        self.rows = k_pages.shape[0]
+        self._set(k_pages.device, k_pages, v_pages, keep)
+
+
+class Batch(_Descriptor):
+    """sz_batch: starts and lens are int32 CUDA tensors of n_seqs + 1 and
+    n_seqs entries; n_tokens is the row count of the token-major tensors."""
+    _fields_ = [("d_starts", ctypes.c_void_p), ("d_lens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_uint64), ("n_tokens", ctypes.c_uint64)]
+
+    def __init__(self, starts, lens, n_tokens: int):
+        import torch
+        for t in (starts, lens):
+            _on_device(t, torch.int32, "starts and lens", 1)
+        if starts.numel() != lens.numel() + 1 or starts.device != lens.device:
+            raise ValueError("starts must have one entry more than lens, on the same device")
+        super().__init__(starts.data_ptr(), lens.data_ptr(), lens.numel(), n_tokens)
+        self._set(starts.device, starts, lens)
+
+
+class Rope(_Descriptor):
+    """sz_rope: phases is an int64 CUDA tensor of rotary_dim / 2 entries (the
+    64-bit patterns of sz_rope_phases, see rope_phases and rope)."""
+    _fields_ = [("d_phases", ctypes.c_void_p), ("rotary_dim", ctypes.c_uint32),
+                ("interleaved", ctypes.c_uint32), ("magnitude", ctypes.c_float)]
+
+    def __init__(self, phases, interleaved: bool = False, magnitude: float = 1.0):
+        import torch
+        _on_device(phases, torch.int64, "phases", 1)
+        super().__init__(phases.data_ptr(), 2 * phases.numel(), int(bool(interleaved)), magnitude)
+        self._set(phases.device, phases)
+
+
+def _at(x) -> int | None:
+    """Address of a descriptor, or of a tensor (a descriptor of its own is
+    made, and must be kept until the call returns)."""
+    return None if x is None else x._at
+
+
+def _heads(x):
+    return x if x is None or isinstance(x, Heads) else Heads(x)
+
+
+def _same_device(*xs):
+    """The device of the descriptors and tensors given (None skipped)."""
+    devices = {x._device if isinstance(x, _Descriptor) else x.device for x in xs
+               if x is not None and not isinstance(x, int)}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _device_stream(device, stream):
+    """Stream handle, with the tensors' device required to be current."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _tokens(n: int, *xs) -> None:
+    for x in xs:
+        if x is not None and x.tokens != n:
+            raise ValueError(f"{x.tokens} tokens where {n} are expected")
+
+
+def _dims(dim: int, *xs) -> None:
+    for x in xs:
+        if x is not None and x.head_dim != dim:
+            raise ValueError(f"rows of {x.head_dim} elements where {dim} are expected")
+
+
+def _array(x, dtype, n: int, what: str) -> None:
+    if x is not None and not isinstance(x, int) and \
+            (x.dtype != dtype or x.numel() < n or not x.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous tensor of at least {n} {dtype}")
+
+
+def sz_rope_frequencies(rotary_dim: int, base: float, stretch: int = SZ_ROPE_PLAIN,
+                        factor: float = 1.0, original_len: float = 0.0, slow: float = 1.0,
+                        fast: float = 32.0):
+    """Angles per position (a list of rotary_dim / 2 floats) and magnitude."""
+    out = (ctypes.c_double * max(1, rotary_dim // 2))()
+    magnitude = ctypes.c_float()
+    _check(_lib.sz_rope_frequencies(rotary_dim, base, stretch, factor, original_len, slow, fast,
+                                    out, ctypes.byref(magnitude)), "sz_rope_frequencies")
+    return list(out), magnitude.value
+
+
+def sz_rope_phases(inv_freq):
+    """Phases of a sequence of angles per position, as a ctypes uint64 array."""
+    n = len(inv_freq)
+    out = (ctypes.c_uint64 * n)()
+    _check(_lib.sz_rope_phases((ctypes.c_double * n)(*inv_freq), n, out), "sz_rope_phases")
+    return out
+
+
+def sz_qk_norm_rope(q, q_out, q_weight, k, k_out, k_weight, head_dim: int, n_tokens: int,
+                    positions, eps: float, rope, stream=None) -> None:
+    """q, q_out, k, k_out: Heads, or tensors [tokens, heads, head_dim]; rope: a
+    Rope or None."""
+    import torch
+    q, q_out, k, k_out = _heads(q), _heads(q_out), _heads(k), _heads(k_out)
+    device = _same_device(q, q_out, q_weight, k, k_out, k_weight, positions, rope)
+    _tokens(n_tokens, q, q_out, k, k_out)
+    _dims(head_dim, q, q_out, k, k_out)
+    _array(q_weight, torch.float32, head_dim, "q_weight")
+    _array(k_weight, torch.float32, head_dim, "k_weight")
+    _array(positions, torch.int32, n_tokens, "positions")
+    _check(_lib.sz_qk_norm_rope(_at(q), _at(q_out), _ptr(q_weight), _at(k), _at(k_out),
+                                _ptr(k_weight), head_dim, n_tokens, _ptr(positions), eps,
+                                _at(rope), _device_stream(device, stream)), "sz_qk_norm_rope")
+
+
+def _check_batch(cache, batch, d_status) -> None:
+    import torch
+    if batch.n_seqs > cache.rows:
+        raise ValueError(f"{batch.n_seqs} sequences, {cache.rows} rows in the page tables")
+    _array(d_status, torch.int32, batch.n_seqs, "d_status")
+
+
+def sz_kv_append(k, v, k_weight, q, q_out, q_weight, eps: float, rope, positions, cache, batch,
+                 d_status=None, stream=None) -> None:
+    """k, v, q, q_out: Heads, or tensors [tokens, heads, head_dim]; cache: a
+    KVCache; batch: a Batch; rope: a Rope or None."""
+    import torch
+    k, v, q, q_out = _heads(k), _heads(v), _heads(q), _heads(q_out)
+    device = _same_device(k, v, k_weight, q, q_out, q_weight, rope, positions, cache, batch,
+                          d_status)
+    _tokens(batch.n_tokens, k, v, q, q_out)
+    _dims(cache.head_dim, k, v, q, q_out)
+    _array(q_weight, torch.float32, cache.head_dim, "q_weight")
+    _array(k_weight, torch.float32, cache.head_dim, "k_weight")
+    _array(positions, torch.int32, batch.n_tokens, "positions")
+    _check_batch(cache, batch, d_status)
+    _check(_lib.sz_kv_append(_at(k), _at(v), _ptr(k_weight), _at(q), _at(q_out), _ptr(q_weight),
+                             eps, _at(rope), _ptr(positions), _at(cache), _at(batch),
+                             _ptr(d_status), _device_stream(device, stream)), "sz_kv_append")
+
+
+def sz_attend_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
+    return int(_lib.sz_attend_workspace_size(q_heads, _at(cache), _at(batch), max_len))
+
+
+def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softcap: float = 0.0,
+                    causal: bool = True, window: int = 0, workspace=None,
+                    workspace_bytes: int = 0, d_status=None, stream=None) -> None:
+    """q, out: Heads, or tensors [tokens, heads, head_dim]; lse: a float32
+    tensor [tokens, heads] or None; cache: a KVCache; batch: a Batch."""
+    import torch
+    q, out = _heads(q), _heads(out)
+    device = _same_device(q, out, lse, cache, batch, workspace, d_status)
+    _tokens(batch.n_tokens, q, out)
+    _dims(cache.head_dim, q, out)
+    _array(lse, torch.float32, batch.n_tokens * q.heads, "lse")
+    _array(workspace, torch.uint8, workspace_bytes, "workspace")
+    _check_batch(cache, batch, d_status)
+    _check(_lib.sz_attend_pages(_at(q), _at(out), _ptr(lse), _at(cache), _at(batch), max_len,
+                                scale, softcap, int(causal), window, _ptr(workspace),
+                                workspace_bytes, _ptr(d_status), _device_stream(device, stream)),
+           "sz_attend_pages")
+
+
 # ---- conveniences (torch allocates; the library computes) -----------------
 
 def encode(x, stream=None):
@@ -454,3 +705,101 @@ def decode_blocks(blocks: BlockContainers, outputs, stream=None, check: bool = T
             b = int(bad[0])
             raise SplitZipError(int(st[b]), f"sz_decode_blocks (block {b})")
     return outputs
+
+
+def rope_phases(inv_freq):
+    """sz_rope_phases as a CPU int64 tensor (the same 64 bits)."""
+    import torch
+    return torch.tensor([x - (1 << 64) if x >> 63 else x for x in sz_rope_phases(inv_freq)],
+                        dtype=torch.int64)
+
+
+def rope(rotary_dim: int, base: float = 10000.0, stretch: int = SZ_ROPE_PLAIN,
+         factor: float = 1.0, original_len: float = 0.0, slow: float = 1.0, fast: float = 32.0,
+         interleaved: bool = False, device="cuda") -> Rope:
+    """The rotation of sz_rope_frequencies' frequencies, on a device."""
+    freq, magnitude = sz_rope_frequencies(rotary_dim, base, stretch, factor, original_len, slow,
+                                          fast)
+    return Rope(rope_phases(freq).to(device), interleaved, magnitude)
+
+
+def paged_cache(k_pool, v_pool, table) -> KVCache:
+    """The cache of two pools [pages, page_tokens, kv_heads, head_dim] of
+    bfloat16 (any strides that keep head_dim contiguous, so that a permuted
+    [pages, kv_heads, page_tokens, head_dim] pool does too) and an integer
+    table [sequences, pages] of page numbers, negative for none.  The address
+    tables are made here; make the cache again when the table changes."""
+    import torch
+    for t in (k_pool, v_pool):
+        _on_device(t, torch.bfloat16, "a pool", 4)
+    if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride():
+        raise ValueError("the pools must have the same shape and strides")
+    if table.dim() != 2 or table.dtype not in (torch.int32, torch.int64) or \
+            not (table.device == k_pool.device == v_pool.device):
+        raise ValueError("the table must be a 2-D integer tensor on the pools' device")
+    ids = table.to(torch.int64)
+    if ids.numel() > 0 and int(ids.max()) >= k_pool.shape[0]:
+        raise ValueError("a page number past the pool")
+    step = k_pool.stride(0) * 2
+
+    def addresses(pool):
+        return torch.where(ids >= 0, pool.data_ptr() + ids * step, torch.zeros_like(ids))
+
+    return KVCache(addresses(k_pool), addresses(v_pool), k_pool.shape[2], k_pool.shape[3],
+                   k_pool.shape[1], k_pool.stride(1), k_pool.stride(2), keep=(k_pool, v_pool))
+
+
+def _raise_on(status, call: str) -> None:
+    st = status.cpu()
+    bad = (st != SZ_OK).nonzero()
+    if bad.numel():
+        s = int(bad[0])
+        raise SplitZipError(int(st[s]), f"{call} (sequence {s})")
+
+
+def qk_norm_rope(q, k, positions, rope=None, q_weight=None, k_weight=None, eps: float = 1e-6):
+    """Norm and rotate queries and keys [tokens, heads, head_dim] (either may
+    be None); returns new bfloat16 tensors (sz_qk_norm_rope)."""
+    import torch
+    some = q if q is not None else k
+    out = [None if x is None else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+           for x in (q, k)]
+    sz_qk_norm_rope(q, out[0], q_weight, k, out[1], k_weight, some.shape[2], some.shape[0],
+                    positions, eps, rope)
+    return out[0], out[1]
+
+
+def kv_append(k, v, cache, batch, rope=None, q=None, k_weight=None, q_weight=None,
+              eps: float = 1e-6, positions=None, check: bool = True):
+    """Append new tokens to a paged cache (sz_kv_append); returns the turned
+    queries as a new bfloat16 tensor where q is given (rows of no sequence
+    are zero).  With ``check`` the statuses are read back (synchronising)
+    and a failure raises, naming the first sequence that failed."""
+    import torch
+    out = None if q is None else torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=k.device) if check else None
+    sz_kv_append(k, v, k_weight, q, out, q_weight, eps, rope, positions, cache, batch, status)
+    if check:
+        _raise_on(status, "sz_kv_append")
+    return out
+
+
+def attend_pages(q, cache, batch, max_len: int = 0, scale: float | None = None,
+                 softcap: float = 0.0, causal: bool = True, window: int = 0, out_dtype=None,
+                 check: bool = True):
+    """Attention of queries [tokens, heads, head_dim] over a paged cache
+    (sz_attend_pages); returns the output (bfloat16 unless ``out_dtype`` is
+    float32) and the log-sums [tokens, heads], zero for rows of no sequence.
+    scale defaults to head_dim ** -0.5; ``check`` as in kv_append."""
+    import torch
+    out = torch.zeros(q.shape, dtype=out_dtype or torch.bfloat16, device=q.device)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+    size = sz_attend_workspace_size(q.shape[1], cache, batch, max_len)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=q.device) if check else None
+    sz_attend_pages(q, out, lse, cache, batch, max_len,
+                    q.shape[2] ** -0.5 if scale is None else scale, softcap, causal, window, ws,
+                    size, status)
+    if check:
+        _raise_on(status, "sz_attend_pages")
+    return out, lse

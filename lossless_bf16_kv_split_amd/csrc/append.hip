@@ -1,0 +1,314 @@
+// append.hip -- norms and rotation of queries and keys, and the append of
+// new tokens' keys and values to a paged cache.
+//
+// For a head row x of D elements and a token at position p:
+//   y = x / sqrt(mean(x^2) + eps) * weight           (with a weight)
+//   (a, b) -> m (a cos t - b sin t), m (b cos t + a sin t)
+// for each pair (a, b) = (y_i, y_{i+R/2}) or (y_2i, y_{2i+1}), i < R/2, with
+// the angle t = p * phase_i / 2^64 turns.  FP32 throughout, one rounding to
+// BF16 at the store.
+//
+// The angle is exact: p * phase_i modulo 2^64 is the fraction of a turn in
+// fixed point, whatever p, and its top 32 bits carry an error below 2^-32
+// turns.  cos and sin are Taylor polynomials on an eighth of a turn (the
+// first terms left out are below 2^-25 there), so no table is read.
+//
+// Bound by the bytes of the rows, and for few tokens by latency.  A row
+// lies across 8 to 64 lanes of a wave, each with 8 (or 4) consecutive
+// elements; a wave works on one token, computes that token's angles once
+// and walks rows of it.
+#include "kv_internal.h"
+
+namespace sz {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kWavesPerGroup = kThreads / kWave;
+// Waves that fill the chip (256 CUs, 16 each): with fewer tokens than
+// this, a token's rows are shared among several waves.
+constexpr uint64_t kFillWaves = 4096;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// cos and sin of a / 2^32 turns
+__device__ __forceinline__ void turn_of(uint32_t a, float& c, float& s) {
+    const uint32_t quarter = (a + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(a - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float z = x * x;
+    const float sn =
+        fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f),
+                         -1.6666667e-1f), x);
+    const float cs =
+        fmaf(z, fmaf(z, fmaf(z, fmaf(z, 2.4801587e-5f, -1.3888889e-3f), 4.1666667e-2f), -0.5f),
+             1.0f);
+    const float u = (quarter & 1) ? sn : cs, v = (quarter & 1) ? cs : sn;
+    c = __uint_as_float(__float_as_uint(u) ^ (((quarter + 1) & 2) << 30));
+    s = __uint_as_float(__float_as_uint(v) ^ ((quarter & 2) << 30));
+}
+
+// VEC elements of a row from element e of it, as floats
+template <int VEC>
+__device__ __forceinline__ void load_row(const Rows& r, uint64_t at, float (&x)[VEC]) {
+    if (r.f32) {
+        const float* p = static_cast<const float*>(r.data) + at;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const uint4 w = load_global(reinterpret_cast<const uint4*>(p + i));
+            x[i] = __uint_as_float(w.x);
+            x[i + 1] = __uint_as_float(w.y);
+            x[i + 2] = __uint_as_float(w.z);
+            x[i + 3] = __uint_as_float(w.w);
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(r.data) + at;
+        uint32_t w[VEC / 2];
+        if constexpr (VEC == 8) {
+            const uint4 v = load_global(reinterpret_cast<const uint4*>(p));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const u32x2 v = *(const SZ_GLOBAL u32x2*)p;
+            w[0] = v.x, w[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC / 2; i++) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t (&w)[VEC / 2]) {
+    if constexpr (VEC == 8) {
+        store_global(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+        const u32x2 v = {w[0], w[1]};
+        *(SZ_GLOBAL u32x2*)p = v;
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&x)[VEC]) {
+    uint32_t w[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; i++) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    store_words<VEC>(p, w);
+}
+
+enum { kNoTurn = 0, kHalves = 1, kInterleaved = 2 };
+
+// LANES lanes hold a row, VEC elements each; slices waves share a token.
+template <int LANES, int VEC, int MODE, bool APPEND>
+__global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batch batch,
+                                                   uint32_t slices) {
+    constexpr uint32_t kRows = kWave / LANES;  // rows a wave holds at once
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint64_t wave =
+        (uint64_t)blockIdx.x * kWavesPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint64_t token = wave / slices;
+    const uint32_t slice = (uint32_t)(wave % slices);
+    if (token >= a.n_tokens) return;
+
+    // where the token goes in the cache
+    uint64_t k_page = 0, v_page = 0, slot = 0;
+    int32_t position = 0;
+    if constexpr (APPEND) {
+        const uint32_t s = find_seq(batch.n_seqs, (int64_t)token,
+                                    [&](uint32_t i) { return (int64_t)batch.starts[i]; });
+        const Seq q = load_seq(batch, s, (int64_t)(cache.pages_per_seq << cache.page_log2));
+        if (!q.good || (int64_t)token < q.begin || (int64_t)token >= q.end) return;
+        const int64_t c = (int64_t)q.len - q.end + (int64_t)token;
+        if (c < 0) return;
+        const uint64_t entry = (uint64_t)s * cache.table_pitch + ((uint64_t)c >> cache.page_log2);
+        k_page = cache.k_pages[entry];
+        v_page = cache.v_pages[entry];
+        slot = ((uint64_t)c & ((1u << cache.page_log2) - 1)) * cache.token_stride;
+        position = (int32_t)c;
+    }
+    if (MODE != kNoTurn && a.positions != nullptr) position = a.positions[token];
+
+    const uint32_t l = lane % LANES;
+    const uint32_t e = l * VEC;  // this lane's first element
+    const bool live = e < a.head_dim;
+    // the lane's angles
+    constexpr int kAngles = MODE == kInterleaved ? VEC / 2 : VEC;
+    float c[kAngles], sn[kAngles];
+    const uint32_t half = a.turn.dims / 2;
+    const bool turns = MODE != kNoTurn && e < a.turn.dims;
+    const bool lower = e < half;
+    uint32_t partner = lane;
+    if (MODE == kHalves && turns) partner = lower ? lane + half / VEC : lane - half / VEC;
+    if (turns) {
+        const uint32_t first = MODE == kInterleaved ? e / 2 : lower ? e : e - half;
+        const uint32_t far = position < 0 ? 0u - (uint32_t)position : (uint32_t)position;
+#pragma unroll
+        for (int i = 0; i < kAngles; i++) {
+            const uint64_t turn = (uint64_t)far * a.turn.phases[first + i];
+            turn_of((uint32_t)(turn >> 32), c[i], sn[i]);
+            c[i] *= a.turn.magnitude;
+            sn[i] *= position < 0 ? -a.turn.magnitude : a.turn.magnitude;
+            if (MODE == kHalves && lower) sn[i] = -sn[i];
+        }
+    }
+
+    const uint32_t turned = a.q.heads + a.k.heads;
+    for (uint32_t r0 = slice * kRows; r0 < turned; r0 += slices * kRows) {
+        const uint32_t r = r0 + lane / LANES;
+        const bool is_k = r >= a.q.heads;
+        const uint32_t h = is_k ? r - a.q.heads : r;
+        const Rows& src = is_k ? a.k : a.q;
+        const bool on = live && r < turned;
+        float x[VEC] = {};
+        if (on) load_row<VEC>(src, token * src.token_stride + h * src.head_stride + e, x);
+        const float* weight = is_k ? a.k_weight : a.q_weight;
+        float sum = 0;
+#pragma unroll
+        for (int i = 0; i < VEC; i++) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+        for (int d = 1; d < LANES; d *= 2) sum += __shfl_xor(sum, d);
+        if (weight != nullptr && on) {
+            const float inv = 1.0f / sqrtf(sum / (float)a.head_dim + a.eps);
+#pragma unroll
+            for (int i = 0; i < VEC; i++) x[i] = x[i] * inv * weight[e + i];
+        }
+        if constexpr (MODE == kHalves) {
+#pragma unroll
+            for (int i = 0; i < VEC; i++) {
+                const float other = __shfl(x[i], partner);
+                if (turns) x[i] = fmaf(x[i], c[i], other * sn[i]);
+            }
+        } else if constexpr (MODE == kInterleaved) {
+            if (turns) {
+#pragma unroll
+                for (int i = 0; i < VEC / 2; i++) {
+                    const float u = x[2 * i], v = x[2 * i + 1];
+                    x[2 * i] = fmaf(u, c[i], -v * sn[i]);
+                    x[2 * i + 1] = fmaf(v, c[i], u * sn[i]);
+                }
+            }
+        }
+        if (on) {
+            if (APPEND && is_k) {
+                if (good_page(k_page))
+                    store_row<VEC>(reinterpret_cast<uint16_t*>(k_page) + slot +
+                                       h * cache.head_stride + e, x);
+            } else {
+                const Rows& dst = is_k ? a.k_out : a.q_out;
+                store_row<VEC>(static_cast<uint16_t*>(dst.data) + token * dst.token_stride +
+                                   h * dst.head_stride + e, x);
+            }
+        }
+    }
+    if constexpr (APPEND) {
+        for (uint32_t h0 = slice * kRows; h0 < a.v.heads; h0 += slices * kRows) {
+            const uint32_t h = h0 + lane / LANES;
+            if (!live || h >= a.v.heads || !good_page(v_page)) continue;
+            const uint64_t at = token * a.v.token_stride + h * a.v.head_stride + e;
+            uint16_t* to = reinterpret_cast<uint16_t*>(v_page) + slot + h * cache.head_stride + e;
+            if (a.v.f32) {
+                float x[VEC];
+                load_row<VEC>(a.v, at, x);
+                store_row<VEC>(to, x);
+            } else {  // the words as they are
+                const uint16_t* p = static_cast<const uint16_t*>(a.v.data) + at;
+                if constexpr (VEC == 8) {
+                    store_global(reinterpret_cast<uint4*>(to),
+                                 load_global(reinterpret_cast<const uint4*>(p)));
+                } else {
+                    *(SZ_GLOBAL u32x2*)to = *(const SZ_GLOBAL u32x2*)p;
+                }
+            }
+        }
+    }
+}
+
+template <int LANES, int VEC, int MODE, bool APPEND>
+hipError_t go(const TurnRows& a, const Cache& cache, const Batch& batch, hipStream_t stream) {
+    const uint64_t rows = a.q.heads + a.k.heads + (uint64_t)a.v.heads;
+    const uint64_t most = (rows + kWave / LANES - 1) / (kWave / LANES);
+    uint64_t slices = (kFillWaves + a.n_tokens - 1) / a.n_tokens;
+    slices = slices < 1 ? 1 : slices > most ? most : slices;
+    const uint64_t groups = (a.n_tokens * slices + kWavesPerGroup - 1) / kWavesPerGroup;
+    k_turn<LANES, VEC, MODE, APPEND>
+        <<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a, cache, batch, (uint32_t)slices);
+    return hipGetLastError();
+}
+
+// Lanes per row: the least power of two that holds it.  A lane's elements
+// must not straddle the halves: 8 a lane where rotary_dim / 2 is a multiple
+// of 8 (or pairs are interleaved), else 4.
+template <int MODE, bool APPEND>
+hipError_t pick(const TurnRows& a, const Cache& cache, const Batch& batch, hipStream_t stream) {
+    const uint32_t d = a.head_dim;
+    if constexpr (MODE == kHalves) {
+        if (a.turn.dims % 16 != 0) {
+            if (d <= 64) return go<16, 4, MODE, APPEND>(a, cache, batch, stream);
+            if (d <= 128) return go<32, 4, MODE, APPEND>(a, cache, batch, stream);
+            return go<64, 4, MODE, APPEND>(a, cache, batch, stream);
+        }
+    }
+    if (d <= 64) return go<8, 8, MODE, APPEND>(a, cache, batch, stream);
+    if (d <= 128) return go<16, 8, MODE, APPEND>(a, cache, batch, stream);
+    return go<32, 8, MODE, APPEND>(a, cache, batch, stream);
+}
+
+template <bool APPEND>
+hipError_t launch(const TurnRows& a, const Cache& cache, const Batch& batch, hipStream_t stream) {
+    if (a.n_tokens == 0) return hipSuccess;
+    if (a.turn.dims == 0) return pick<kNoTurn, APPEND>(a, cache, batch, stream);
+    if (a.turn.interleaved) return pick<kInterleaved, APPEND>(a, cache, batch, stream);
+    return pick<kHalves, APPEND>(a, cache, batch, stream);
+}
+
+__global__ __launch_bounds__(kWave) void k_check_seqs(SeqCheck c) {
+    const uint32_t s = blockIdx.x, lane = threadIdx.x;
+    const Seq q = load_seq(c.batch, s, c.max_len);
+    bool good = q.good;
+    if (good) {
+        const int64_t first_new = (int64_t)q.len - (q.end - q.begin);
+        int64_t from = 0;
+        if (c.append) {
+            if (first_new < 0) good = false;
+            from = first_new;
+        } else if (c.causal && c.window != 0 && (uint64_t)first_new + 1 > c.window &&
+                   first_new >= 0) {
+            from = first_new + 1 - (int64_t)c.window;
+        }
+        if (good && q.begin < q.end && from < q.len) {
+            const uint64_t row = (uint64_t)s * c.cache.table_pitch;
+            const uint64_t last = (uint64_t)(q.len - 1) >> c.cache.page_log2;
+            for (uint64_t p = ((uint64_t)from >> c.cache.page_log2) + lane; p <= last; p += kWave)
+                good = good && good_page(c.cache.k_pages[row + p]) &&
+                       good_page(c.cache.v_pages[row + p]);
+        }
+    }
+    const bool all = __ballot(!good) == 0;
+    if (lane == 0) c.status[s] = all ? kSeqGood : kBlockInvalid;
+}
+
+}  // namespace
+
+hipError_t launch_turn(const TurnRows& a, hipStream_t stream) {
+    return launch<false>(a, Cache{}, Batch{}, stream);
+}
+
+hipError_t launch_append(const TurnRows& a, const Cache& cache, const Batch& batch,
+                         hipStream_t stream) {
+    if (batch.n_seqs == 0) return hipSuccess;
+    return launch<true>(a, cache, batch, stream);
+}
+
+hipError_t launch_check_seqs(const SeqCheck& c, hipStream_t stream) {
+    if (c.batch.n_seqs == 0) return hipSuccess;
+    k_check_seqs<<<dim3(c.batch.n_seqs), dim3(kWave), 0, stream>>>(c);
+    return hipGetLastError();
+}
+
+}  // namespace sz
