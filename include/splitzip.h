@@ -450,8 +450,8 @@ typedef struct {
     const void *const *d_v_pages;
     uint64_t pages_per_seq; /* entries of a table row that may be used, >= 1 */
     uint64_t table_pitch;   /* entries from a row to the next, >= pages_per_seq */
-    uint64_t token_stride;  /* elements; multiples of 8, < 2^32; rows must not overlap */
-    uint64_t head_stride;
+    uint64_t token_stride;  /* elements; multiples of 8, below 2^26 and 2^32; */
+    uint64_t head_stride;   /* rows must not overlap */
     uint32_t kv_heads;      /* 1 .. 65535 */
     uint32_t head_dim;
     uint32_t page_tokens;   /* a power of two, 16 .. 65536 */
@@ -464,7 +464,7 @@ typedef struct {
  * left as they are.  Both arrays are checked on the device. */
 typedef struct {
     const int32_t *d_starts; /* n_seqs + 1 entries, ascending, 0 .. n_tokens */
-    const int32_t *d_lens;   /* n_seqs entries, 0 .. pages_per_seq * page_tokens */
+    const int32_t *d_lens;   /* n_seqs entries, 0 .. pages_per_seq * page_tokens or 2^30 */
     uint64_t n_seqs;         /* 0 .. 65535 */
     uint64_t n_tokens;       /* rows of the token-major tensors, < 2^31 */
 } sz_batch;
@@ -556,13 +556,16 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  * see has no effect on it, whatever its bits.
  * Scores, the softmax's maximum and sum, and the accumulated output are
  * FP32; the weights are rounded to BF16 before they multiply the values.
- *   q         BF16, batch->n_tokens tokens, heads a multiple of kv_heads
+ *   q         BF16, batch->n_tokens tokens, heads a multiple of kv_heads;
+ *             n_tokens * heads < 2^31, and n_tokens * heads / 16 + n_seqs *
+ *             kv_heads < 2^31
  *   out       BF16 or F32, as many heads
  *   d_lse     optional device float[n_tokens][q heads]: ln of the sum of
  *             exp(score) over the visible keys
  *   max_len   a host-side bound of d_lens (longer sequences are refused),
- *             1 .. pages_per_seq * page_tokens; 0 means that product.  Work
- *             is split for it, so it should not be far above the lengths.
+ *             1 .. pages_per_seq * page_tokens or 2^30, the lesser; 0 means
+ *             that.  Work is split for it, so it should not be far above the
+ *             lengths.
  *   scale     > 0, finite; softcap >= 0, finite (0: none)
  *   d_workspace, workspace_bytes   256-byte aligned, at least
  *             sz_attend_workspace_size(q->heads, cache, batch, max_len); any

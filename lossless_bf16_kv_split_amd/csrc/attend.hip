@@ -4,128 +4,678 @@
 // causal j <= c, window j > c - W):
 //   s_j = scale * q.k_j, or softcap * tanh(scale * q.k_j / softcap)
 //   m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m) v_j / l
-// in one pass over the keys with a running m and l.
+// in one pass over the keys with a running m and l, in powers of two:
+// t = s log2(e), weights 2^(t - m).
+//
+// The query heads of one KV head read the same keys, so a sequence's rows
+// for a KV head are (token, head of the group) pairs, row r = token * G + g,
+// cut into tiles.  Both products run on the matrix cores in the form
+//   S^T = K Q^T,  O^T = V^T P^T
+// whose results hold one query per lane: the softmax's statistics are
+// lane-local but for one exchange, and since the order of a contraction's
+// terms is free, the weights go from the first product's result registers
+// into the second's operand without any exchange at all.
 #include "kv_internal.h"
+
+#include <cfloat>
 
 namespace sz {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kWaves = kThreads / kWave;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's running maximum before any key: below every finite score, and
+// finite itself, so that differences with it are never infinity - infinity.
+constexpr float kNoKey = -FLT_MAX;
+// The maximum follows the scores only when one exceeds it by more than
+// this (in powers of two): weights then stay below 2^8, which neither FP32
+// sums nor BF16's relative rounding notice, and most tiles need no exchange
+// between lanes and no rescaling.
+constexpr float kLag = 8.0f;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const f32x2 v = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-__device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ bf16x8 words8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const u32x4 v = {a, b, c, d};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// How a call is cut up.  Tiles: the rows of sequence s for one KV head,
+// tile_rows at a time; the first tile of sequence s has number
+// floor(starts[s] * G / tile_rows) + s, which leaves room for every tile
+// whatever the lengths and needs no sum over the sequences.  Splits: a
+// tile's visible keys, split_len at a time, joined by a second launch where
+// there can be more than one.
+struct AttendPlan {
+    uint32_t group;      // G
+    uint32_t tile_log2;
+    uint32_t tiles;
+    uint32_t splits;     // most splits of a tile
+    uint32_t split_len;
+    uint64_t units() const { return (uint64_t)tiles * splits; }
+};
+
+constexpr uint32_t kStep = 128;          // keys that a workgroup takes at a time
+constexpr uint64_t kFillGroups = 2048;   // workgroups that keep 256 CUs busy and even
+
+AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
+                       uint64_t max_len) {
+    AttendPlan p;
+    p.group = q_heads / c.kv_heads;
+    const uint64_t rows = n_tokens * p.group;
+    p.tile_log2 = rows <= 16 * n_seqs || c.head_dim > 128 ? 4 : 5;
+    p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
+    const uint64_t groups = (uint64_t)p.tiles * c.kv_heads;
+    uint64_t splits = (kFillGroups + groups - 1) / groups;
+    const uint64_t most = (max_len + 2 * kStep - 1) / (2 * kStep);
+    splits = splits < 1 ? 1 : splits > most ? most : splits;
+    // a split starts at a multiple of 32 keys, which a window can put up to
+    // 31 keys before the first visible one
+    const uint64_t len = (max_len + 31 + splits - 1) / splits;
+    p.split_len = (uint32_t)((len + kStep - 1) / kStep * kStep);
+    p.splits = (uint32_t)((max_len + 31 + p.split_len - 1) / p.split_len);
+    return p;
+}
+
+// What a workgroup works on, all uniform.
+struct Tile {
+    uint32_t seq;
+    int32_t begin;      // first token of the sequence
+    int32_t row0, rows; // rows row0 .. row0 + rows - 1 of the sequence
+    int32_t c0;         // position of the sequence's first new token
+    int32_t len;
+    int32_t lo, hi;     // keys visible to any row of the tile: lo .. hi - 1
+    int32_t all_lo, all_hi;  // keys visible to every row
+    int32_t from;       // lo rounded down to a multiple of 32
+    uint32_t splits;    // of this tile, at least 1
+};
+
+__device__ __forceinline__ bool find_tile(const Attend& a, const AttendPlan& p, uint32_t tile,
+                                          Tile& t) {
+    const auto first = [&](uint32_t s) {
+        return (((int64_t)a.batch.starts[s] * p.group) >> p.tile_log2) + s;
+    };
+    t.seq = find_seq(a.batch.n_seqs, tile, first);
+    const Seq q = load_seq(a.batch, t.seq, a.max_len);
+    if (!q.good) return false;
+    const int64_t at = (int64_t)tile - ((((int64_t)q.begin * p.group) >> p.tile_log2) + t.seq);
+    const int64_t row0 = at << p.tile_log2;
+    const int64_t all = (int64_t)(q.end - q.begin) * p.group;
+    if (at < 0 || row0 >= all) return false;
+    t.begin = q.begin;
+    t.len = q.len;
+    t.c0 = q.len - (q.end - q.begin);
+    // (row numbers fit 32 bits: the host keeps n_tokens * q heads below 2^31)
+    t.row0 = (int32_t)row0;
+    const int64_t left = all - row0, most = 1ll << p.tile_log2;
+    t.rows = (int32_t)(left < most ? left : most);
+    t.lo = t.all_lo = 0;
+    t.hi = t.all_hi = q.len;
+    if (a.causal) {
+        const int32_t first_c = t.c0 + t.row0 / (int32_t)p.group;
+        const int32_t last_c = t.c0 + (t.row0 + t.rows - 1) / (int32_t)p.group;
+        t.hi = last_c + 1 < 0 ? 0 : last_c + 1;
+        t.all_hi = first_c + 1 < 0 ? 0 : first_c + 1;
+        if (a.window != 0) {
+            if ((int64_t)first_c + 1 > (int64_t)a.window) t.lo = first_c + 1 - (int32_t)a.window;
+            if ((int64_t)last_c + 1 > (int64_t)a.window) t.all_lo = last_c + 1 - (int32_t)a.window;
+        }
+    }
+    t.from = t.lo & ~31;
+    t.splits = t.hi > t.lo ? (uint32_t)(t.hi - t.from + p.split_len - 1) / p.split_len : 1;
+    return true;
+}
+
+// Keys that a row sees: low .. high - 1.  Rows past the tile's end are given
+// all of the tile's (nothing of them is stored).
+struct Row {
+    int32_t token, head;  // head within the group
+    int32_t low, high;
+    bool on;
+};
+__device__ __forceinline__ Row find_row(const Attend& a, const AttendPlan& p, const Tile& t,
+                                        int32_t r) {
+    Row w;
+    w.on = r < t.rows;
+    const int32_t row = t.row0 + (w.on ? r : 0);
+    const int32_t i = row / (int32_t)p.group;
+    w.token = t.begin + i;
+    w.head = row - i * (int32_t)p.group;
+    w.low = t.lo;
+    w.high = t.hi;
+    if (w.on && a.causal) {
+        const int32_t c = t.c0 + i;
+        w.high = c + 1;
+        if (a.window != 0 && (int64_t)c + 1 > (int64_t)a.window)
+            w.low = c + 1 - (int32_t)a.window;
+    }
+    return w;
+}
+
+// t of a raw score: score * (scale log2 e), or the capped form, whose tanh
+// is 1 - 2 / (1 + e^2x)
+struct Score {
+    float by;    // scale log2 e; capped: 2 scale log2 e / softcap
+    float cap;   // softcap log2 e, 0 for none
+};
+Score score_of(const Attend& a) {
+    Score s;
+    s.cap = a.softcap * kLog2e;
+    s.by = a.softcap > 0 ? 2 * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e;
+    return s;
+}
+__device__ __forceinline__ float capped(const Score& s, float x) {
+    const float e = __builtin_amdgcn_exp2f(x * s.by);
+    return s.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+}
+
+// One BF16 word pair with an infinity or a NaN in it
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+// Such words taken out (0 in their place)
+__device__ __forceinline__ uint32_t plain_pair(uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+// Such words as marks, BF16 numbers: NaN 1, infinity 128, -infinity 16384.
+// A sum of up to 127 marks of each kind is exact in FP32 and says which
+// there were.
+__device__ __forceinline__ uint32_t mark(uint32_t w) {
+    if ((w & 0x7F80u) != 0x7F80u) return 0;
+    if (w & 0x7Fu) return 0x3F80u;
+    return w & 0x8000u ? 0x4680u : 0x4300u;
+}
+__device__ __forceinline__ uint32_t mark_pair(uint32_t w) {
+    return mark(w & 0xFFFFu) | mark(w >> 16) << 16;
+}
+__device__ __forceinline__ float unmark(float marks) {
+    const uint32_t n = (uint32_t)marks;
+    float x = 0;
+    if (n & 0x7Fu) x = NAN;
+    if (n >> 7 & 0x7Fu) x += INFINITY;
+    if (n >> 14) x -= INFINITY;
+    return x;
+}
+
+// The resource of a block of 16 keys' rows in a page: rows from `skip` on
+// (a page that no visible key lies in, or a bad page address: none) up to
+// `rows`.  Offsets past the end read as zeros, so keys past the last visible
+// one, elements past head_dim and unusable pages need no test at the loads.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const Cache& c, uint64_t page,
+                                                             uint32_t slot, uint32_t head,
+                                                             int32_t rows) {
+    const uint64_t at = page + 2 * (slot * c.token_stride + head * c.head_stride);
+    const bool good = good_page(page) && rows > 0;
+    const uint32_t n = rows > 16 ? 15 : (uint32_t)rows - 1;
+    const uint32_t bytes = good ? 2 * (n * (uint32_t)c.token_stride + c.head_dim) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(good ? at : 0), 0, bytes,
+                                             kBufferFlags);
+}
+
+// Partial results of the splits: for unit (tile, KV head, split), tile_rows
+// rows of head_dim sums and of (maximum, sum of weights).
+struct Partial {
+    float* o;
+    float* ml;
+};
+__device__ __forceinline__ Partial partial_of(uint8_t* ws, const Attend& a, const AttendPlan& p,
+                                              uint32_t tile, uint32_t kv, uint32_t split) {
+    const uint64_t units = (uint64_t)p.tiles * a.cache.kv_heads * p.splits;
+    const uint64_t unit = ((uint64_t)tile * a.cache.kv_heads + kv) * p.splits + split;
+    float* f = reinterpret_cast<float*>(ws);
+    return Partial{f + 2 * (units << p.tile_log2) + (unit << p.tile_log2) * a.cache.head_dim,
+                   f + 2 * (unit << p.tile_log2)};
+}
+
+// N finished elements of a row to the output, from element e on
+template <int N>
+__device__ __forceinline__ void store_out(const Rows& out, uint64_t at, const float (&x)[N]) {
+    if (out.f32) {
+        float* p = static_cast<float*>(out.data) + at;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        x[2 * i] = __uint_as_float(v[i] << 16);
-        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        for (int i = 0; i < N; i += 4)
+            store_global(reinterpret_cast<uint4*>(p + i),
+                         make_uint4(__float_as_uint(x[i]), __float_as_uint(x[i + 1]),
+                                    __float_as_uint(x[i + 2]), __float_as_uint(x[i + 3])));
+        return;
+    }
+    uint16_t* p = static_cast<uint16_t*>(out.data) + at;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; i++) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i + 4 <= N / 2; i += 4)
+        store_global(reinterpret_cast<uint4*>(p + 2 * i),
+                     make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
+    if constexpr (N == 4) {
+        const u32x2 v = {w[0], w[1]};
+        *(SZ_GLOBAL u32x2*)p = v;
     }
 }
 
-// One wave per (token, query head).  LANES lanes share a key, 8 elements
-// each, so a wave takes 64 / LANES keys a step, each group with its own
-// running statistics, joined at the end.
-template <int LANES>
-__global__ __launch_bounds__(kWave) void k_attend_rows(Attend a) {
-    const uint32_t lane = threadIdx.x, l = lane % LANES, g = lane / LANES;
-    constexpr uint32_t kGroups = kWave / LANES;
-    const uint64_t token = blockIdx.x / a.q.heads;
-    const uint32_t h = blockIdx.x % a.q.heads;
-    const uint32_t s = find_seq(a.batch.n_seqs, (int64_t)token,
-                                [&](uint32_t i) { return (int64_t)a.batch.starts[i]; });
-    const Seq q = load_seq(a.batch, s, a.max_len);
-    if (!q.good || (int64_t)token < q.begin || (int64_t)token >= q.end) return;
-    const uint32_t kv = h / (a.q.heads / a.cache.kv_heads);
-    const int64_t c = (int64_t)q.len - q.end + (int64_t)token;
-    int64_t from = 0, upto = q.len;
-    if (a.causal) {
-        upto = c + 1 < upto ? c + 1 : upto;
-        if (a.window != 0 && c >= 0 && (uint64_t)c + 1 > a.window) from = c + 1 - (int64_t)a.window;
-    }
-    const bool live = l * 8 < a.cache.head_dim;
-    float x[8] = {};
-    if (live)
-        unpack(load_global(reinterpret_cast<const uint4*>(
-                   static_cast<const uint16_t*>(a.q.data) + token * a.q.token_stride +
-                   h * a.q.head_stride + l * 8)), x);
-    float m = -INFINITY, sum = 0, o[8] = {};
-    const uint64_t row = (uint64_t)s * a.cache.table_pitch;
-    for (int64_t j0 = from; j0 < upto; j0 += kGroups) {
-        const int64_t j = j0 + g;
-        const bool seen = j < upto;
-        float k[8] = {}, v[8] = {};
-        if (seen && live) {
-            const uint64_t entry = row + ((uint64_t)j >> a.cache.page_log2);
-            const uint64_t at = ((uint64_t)j & ((1u << a.cache.page_log2) - 1)) *
-                                    a.cache.token_stride + kv * a.cache.head_stride + l * 8;
-            const uint64_t kp = a.cache.k_pages[entry], vp = a.cache.v_pages[entry];
-            if (good_page(kp))
-                unpack(load_global(reinterpret_cast<const uint4*>(
-                           reinterpret_cast<const uint16_t*>(kp) + at)), k);
-            if (good_page(vp))
-                unpack(load_global(reinterpret_cast<const uint4*>(
-                           reinterpret_cast<const uint16_t*>(vp) + at)), v);
-        }
-        float dot = 0;
+// 1 / l; 0 where no key was seen
+__device__ __forceinline__ float inverse(float l) { return l == 0 ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---- few rows: a decode step, drafted tokens ------------------------------
+//
+// One workgroup takes a tile of 16 (or 32) rows and a split of its keys;
+// each wave streams every fourth block of 32 keys straight from the pages
+// into registers, with the next block's loads in flight, and the waves'
+// results are joined in LDS at the end.  Bound by the bytes of the cache.
+//
+// Matrix operands of 16x16x32: lane (n = lane % 16, h = lane / 16) holds
+// eight of 32 contraction terms of row n.
+//  - K: row n of a block of 16 keys, elements 32 s + 8 h .. + 7: one 16-byte
+//    load a slice, a key's four lanes together 64 contiguous bytes.
+//  - S^T's result: lane (query n, h) has the scores of keys 4 h + i of each
+//    block.  These eight are what the lane feeds the second product as its
+//    contraction terms,
+//  - so V's operand needs, in lane (n, h), eight keys 4 h + i of both blocks
+//    for one element.  A lane loads those eight keys' rows at elements
+//    8 n .. 8 n + 7 (16 lanes read a whole contiguous row) and transposes
+//    8 x 8 words in registers (32 byte permutes); product i takes the
+//    elements 8 n + i as its rows.
+//  - O^T's result: lane (query n, h) then has, for r < 4, elements
+//    32 h + 8 r + i: 32 consecutive ones.
+template <int DP, int RB>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Attend a, AttendPlan p,
+                                                                         Score score,
+                                                                         uint8_t* ws) {
+    constexpr int kSlices = DP / 32;       // of K, 32 elements each
+    constexpr int kVec = DP < 128 ? 4 : 8; // elements of a V row per load
+    constexpr int kVLoads = DP / (16 * kVec);
+    constexpr int kProducts = DP / 16;     // of 16 elements of the output
+    const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
+    const uint32_t rest = blockIdx.x / a.cache.kv_heads;
+    const uint32_t split = rest % p.splits, tile = rest / p.splits;
+    Tile t;
+    if (!find_tile(a, p, tile, t) || split >= t.splits) return;
+    const int32_t first = t.from + (int32_t)(split * p.split_len);
+    const int32_t last = t.splits == 1 || split == t.splits - 1 ? t.hi
+                                                                : first + (int32_t)p.split_len;
+
+    // the rows, their queries (slices of 32 elements, zeros past head_dim)
+    const uint32_t dim = a.cache.head_dim;
+    bf16x8 q[RB][kSlices];
+    int32_t low[RB], high[RB];
 #pragma unroll
-        for (int i = 0; i < 8; i++) dot = fmaf(x[i], k[i], dot);
+    for (int b = 0; b < RB; b++) {
+        const Row w = find_row(a, p, t, 16 * b + (int32_t)n);
+        low[b] = w.low;
+        high[b] = w.high;
+        const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
+                              (uint64_t)w.token * a.q.token_stride +
+                              (uint64_t)(kv * p.group + w.head) * a.q.head_stride;
 #pragma unroll
-        for (int d = 1; d < LANES; d *= 2) dot += __shfl_xor(dot, d);
-        float z = dot * a.scale;
-        if (a.softcap > 0) z = a.softcap * tanhf(z / a.softcap);
-        if (!seen) continue;
-        const float top = fmaxf(m, z);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - top);
-        const float p = top == -INFINITY ? 0.0f : expf(z - top);
-        sum = sum * keep + p;
-#pragma unroll
-        for (int i = 0; i < 8; i++) o[i] = fmaf(p, v[i], o[i] * keep);
-        m = top;
-    }
-#pragma unroll
-    for (int d = LANES; d < (int)kWave; d *= 2) {
-        const float other = __shfl_xor(m, d), top = fmaxf(m, other);
-        const float mine = m == -INFINITY ? 0.0f : expf(m - top);
-        const float theirs = other == -INFINITY ? 0.0f : expf(other - top);
-        sum = sum * mine + __shfl_xor(sum, d) * theirs;
-#pragma unroll
-        for (int i = 0; i < 8; i++) o[i] = o[i] * mine + __shfl_xor(o[i], d) * theirs;
-        m = top;
-    }
-    const float inv = sum > 0 ? 1.0f / sum : sum == 0 ? 0.0f : sum;
-    if (g == 0 && live) {
-        const uint64_t at = token * a.out.token_stride + h * a.out.head_stride + l * 8;
-        if (a.out.f32) {
-            float* p = static_cast<float*>(a.out.data) + at;
-#pragma unroll
-            for (int i = 0; i < 8; i++) p[i] = o[i] * inv;
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-            store_global(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out.data) + at),
-                         make_uint4(w[0], w[1], w[2], w[3]));
+        for (int s = 0; s < kSlices; s++) {
+            u32x4 v = {0, 0, 0, 0};
+            if (w.on && 32 * s + 8 * h < dim)
+                v = *(const SZ_GLOBAL u32x4*)(row + 32 * s + 8 * h);
+            q[b][s] = __builtin_bit_cast(bf16x8, v);
         }
     }
+
+    // byte offsets of the lane's loads within a block of 16 keys
+    constexpr uint32_t kPast = 0x80000000u;
+    const uint32_t step = 2 * (uint32_t)a.cache.token_stride;
+    uint32_t k_off[kSlices], v_off[4][kVLoads];
+#pragma unroll
+    for (int s = 0; s < kSlices; s++)
+        k_off[s] = 32 * s + 8 * h < dim ? n * step + 64 * s + 16 * h : kPast;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int u = 0; u < kVLoads; u++)
+            v_off[i][u] = kVec * n + 128 * u < dim ? (4 * h + i) * step + 2 * (kVec * n + 128 * u)
+                                                   : kPast;
+
+    struct Block {
+        u32x4 k[2][kSlices];
+        u32x4 v[8][kVLoads];
+    };
+    const uint64_t table_row = (uint64_t)t.seq * a.cache.table_pitch;
+    const auto load = [&](Block& x, int32_t j) {
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            const int32_t jb = j + 16 * b;
+            uint64_t k_page = 0, v_page = 0;
+            if (jb < last && jb + 16 > t.lo) {
+                const uint64_t entry = table_row + ((uint32_t)jb >> a.cache.page_log2);
+                k_page = a.cache.k_pages[entry];
+                v_page = a.cache.v_pages[entry];
+            }
+            const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
+            const auto kr = block_rows(a.cache, k_page, slot, kv, last - jb);
+            const auto vr = block_rows(a.cache, v_page, slot, kv, last - jb);
+#pragma unroll
+            for (int s = 0; s < kSlices; s++)
+                x.k[b][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, k_off[s], 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int u = 0; u < kVLoads; u++) {
+                    if constexpr (kVec == 8) {
+                        x.v[4 * b + i][u] =
+                            __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[i][u], 0, 0);
+                    } else {
+                        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[i][u], 0, 0);
+                        x.v[4 * b + i][u] = u32x4{w.x, w.y, 0, 0};
+                    }
+                }
+        }
+    };
+
+    float m[RB], l[RB];
+    f32x4 o[RB][kProducts];
+#pragma unroll
+    for (int b = 0; b < RB; b++) {
+        m[b] = kNoKey;
+        l[b] = 0;
+#pragma unroll
+        for (int d = 0; d < kProducts; d++) o[b][d] = f32x4{0, 0, 0, 0};
+    }
+
+    // operand i of the transposed values
+    const auto values = [&](const Block& x, int d) {
+        const int u = d / kVec, i = d % kVec;
+        const uint32_t pick = i & 1 ? 0x07060302u : 0x05040100u;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            w[k] = __builtin_amdgcn_perm(x.v[2 * k + 1][u][i / 2], x.v[2 * k][u][i / 2], pick);
+        return words8(w[0], w[1], w[2], w[3]);
+    };
+
+    const auto compute = [&](Block& x, int32_t j) {
+        // keys that some row does not see
+        const bool edge = j < t.all_lo || j + 32 > t.all_hi;
+        bool odd = false;
+        if (edge) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int32_t key = j + 16 * (k / 4) + 4 * (int32_t)h + k % 4;
+#pragma unroll
+                for (int u = 0; u < kVLoads; u++)
+#pragma unroll
+                    for (int i = 0; i < kVec / 2; i++) {
+                        if (key < t.lo) x.v[k][u][i] = 0;
+                        odd = odd || odd_pair(x.v[k][u][i]);
+                    }
+            }
+            odd = __ballot(odd) != 0;
+        }
+        uint32_t weights[RB][4], seen[RB][4];
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            float s[8];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                f32x4 z = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < kSlices; c++)
+                    z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, x.k[k][c]), q[b][c], z, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[4 * k + i] = z[i];
+            }
+            if (score.cap > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) s[i] = capped(score, s[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) s[i] *= score.by;
+            }
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int32_t key = j + 16 * (i / 4) + 4 * (int32_t)h + i % 4;
+                    if (key < low[b] || key >= high[b]) s[i] = -INFINITY;
+                }
+            }
+            float top = s[0];
+#pragma unroll
+            for (int i = 1; i < 8; i++) top = fmaxf(top, s[i]);
+            if (__ballot(top > m[b] + kLag) != 0) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                top = fmaxf(top, m[b]);
+                const float keep = __builtin_amdgcn_exp2f(m[b] - top);
+                m[b] = top;
+                l[b] *= keep;
+#pragma unroll
+                for (int d = 0; d < kProducts; d++) o[b][d] *= keep;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                s[i] = __builtin_amdgcn_exp2f(s[i] - m[b]);
+                l[b] += s[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) weights[b][i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int32_t key = j + 16 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
+                    seen[b][i] = (key >= low[b] && key < high[b] ? 0x3F80u : 0u) |
+                                 (key + 1 >= low[b] && key + 1 < high[b] ? 0x3F800000u : 0u);
+                }
+            }
+        }
+        if (odd) {
+            // an infinity or a NaN must reach the rows that see it and no
+            // other: 0 times it would be NaN.  The values go in without it,
+            // and a product of marks with what each row sees brings it in.
+            Block y;
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+#pragma unroll
+                for (int u = 0; u < kVLoads; u++)
+#pragma unroll
+                    for (int i = 0; i < kVec / 2; i++) {
+                        y.v[k][u][i] = mark_pair(x.v[k][u][i]);
+                        x.v[k][u][i] = plain_pair(x.v[k][u][i]);
+                    }
+#pragma unroll
+            for (int d = 0; d < kProducts; d++)
+#pragma unroll
+                for (int b = 0; b < RB; b++) {
+                    f32x4 z = {0, 0, 0, 0};
+                    z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        values(y, d), words8(seen[b][0], seen[b][1], seen[b][2], seen[b][3]), z, 0,
+                        0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) o[b][d][i] += unmark(z[i]);
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < kProducts; d++) {
+            const bf16x8 v = values(x, d);
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+                o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    v, words8(weights[b][0], weights[b][1], weights[b][2], weights[b][3]), o[b][d],
+                    0, 0, 0);
+        }
+    };
+
+    int32_t j = first + 32 * (int32_t)wave;
+    Block even, odd;
+    load(even, j);
+    for (; j < last; j += 2 * kStep) {
+        load(odd, j + kStep);
+        compute(even, j);
+        load(even, j + 2 * kStep);
+        if (j + (int32_t)kStep < last) compute(odd, j + kStep);
+    }
+
+    // join the waves: row by row in LDS
+    constexpr int kPitch = DP + 4;
+    __shared__ float join_o[kWaves][16][kPitch];
+    __shared__ float join_m[kWaves][16], join_l[kWaves][16];
+    constexpr int kRun = 4 * kVec;  // consecutive elements of a lane's result, per 16 kVec
+#pragma unroll
+    for (int b = 0; b < RB; b++) {
+        float sum = l[b];
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (b > 0) __syncthreads();
+        if (h == 0) {
+            join_m[wave][n] = m[b];
+            join_l[wave][n] = sum;
+        }
+#pragma unroll
+        for (int u = 0; u < kVLoads; u++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int i = 0; i < kVec; i++)
+                    join_o[wave][n][16 * kVec * u + kRun * h + kVec * r + i] =
+                        o[b][kVec * u + i][r];
+        __syncthreads();
+        constexpr int kPer = DP / 16;  // elements of a thread
+        const uint32_t r = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
+        const Row w = find_row(a, p, t, 16 * b + (int32_t)r);
+        if (w.on) {
+            float top = join_m[0][r];
+#pragma unroll
+            for (int i = 1; i < (int)kWaves; i++) top = fmaxf(top, join_m[i][r]);
+            float total = 0, x[kPer] = {};
+#pragma unroll
+            for (int i = 0; i < (int)kWaves; i++) {
+                const float keep = __builtin_amdgcn_exp2f(join_m[i][r] - top);
+                total += join_l[i][r] * keep;
+#pragma unroll
+                for (int k = 0; k < kPer; k++) x[k] = fmaf(join_o[i][r][e + k], keep, x[k]);
+            }
+            const uint32_t head = kv * p.group + w.head;
+            if (t.splits == 1) {
+                const float inv = inverse(total);
+#pragma unroll
+                for (int k = 0; k < kPer; k++) x[k] *= inv;
+                const uint64_t at = (uint64_t)w.token * a.out.token_stride +
+                                    (uint64_t)head * a.out.head_stride + e;
+                constexpr int kPiece = kPer < 8 ? kPer : 8;
+#pragma unroll
+                for (int k = 0; k < kPer; k += kPiece) {
+                    float y[kPiece];
+#pragma unroll
+                    for (int i = 0; i < kPiece; i++) y[i] = x[k + i];
+                    if (e + k < dim) store_out<kPiece>(a.out, at + k, y);
+                }
+                if (e == 0 && a.lse != nullptr)
+                    a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
+            } else {
+                const Partial u = partial_of(ws, a, p, tile, kv, split);
+#pragma unroll
+                for (int k = 0; k < kPer; k += 4)
+                    if (e + k < dim)
+                        store_global(reinterpret_cast<uint4*>(
+                                         u.o + (uint64_t)(16 * b + r) * dim + e + k),
+                                     make_uint4(__float_as_uint(x[k]), __float_as_uint(x[k + 1]),
+                                                __float_as_uint(x[k + 2]),
+                                                __float_as_uint(x[k + 3])));
+                if (e == 0) {
+                    u.ml[2 * (16 * b + r)] = top;
+                    u.ml[2 * (16 * b + r) + 1] = total;
+                }
+            }
+        }
+    }
+}
+
+// Joins a tile's splits: one wave per row, four elements a lane.
+__global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t pieces = (1u << p.tile_log2) / kWaves;
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
+    const uint32_t rest = blockIdx.x / a.cache.kv_heads;
+    const int32_t r = (int32_t)(rest % pieces * kWaves + wave);
+    const uint32_t tile = rest / pieces;
+    Tile t;
+    if (!find_tile(a, p, tile, t) || t.splits == 1 || r >= t.rows) return;
+    const Row w = find_row(a, p, t, r);
+    float top = kNoKey;
+    for (uint32_t s = 0; s < t.splits; s++)
+        top = fmaxf(top, partial_of(ws, a, p, tile, kv, s).ml[2 * r]);
+    float total = 0, x[4] = {};
+    const uint32_t e = 4 * lane, dim = a.cache.head_dim;
+    for (uint32_t s = 0; s < t.splits; s++) {
+        const Partial u = partial_of(ws, a, p, tile, kv, s);
+        const float keep = __builtin_amdgcn_exp2f(u.ml[2 * r] - top);
+        total += u.ml[2 * r + 1] * keep;
+        if (e < dim) {
+            const uint4 v = load_global(reinterpret_cast<const uint4*>(u.o + (uint64_t)r * dim + e));
+            x[0] = fmaf(__uint_as_float(v.x), keep, x[0]);
+            x[1] = fmaf(__uint_as_float(v.y), keep, x[1]);
+            x[2] = fmaf(__uint_as_float(v.z), keep, x[2]);
+            x[3] = fmaf(__uint_as_float(v.w), keep, x[3]);
+        }
+    }
+    const float inv = inverse(total);
+#pragma unroll
+    for (int i = 0; i < 4; i++) x[i] *= inv;
+    const uint32_t head = kv * p.group + w.head;
+    if (e < dim)
+        store_out<4>(a.out, (uint64_t)w.token * a.out.token_stride +
+                                (uint64_t)head * a.out.head_stride + e, x);
     if (lane == 0 && a.lse != nullptr)
-        a.lse[token * a.q.heads + h] = sum == 0 ? -INFINITY : m + logf(sum);
+        a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
+}
+
+template <int DP>
+hipError_t go_few(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
+    const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads)), block(kThreads);
+    const Score score = score_of(a);
+    if constexpr (DP <= 128) {
+        if (p.tile_log2 == 5) {
+            k_attend_few<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
+            return hipGetLastError();
+        }
+    }
+    k_attend_few<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-uint64_t attend_workspace(uint32_t, const Cache&, uint64_t, uint64_t, uint64_t) { return 0; }
+uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
+                          uint64_t max_len) {
+    const AttendPlan p = plan_attend(q_heads, c, n_seqs, n_tokens, max_len);
+    if (p.splits == 1) return 0;
+    return ((p.units() * c.kv_heads << p.tile_log2) * (c.head_dim + 2) * 4 + 255) / 256 * 256;
+}
 
-hipError_t launch_attend(const Attend& a, uint8_t*, hipStream_t stream) {
+hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
     if (a.batch.n_seqs == 0 || a.batch.n_tokens == 0) return hipSuccess;
-    const dim3 grid((uint32_t)(a.batch.n_tokens * a.q.heads)), block(kWave);
-    if (a.cache.head_dim <= 64) k_attend_rows<8><<<grid, block, 0, stream>>>(a);
-    else if (a.cache.head_dim <= 128) k_attend_rows<16><<<grid, block, 0, stream>>>(a);
-    else k_attend_rows<32><<<grid, block, 0, stream>>>(a);
+    const AttendPlan p =
+        plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
+    const uint32_t dim = a.cache.head_dim;
+    hipError_t e = dim <= 64    ? go_few<64>(a, p, ws, stream)
+                   : dim <= 128 ? go_few<128>(a, p, ws, stream)
+                                : go_few<256>(a, p, ws, stream);
+    if (e != hipSuccess || p.splits == 1) return e;
+    const uint32_t pieces = (1u << p.tile_log2) / kWaves;
+    k_attend_join<<<dim3(p.tiles * a.cache.kv_heads * pieces), dim3(kThreads), 0, stream>>>(a, p,
+                                                                                            ws);
     return hipGetLastError();
 }
 

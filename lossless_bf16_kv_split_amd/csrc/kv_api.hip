@@ -12,6 +12,9 @@ constexpr uint64_t kMaxHeads = 65535;
 constexpr uint64_t kMaxStride = uint64_t{1} << 32;
 constexpr uint64_t kMaxTokens = (uint64_t{1} << 31) - 1;
 constexpr uint64_t kMaxSeqs = 65535;
+// A block of 16 cached tokens is addressed by 31-bit byte offsets.
+constexpr uint64_t kMaxPageStride = uint64_t{1} << 26;
+constexpr uint64_t kMaxLen = uint64_t{1} << 30;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -107,7 +110,7 @@ bool cache_ok(const sz_kv_cache* c) {
     if (c->pages_per_seq == 0 || c->pages_per_seq > kMaxTokens ||
         c->table_pitch < c->pages_per_seq || c->table_pitch > (uint64_t{1} << 40))
         return false;
-    return strides_ok(c->token_stride, c->head_stride) &&
+    return strides_ok(c->token_stride, c->head_stride) && c->token_stride < kMaxPageStride &&
            rows_apart(c->page_tokens, c->kv_heads, c->token_stride, c->head_stride, c->head_dim);
 }
 
@@ -151,7 +154,12 @@ bool turned_ok(const sz_heads* src, const sz_heads* dst, const float* weight, ui
 
 uint64_t most_len(const sz_kv_cache& c) {
     const uint64_t n = c.pages_per_seq * c.page_tokens;
-    return n > kMaxTokens ? kMaxTokens : n;
+    return n > kMaxLen ? kMaxLen : n;
+}
+
+// Attention counts a call's rows, and its tiles for every KV head, in 31 bits
+bool attend_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t q_heads, uint64_t kv_heads) {
+    return n_tokens * q_heads <= kMaxTokens && n_tokens * q_heads / 16 + n_seqs * kv_heads <= kMaxTokens;
 }
 
 }  // namespace
@@ -286,7 +294,8 @@ uint64_t sz_attend_workspace_size(uint64_t q_heads, const sz_kv_cache* cache,
         cache->pages_per_seq > kMaxTokens || cache->page_tokens > 65536)
         return 0;
     const uint64_t most = most_len(*cache);
-    if (max_len > most) return 0;
+    if (max_len > most || !attend_fits(batch->n_seqs, batch->n_tokens, q_heads, cache->kv_heads))
+        return 0;
     if (batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
     return sz::attend_workspace((uint32_t)q_heads, cache_of(*cache), batch->n_seqs,
                                 batch->n_tokens, max_len == 0 ? most : max_len);
@@ -302,6 +311,7 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
     const uint32_t dim = cache->head_dim;
     if (!heads_ok(q, n, dim, false) || !heads_ok(out, n, dim, true) || q->type != SZ_TYPE_BF16 ||
         q->heads != out->heads || q->heads % cache->kv_heads != 0 ||
+        !attend_fits(batch->n_seqs, n, q->heads, cache->kv_heads) ||
         !apart(*q, *out, n, dim, false))
         return SZ_ERR_INVALID_ARGUMENT;
     if (!(scale > 0) || !std::isfinite(scale) || !(softcap >= 0) || !std::isfinite(softcap) ||

@@ -98,7 +98,10 @@ def test_attend_refuses(sz):
         dict(c=cache(dim=264, head_stride=264, token_stride=264 * 8)),
         dict(c=cache(dim=4)), dict(c=cache(dim=0)), dict(c=cache(kv_heads=0)),
         dict(c=cache(head_stride=64)), dict(c=cache(token_stride=1016)),
-        dict(c=cache(token_stride=1 << 33)),
+        dict(c=cache(token_stride=1 << 33)), dict(c=cache(token_stride=1 << 26)),
+        dict(b=batch(tokens=(1 << 26) + 1), q=heads(n=32), out=heads(A + (1 << 45), n=32)),
+        dict(b=batch(seqs=65535), c=cache(kv_heads=65528, token_stride=65528 * 128),
+             q=heads(n=65528), out=heads(A + (1 << 45), n=65528)),
         dict(c=cache(pages=0)), dict(c=cache(pitch=63)),
         dict(c=cache(k=None)), dict(c=cache(v=A + 4)),
         dict(b=batch(seqs=65536)), dict(b=batch(tokens=1 << 31)),
