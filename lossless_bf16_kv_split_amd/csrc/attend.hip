@@ -64,20 +64,26 @@ struct AttendPlan {
     uint32_t splits;     // most splits of a tile
     uint32_t split_len;
     uint64_t units() const { return (uint64_t)tiles * splits; }
+    bool few() const { return tile_log2 <= 5; }
 };
 
-constexpr uint32_t kStep = 128;          // keys that a workgroup takes at a time
-constexpr uint64_t kFillGroups = 2048;   // workgroups that keep 256 CUs busy and even
+constexpr uint32_t kStep = 128;  // split lengths are multiples of this many keys
+// Workgroups that keep 256 CUs busy and even: of the few-row kernel, and of
+// the chunk kernel.
+constexpr uint64_t kFillFew = 2048, kFillChunk = 512;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                        uint64_t max_len) {
     AttendPlan p;
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
-    p.tile_log2 = rows <= 16 * n_seqs || c.head_dim > 128 ? 4 : 5;
+    if (rows <= 16 * n_seqs) p.tile_log2 = 4;
+    else if (rows <= 32 * n_seqs && c.head_dim <= 128) p.tile_log2 = 5;
+    else p.tile_log2 = rows > 128 * n_seqs && c.head_dim <= 128 ? 8 : 7;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     const uint64_t groups = (uint64_t)p.tiles * c.kv_heads;
-    uint64_t splits = (kFillGroups + groups - 1) / groups;
+    const uint64_t fill = p.few() ? kFillFew : kFillChunk;
+    uint64_t splits = (fill + groups - 1) / groups;
     const uint64_t most = (max_len + 2 * kStep - 1) / (2 * kStep);
     splits = splits < 1 ? 1 : splits > most ? most : splits;
     // a split starts at a multiple of 32 keys, which a window can put up to
@@ -601,6 +607,368 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
     }
 }
 
+// ---- chunks: a part of a prompt, or all of it -----------------------------
+//
+// One workgroup of four waves takes a tile of 128 or 256 rows, each wave 32
+// or 64 of them, and walks the tile's keys 64 at a time.  The keys and values
+// of a step go from the pages straight to LDS (each wave fetches a block of
+// 16 keys) while the step before is worked on: two buffers, one barrier a
+// step.  Bound by the matrix cores and by the softmax's arithmetic beside
+// them.
+//
+// Matrix operands of 32x32x16: lane (n = lane % 32, h = lane / 32) holds eight
+// of 16 contraction terms of row n.
+//  - K: key 32 b + n, elements 16 s + 8 h .. + 7: 16 bytes of LDS.
+//  - S^T's result i: query n, key 32 b + 8 (i / 4) + 4 h + i % 4.
+//  - V: keys 16 t + 4 h + .. and 16 t + 8 + 4 h + .. (four each) for element
+//    32 d + n: LDS reads that transpose four rows of 16 words.
+//  - O^T's result i: query n, element 32 d + 8 (i / 4) + 4 h + i % 4.
+//
+// LDS holds rows of DP words in 16-byte pieces, permuted so that both kinds
+// of reads spread over the banks: piece c of key j lies at c ^ k_mix(j) (16
+// keys' same piece: 16 places) and c ^ v_mix(j) (four keys' 64 consecutive
+// bytes: four places).
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define SZ_LDS __attribute__((address_space(3)))
+
+template <int DP>
+__device__ __forceinline__ constexpr uint32_t k_mix(uint32_t j) {
+    return DP == 64 ? j >> 1 & 7 : j & 15;
+}
+template <int DP>
+__device__ __forceinline__ constexpr uint32_t v_mix(uint32_t j) {
+    return DP == 64 ? (j >> 1 & 1) << 2 : (j & 3) << 2;
+}
+
+// 64 lanes' 16 bytes each, from offsets of a buffer to consecutive LDS bytes;
+// offsets past the buffer's end store zeros.  Completion is counted by vmcnt.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset,
+                                            uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(from)
+                 : "memory");
+}
+
+template <int DP, int QB>
+__global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
+    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+    constexpr int kKeys = 64;
+    constexpr uint32_t kRow = 2 * DP;             // bytes of a row in LDS
+    constexpr uint32_t kBuffer = kKeys * kRow;    // K or V of a step
+    constexpr int kLoads = DP / 32;               // per wave, of K or V
+    constexpr int kSlices = DP / 16, kParts = DP / 32;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBuffer];  // K, K, V, V
+
+    const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
+    const uint32_t rest = blockIdx.x / a.cache.kv_heads;
+    // the last tiles of a prompt see the most keys: they go first
+    const uint32_t split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits;
+    Tile t;
+    if (!find_tile(a, p, tile, t) || split >= t.splits) return;
+    const int32_t first = t.from + (int32_t)(split * p.split_len);
+    const int32_t last = split == t.splits - 1 ? t.hi : first + (int32_t)p.split_len;
+
+    const uint32_t dim = a.cache.head_dim;
+    bf16x8 q[QB][kSlices];
+    int32_t low[QB], high[QB];
+#pragma unroll
+    for (int b = 0; b < QB; b++) {
+        const Row w = find_row(a, p, t, (int32_t)(32 * QB * wave + 32 * b + n));
+        low[b] = w.low;
+        high[b] = w.high;
+        const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
+                              (uint64_t)w.token * a.q.token_stride +
+                              (uint64_t)(kv * p.group + w.head) * a.q.head_stride;
+#pragma unroll
+        for (int s = 0; s < kSlices; s++) {
+            u32x4 v = {0, 0, 0, 0};
+            if (w.on && 16 * s + 8 * h < dim)
+                v = *(const SZ_GLOBAL u32x4*)(row + 16 * s + 8 * h);
+            q[b][s] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+    // keys visible to some and to every row of this wave
+    int32_t w_lo = t.lo, w_hi = t.hi, w_all_lo = t.all_lo, w_all_hi = t.all_hi;
+    {
+        const int32_t r0 = 32 * QB * (int32_t)wave;
+        const Row x = find_row(a, p, t, r0), y = find_row(a, p, t, r0 + 32 * QB - 1);
+        if (r0 >= t.rows) {
+            w_hi = w_lo;  // no rows: nothing to do
+        } else {
+            w_lo = x.low;
+            w_all_hi = x.high;
+            if (y.on) {
+                w_hi = y.high;
+                w_all_lo = y.low;
+            }
+        }
+    }
+
+    // this wave's part of a step: 16 keys, kLoads KB of K and of V
+    constexpr uint32_t kPast = 0x80000000u;
+    const uint32_t step = 2 * (uint32_t)a.cache.token_stride;
+    uint32_t k_off[kLoads], v_off[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+        const uint32_t at = 1024 * i + 16 * lane, row = at / kRow, piece = at % kRow / 16;
+        const uint32_t kp = piece ^ k_mix<DP>(row), vp = piece ^ v_mix<DP>(row);
+        k_off[i] = 8 * kp < dim ? row * step + 16 * kp : kPast;
+        v_off[i] = 8 * vp < dim ? row * step + 16 * vp : kPast;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(SZ_LDS uint8_t*)lds;
+    const uint64_t table_row = (uint64_t)t.seq * a.cache.table_pitch;
+    const auto fetch = [&](int32_t j, uint32_t buffer) {
+        const int32_t jb = j + 16 * (int32_t)wave;
+        uint64_t k_page = 0, v_page = 0;
+        if (jb < last && jb + 16 > t.lo) {
+            const uint64_t entry = table_row + ((uint32_t)jb >> a.cache.page_log2);
+            k_page = a.cache.k_pages[entry];
+            v_page = a.cache.v_pages[entry];
+        }
+        const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
+        const auto kr = block_rows(a.cache, k_page, slot, kv, last - jb);
+        const auto vr = block_rows(a.cache, v_page, slot, kv, last - jb);
+        const uint32_t to = lds0 + buffer * kBuffer + wave * 16 * kRow;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) load_to_lds(kr, k_off[i], to + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < kLoads; i++)
+            load_to_lds(vr, v_off[i], to + 2 * kBuffer + 1024 * i);
+    };
+
+    // LDS addresses of this lane's reads, before the buffer's
+    uint32_t k_at[kSlices], v_at[kParts];
+#pragma unroll
+    for (int s = 0; s < kSlices; s++) k_at[s] = n * kRow + ((2 * s + h) ^ k_mix<DP>(n)) * 16;
+    {
+        const uint32_t key = lane % 16 / 4, piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
+#pragma unroll
+        for (int d = 0; d < kParts; d++)
+            v_at[d] = (4 * h + key) * kRow + ((4 * d + piece) ^ v_mix<DP>(key)) * 16 + lane % 2 * 8;
+    }
+    const auto keys_at = [&](uint32_t buffer, int b, int s) {
+        return *(const SZ_LDS bf16x8*)(uintptr_t)(lds0 + buffer * kBuffer + 32 * b * kRow + k_at[s]);
+    };
+    const auto value_words = [&](uint32_t buffer, int t16, int d) {
+        const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * t16 * kRow + v_at[d];
+        const u32x2 x = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SZ_LDS s16x4*)(uintptr_t)at));
+        const u32x2 y = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                       (SZ_LDS s16x4*)(uintptr_t)(at + 8 * kRow)));
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+
+    float m[QB], l[QB];
+    f32x16 o[QB][kParts];
+#pragma unroll
+    for (int b = 0; b < QB; b++) {
+        m[b] = kNoKey;
+        l[b] = 0;
+#pragma unroll
+        for (int d = 0; d < kParts; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[b][d][i] = 0;
+    }
+
+    const auto compute = [&](int32_t j, uint32_t buffer) {
+        const bool edge = j < w_all_lo || j + kKeys > w_all_hi;
+        uint32_t weights[QB][2][8];
+        f32x16 s[QB][2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+#pragma unroll
+            for (int b = 0; b < QB; b++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[b][k][i] = 0;
+#pragma unroll
+            for (int c = 0; c < kSlices; c++) {
+                const bf16x8 x = keys_at(buffer, k, c);
+#pragma unroll
+                for (int b = 0; b < QB; b++)
+                    s[b][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[b][c], s[b][k], 0, 0, 0);
+            }
+        }
+        float by = score.by;
+        if (score.cap > 0) {
+            by = 1.0f;
+#pragma unroll
+            for (int b = 0; b < QB; b++)
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) s[b][k][i] = capped(score, s[b][k][i]);
+        }
+        if (edge) {
+#pragma unroll
+            for (int b = 0; b < QB; b++)
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const int32_t key = j + 32 * k + 8 * (i / 4) + 4 * (int32_t)h + i % 4;
+                        if (key < low[b] || key >= high[b]) s[b][k][i] = -INFINITY;
+                    }
+        }
+#pragma unroll
+        for (int b = 0; b < QB; b++) {
+            float top = s[b][0][0];
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][k][i]);
+            top *= by;
+            if (__ballot(top > m[b] + kLag) != 0) {
+                top = fmaxf(top, __shfl_xor(top, 32));
+                top = fmaxf(top, m[b]);
+                const float keep = __builtin_amdgcn_exp2f(m[b] - top);
+                m[b] = top;
+                l[b] *= keep;
+#pragma unroll
+                for (int d = 0; d < kParts; d++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[b][d][i] *= keep;
+            }
+            float sum = 0;
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(s[b][k][i], by, -m[b]));
+                    const float y = __builtin_amdgcn_exp2f(fmaf(s[b][k][i + 1], by, -m[b]));
+                    sum += x;
+                    sum += y;
+                    weights[b][k][i / 2] = pack_bf16(x, y);
+                }
+            l[b] += sum;
+        }
+        const auto operand = [](const uint32_t (&w)[2][8], int t16) {
+            const uint32_t* x = w[t16 / 2] + 4 * (t16 % 2);
+            return words8(x[0], x[1], x[2], x[3]);
+        };
+        bool odd = false;
+        if (edge) {
+            const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * lane;
+#pragma unroll
+            for (int i = 0; i < (int)(kBuffer / 1024); i++) {
+                const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(at + 1024 * i);
+                odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
+            }
+            odd = __ballot(odd) != 0;
+        }
+        if (odd) {
+            // (as in the few-row kernel)
+            for (int d = 0; d < kParts; d++) {
+                f32x16 marks[QB];
+#pragma unroll
+                for (int b = 0; b < QB; b++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) marks[b][i] = 0;
+#pragma unroll
+                for (int t16 = 0; t16 < 4; t16++) {
+                    u32x4 v = value_words(buffer, t16, 0);
+#pragma unroll
+                    for (int e = 1; e < kParts; e++)
+                        if (e == d) v = value_words(buffer, t16, e);
+                    const bf16x8 marked = words8(mark_pair(v.x), mark_pair(v.y), mark_pair(v.z),
+                                                 mark_pair(v.w));
+#pragma unroll
+                    for (int b = 0; b < QB; b++) {
+                        uint32_t seen[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int32_t key =
+                                j + 16 * t16 + 8 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
+                            seen[i] = (key >= low[b] && key < high[b] ? 0x3F80u : 0u) |
+                                      (key + 1 >= low[b] && key + 1 < high[b] ? 0x3F800000u : 0u);
+                        }
+                        marks[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            marked, words8(seen[0], seen[1], seen[2], seen[3]), marks[b], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kParts; e++)
+                    if (e == d) {
+#pragma unroll
+                        for (int b = 0; b < QB; b++)
+#pragma unroll
+                            for (int i = 0; i < 16; i++) o[b][e][i] += unmark(marks[b][i]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int t16 = 0; t16 < 4; t16++)
+#pragma unroll
+            for (int d = 0; d < kParts; d++) {
+                u32x4 v = value_words(buffer, t16, d);
+                if (odd) v = u32x4{plain_pair(v.x), plain_pair(v.y), plain_pair(v.z), plain_pair(v.w)};
+                const bf16x8 x = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+                for (int b = 0; b < QB; b++)
+                    o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, operand(weights[b], t16),
+                                                                      o[b][d], 0, 0, 0);
+            }
+    };
+
+    uint32_t buffer = 0;
+    if (first < last) fetch(first, 0);
+    for (int32_t j = first; j < last; j += kKeys) {
+        // this step's words have arrived from every wave, and every wave is
+        // done with the step before, whose buffer the next fetch fills
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (j + kKeys < last) fetch(j + kKeys, buffer ^ 1);
+        if (j < w_hi && j + kKeys > w_lo) compute(j, buffer);
+        buffer ^= 1;
+    }
+
+#pragma unroll
+    for (int b = 0; b < QB; b++) {
+        const uint32_t r = 32 * QB * wave + 32 * b + n;
+        const Row w = find_row(a, p, t, (int32_t)r);
+        const float total = l[b] + __shfl_xor(l[b], 32);
+        if (!w.on) continue;
+        const uint32_t head = kv * p.group + w.head;
+        if (t.splits == 1) {
+            const float inv = inverse(total);
+            const uint64_t at = (uint64_t)w.token * a.out.token_stride +
+                                (uint64_t)head * a.out.head_stride;
+#pragma unroll
+            for (int d = 0; d < kParts; d++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const uint32_t e = 32 * d + 8 * g + 4 * h;
+                    const float x[4] = {o[b][d][4 * g] * inv, o[b][d][4 * g + 1] * inv,
+                                        o[b][d][4 * g + 2] * inv, o[b][d][4 * g + 3] * inv};
+                    if (e < dim) store_out<4>(a.out, at + e, x);
+                }
+            if (h == 0 && a.lse != nullptr)
+                a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(m[b], total);
+        } else {
+            const Partial u = partial_of(ws, a, p, tile, kv, split);
+#pragma unroll
+            for (int d = 0; d < kParts; d++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const uint32_t e = 32 * d + 8 * g + 4 * h;
+                    if (e < dim)
+                        store_global(reinterpret_cast<uint4*>(u.o + (uint64_t)r * dim + e),
+                                     make_uint4(__float_as_uint(o[b][d][4 * g]),
+                                                __float_as_uint(o[b][d][4 * g + 1]),
+                                                __float_as_uint(o[b][d][4 * g + 2]),
+                                                __float_as_uint(o[b][d][4 * g + 3])));
+                }
+            if (h == 0) {
+                u.ml[2 * r] = m[b];
+                u.ml[2 * r + 1] = total;
+            }
+        }
+    }
+}
+
 // Joins a tile's splits: one wave per row, four elements a lane.
 __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
     const uint32_t lane = threadIdx.x % kWave;
@@ -642,16 +1010,16 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
 }
 
 template <int DP>
-hipError_t go_few(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
+hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads)), block(kThreads);
     const Score score = score_of(a);
+    if (p.tile_log2 == 4) k_attend_few<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
+    else if (p.tile_log2 == 7) k_attend_chunk<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
     if constexpr (DP <= 128) {
-        if (p.tile_log2 == 5) {
-            k_attend_few<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
-            return hipGetLastError();
-        }
+        if (p.tile_log2 == 5) k_attend_few<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
+        else if (p.tile_log2 == 8)
+            k_attend_chunk<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
     }
-    k_attend_few<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
     return hipGetLastError();
 }
 
@@ -669,9 +1037,9 @@ hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
     const AttendPlan p =
         plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
     const uint32_t dim = a.cache.head_dim;
-    hipError_t e = dim <= 64    ? go_few<64>(a, p, ws, stream)
-                   : dim <= 128 ? go_few<128>(a, p, ws, stream)
-                                : go_few<256>(a, p, ws, stream);
+    hipError_t e = dim <= 64    ? go<64>(a, p, ws, stream)
+                   : dim <= 128 ? go<128>(a, p, ws, stream)
+                                : go<256>(a, p, ws, stream);
     if (e != hipSuccess || p.splits == 1) return e;
     const uint32_t pieces = (1u << p.tile_log2) / kWaves;
     k_attend_join<<<dim3(p.tiles * a.cache.kv_heads * pieces), dim3(kThreads), 0, stream>>>(a, p,
