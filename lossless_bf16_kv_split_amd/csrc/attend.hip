@@ -651,7 +651,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                  : "memory");
 }
 
-template <int DP, int QB>
+template <int DP, int QB, bool CAP>
 __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     constexpr int kKeys = 64;
@@ -691,21 +691,14 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             q[b][s] = __builtin_bit_cast(bf16x8, v);
         }
     }
-    // keys visible to some and to every row of this wave
-    int32_t w_lo = t.lo, w_hi = t.hi, w_all_lo = t.all_lo, w_all_hi = t.all_hi;
+    // keys visible to some row of this wave
+    int32_t w_lo = t.lo, w_hi = t.hi;
     {
         const int32_t r0 = 32 * QB * (int32_t)wave;
         const Row x = find_row(a, p, t, r0), y = find_row(a, p, t, r0 + 32 * QB - 1);
-        if (r0 >= t.rows) {
-            w_hi = w_lo;  // no rows: nothing to do
-        } else {
-            w_lo = x.low;
-            w_all_hi = x.high;
-            if (y.on) {
-                w_hi = y.high;
-                w_all_lo = y.low;
-            }
-        }
+        if (x.on) w_lo = x.low;
+        else w_hi = w_lo;  // no rows: nothing to do
+        if (y.on) w_hi = y.high;
     }
 
     // this wave's part of a step: 16 keys, kLoads KB of K and of V
@@ -721,23 +714,24 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SZ_LDS uint8_t*)lds;
     const uint64_t table_row = (uint64_t)t.seq * a.cache.table_pitch;
-    const auto fetch = [&](int32_t j, uint32_t buffer) {
+    // K (which = 0) or V (1) of the step at j to a buffer
+    const auto fetch = [&](const uint64_t* pages, const uint32_t (&off)[kLoads], uint32_t which,
+                           int32_t j, uint32_t buffer) {
         const int32_t jb = j + 16 * (int32_t)wave;
-        uint64_t k_page = 0, v_page = 0;
-        if (jb < last && jb + 16 > t.lo) {
-            const uint64_t entry = table_row + ((uint32_t)jb >> a.cache.page_log2);
-            k_page = a.cache.k_pages[entry];
-            v_page = a.cache.v_pages[entry];
-        }
+        uint64_t page = 0;
+        if (jb < last && jb + 16 > t.lo)
+            page = pages[table_row + ((uint32_t)jb >> a.cache.page_log2)];
         const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
-        const auto kr = block_rows(a.cache, k_page, slot, kv, last - jb);
-        const auto vr = block_rows(a.cache, v_page, slot, kv, last - jb);
-        const uint32_t to = lds0 + buffer * kBuffer + wave * 16 * kRow;
+        const auto rows = block_rows(a.cache, page, slot, kv, last - jb);
+        const uint32_t to = lds0 + (2 * which + buffer) * kBuffer + wave * 16 * kRow;
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) load_to_lds(kr, k_off[i], to + 1024 * i);
-#pragma unroll
-        for (int i = 0; i < kLoads; i++)
-            load_to_lds(vr, v_off[i], to + 2 * kBuffer + 1024 * i);
+        for (int i = 0; i < kLoads; i++) load_to_lds(rows, off[i], to + 1024 * i);
+    };
+    const auto fetch_k = [&](int32_t j, uint32_t buffer) {
+        fetch(a.cache.k_pages, k_off, 0, j, buffer);
+    };
+    const auto fetch_v = [&](int32_t j, uint32_t buffer) {
+        fetch(a.cache.v_pages, v_off, 1, j, buffer);
     };
 
     // LDS addresses of this lane's reads, before the buffer's
@@ -775,52 +769,59 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             for (int i = 0; i < 16; i++) o[b][d][i] = 0;
     }
 
-    const auto compute = [&](int32_t j, uint32_t buffer) {
-        const bool edge = j < w_all_lo || j + kKeys > w_all_hi;
-        uint32_t weights[QB][2][8];
-        f32x16 s[QB][2];
+    const float by = CAP ? 1.0f : score.by;
+    const auto scored = [&](float x) { return CAP ? capped(score, x) : x; };
+    // follow(top): the running maximum and what hangs on it, where a score
+    // of block b (its largest in this lane: top, a multiple of 1 / by) is
+    // too far above it
+    const auto follow = [&](int b, float top) {
+        top = scored(top) * by;
+        if (__ballot(top > m[b] + kLag) == 0) return;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        top = fmaxf(top, m[b]);
+        const float keep = __builtin_amdgcn_exp2f(m[b] - top);
+        m[b] = top;
+        l[b] *= keep;
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
+        for (int d = 0; d < kParts; d++)
 #pragma unroll
-            for (int b = 0; b < QB; b++)
+            for (int i = 0; i < 16; i++) o[b][d][i] *= keep;
+    };
+
+    // A step at the rim of what the wave's rows see, one block of 32 rows
+    // at a time.
+    const auto rim = [&](int32_t j, uint32_t buffer) {
+        bool odd = false;
+        {
+            const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * lane;
 #pragma unroll
-                for (int i = 0; i < 16; i++) s[b][k][i] = 0;
-#pragma unroll
-            for (int c = 0; c < kSlices; c++) {
-                const bf16x8 x = keys_at(buffer, k, c);
-#pragma unroll
-                for (int b = 0; b < QB; b++)
-                    s[b][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[b][c], s[b][k], 0, 0, 0);
+            for (int i = 0; i < (int)(kBuffer / 1024); i++) {
+                const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(at + 1024 * i);
+                odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
             }
-        }
-        float by = score.by;
-        if (score.cap > 0) {
-            by = 1.0f;
-#pragma unroll
-            for (int b = 0; b < QB; b++)
-#pragma unroll
-                for (int k = 0; k < 2; k++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) s[b][k][i] = capped(score, s[b][k][i]);
-        }
-        if (edge) {
-#pragma unroll
-            for (int b = 0; b < QB; b++)
-#pragma unroll
-                for (int k = 0; k < 2; k++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const int32_t key = j + 32 * k + 8 * (i / 4) + 4 * (int32_t)h + i % 4;
-                        if (key < low[b] || key >= high[b]) s[b][k][i] = -INFINITY;
-                    }
+            odd = __ballot(odd) != 0;
         }
 #pragma unroll
         for (int b = 0; b < QB; b++) {
-            float top = s[b][0][0];
+            f32x16 s[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[k][i] = 0;
+#pragma unroll
+                for (int c = 0; c < kSlices; c++)
+                    s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(keys_at(buffer, k, c), q[b][c],
+                                                                   s[k], 0, 0, 0);
+            }
+            float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
-                for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][k][i]);
+                for (int i = 0; i < 16; i++) {
+                    const int32_t key = j + 32 * k + 8 * (i / 4) + 4 * (int32_t)h + i % 4;
+                    s[k][i] = key < low[b] || key >= high[b] ? -INFINITY : scored(s[k][i]);
+                    top = fmaxf(top, s[k][i]);
+                }
             top *= by;
             if (__ballot(top > m[b] + kLag) != 0) {
                 top = fmaxf(top, __shfl_xor(top, 32));
@@ -833,51 +834,26 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 #pragma unroll
                     for (int i = 0; i < 16; i++) o[b][d][i] *= keep;
             }
-            float sum = 0;
+            uint32_t weights[16];
 #pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(s[b][k][i], by, -m[b]));
-                    const float y = __builtin_amdgcn_exp2f(fmaf(s[b][k][i + 1], by, -m[b]));
-                    sum += x;
-                    sum += y;
-                    weights[b][k][i / 2] = pack_bf16(x, y);
+                    const float x = __builtin_amdgcn_exp2f(fmaf(s[k][i], by, -m[b]));
+                    const float y = __builtin_amdgcn_exp2f(fmaf(s[k][i + 1], by, -m[b]));
+                    l[b] += x + y;
+                    weights[8 * k + i / 2] = pack_bf16(x, y);
                 }
-            l[b] += sum;
-        }
-        const auto operand = [](const uint32_t (&w)[2][8], int t16) {
-            const uint32_t* x = w[t16 / 2] + 4 * (t16 % 2);
-            return words8(x[0], x[1], x[2], x[3]);
-        };
-        bool odd = false;
-        if (edge) {
-            const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * lane;
 #pragma unroll
-            for (int i = 0; i < (int)(kBuffer / 1024); i++) {
-                const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(at + 1024 * i);
-                odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
-            }
-            odd = __ballot(odd) != 0;
-        }
-        if (odd) {
-            // (as in the few-row kernel)
             for (int d = 0; d < kParts; d++) {
-                f32x16 marks[QB];
+                if (odd) {
+                    // (as in the few-row kernel)
+                    f32x16 marks;
 #pragma unroll
-                for (int b = 0; b < QB; b++)
+                    for (int i = 0; i < 16; i++) marks[i] = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) marks[b][i] = 0;
-#pragma unroll
-                for (int t16 = 0; t16 < 4; t16++) {
-                    u32x4 v = value_words(buffer, t16, 0);
-#pragma unroll
-                    for (int e = 1; e < kParts; e++)
-                        if (e == d) v = value_words(buffer, t16, e);
-                    const bf16x8 marked = words8(mark_pair(v.x), mark_pair(v.y), mark_pair(v.z),
-                                                 mark_pair(v.w));
-#pragma unroll
-                    for (int b = 0; b < QB; b++) {
+                    for (int t16 = 0; t16 < 4; t16++) {
+                        const u32x4 v = value_words(buffer, t16, d);
                         uint32_t seen[4];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
@@ -886,44 +862,190 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
                             seen[i] = (key >= low[b] && key < high[b] ? 0x3F80u : 0u) |
                                       (key + 1 >= low[b] && key + 1 < high[b] ? 0x3F800000u : 0u);
                         }
-                        marks[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            marked, words8(seen[0], seen[1], seen[2], seen[3]), marks[b], 0, 0, 0);
+                        marks = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            words8(mark_pair(v.x), mark_pair(v.y), mark_pair(v.z), mark_pair(v.w)),
+                            words8(seen[0], seen[1], seen[2], seen[3]), marks, 0, 0, 0);
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[b][d][i] += unmark(marks[i]);
                 }
 #pragma unroll
-                for (int e = 0; e < kParts; e++)
-                    if (e == d) {
-#pragma unroll
-                        for (int b = 0; b < QB; b++)
-#pragma unroll
-                            for (int i = 0; i < 16; i++) o[b][e][i] += unmark(marks[b][i]);
-                    }
+                for (int t16 = 0; t16 < 4; t16++) {
+                    u32x4 v = value_words(buffer, t16, d);
+                    if (odd)
+                        v = u32x4{plain_pair(v.x), plain_pair(v.y), plain_pair(v.z),
+                                  plain_pair(v.w)};
+                    o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, v),
+                        words8(weights[4 * t16], weights[4 * t16 + 1], weights[4 * t16 + 2],
+                               weights[4 * t16 + 3]),
+                        o[b][d], 0, 0, 0);
+                }
             }
         }
-#pragma unroll
-        for (int t16 = 0; t16 < 4; t16++)
-#pragma unroll
-            for (int d = 0; d < kParts; d++) {
-                u32x4 v = value_words(buffer, t16, d);
-                if (odd) v = u32x4{plain_pair(v.x), plain_pair(v.y), plain_pair(v.z), plain_pair(v.w)};
-                const bf16x8 x = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-                for (int b = 0; b < QB; b++)
-                    o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, operand(weights[b], t16),
-                                                                      o[b][d], 0, 0, 0);
-            }
     };
 
-    uint32_t buffer = 0;
-    if (first < last) fetch(first, 0);
-    for (int32_t j = first; j < last; j += kKeys) {
-        // this step's words have arrived from every wave, and every wave is
-        // done with the step before, whose buffer the next fetch fills
+    // A step that every row sees all of, in a pipeline: while the softmax of
+    // this step's scores (now) runs on the vector units, the matrix cores
+    // form the next step's (next); then they add this step's values.  The
+    // order is laid down instruction group by instruction group, so that
+    // each product has its share of the softmax beside it and its operand
+    // read two groups ahead.
+    struct Scores {
+        f32x16 s[QB][2];
+        float top[QB];
+    };
+    constexpr int kGroupsA = 2 * kSlices, kGroupsB = 4 * kParts, kUnits = 16 * QB;
+    const auto inner = [&](Scores& now, Scores& next, uint32_t buffer) {
+#pragma unroll
+        for (int b = 0; b < QB; b++) follow(b, now.top[b]);
+        uint32_t weights[QB][16];
+        // two weights: of 16 keys u / (4 QB), rows' block u / 4 % QB
+        const auto unit = [&](int u) {
+            const int t16 = u / (4 * QB), b = u / 4 % QB, i = 8 * (t16 % 2) + 2 * (u % 4);
+            const float x = __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][t16 / 2][i]), by, -m[b]));
+            const float y =
+                __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][t16 / 2][i + 1]), by, -m[b]));
+            l[b] += x + y;
+            weights[b][4 * t16 + u % 4] = pack_bf16(x, y);
+        };
+        constexpr int kFirst = kUnits * 3 / 4;  // units beside the first product
+        bf16x8 kf[3];
+        u32x4 vf[3];
+        kf[0] = keys_at(buffer ^ 1, 0, 0);
+        kf[1] = keys_at(buffer ^ 1, 1 / kSlices, 1 % kSlices);
+#pragma unroll
+        for (int b = 0; b < QB; b++)
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) next.s[b][k][i] = 0;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < kGroupsA; g++) {
+            if (g + 2 < kGroupsA)
+                kf[(g + 2) % 3] = keys_at(buffer ^ 1, (g + 2) / kSlices, (g + 2) % kSlices);
+            else
+                vf[g + 2 - kGroupsA] = value_words(buffer, 0, g + 2 - kGroupsA);
+#pragma unroll
+            for (int b = 0; b < QB; b++)
+                next.s[b][g / kSlices] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    kf[g % 3], q[b][g % kSlices], next.s[b][g / kSlices], 0, 0, 0);
+#pragma unroll
+            for (int u = g * kFirst / kGroupsA; u < (g + 1) * kFirst / kGroupsA; u++) unit(u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int b = 0; b < QB; b++) next.top[b] = next.s[b][0][0];
+#pragma unroll
+        for (int g = 0; g < kGroupsB; g++) {
+            if (g + 2 < kGroupsB)
+                vf[(g + 2) % 3] = value_words(buffer, (g + 2) / kParts, (g + 2) % kParts);
+            const int t16 = g / kParts, d = g % kParts;
+#pragma unroll
+            for (int b = 0; b < QB; b++)
+                o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, vf[g % 3]),
+                    words8(weights[b][4 * t16], weights[b][4 * t16 + 1], weights[b][4 * t16 + 2],
+                           weights[b][4 * t16 + 3]),
+                    o[b][d], 0, 0, 0);
+            if (g < kGroupsB / 2) {
+#pragma unroll
+                for (int u = kFirst + g * (kUnits - kFirst) / (kGroupsB / 2);
+                     u < kFirst + (g + 1) * (kUnits - kFirst) / (kGroupsB / 2); u++)
+                    unit(u);
+            } else {
+                constexpr int kHalf = kGroupsB / 2;
+#pragma unroll
+                for (int u = (g - kHalf) * 32 / kHalf; u < (g - kHalf + 1) * 32 / kHalf; u++)
+#pragma unroll
+                    for (int b = 0; b < QB; b++)
+                        next.top[b] = fmaxf(next.top[b], next.s[b][u / 16][u % 16]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // The scores of the first such step
+    const auto ahead = [&](Scores& x, uint32_t buffer) {
+#pragma unroll
+        for (int b = 0; b < QB; b++) {
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) x.s[b][k][i] = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int c = 0; c < kSlices; c++) {
+                const bf16x8 f = keys_at(buffer, k, c);
+#pragma unroll
+                for (int b = 0; b < QB; b++)
+                    x.s[b][k] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][c], x.s[b][k], 0, 0, 0);
+            }
+#pragma unroll
+        for (int b = 0; b < QB; b++) {
+            x.top[b] = x.s[b][0][0];
+#pragma unroll
+            for (int i = 1; i < 32; i++) x.top[b] = fmaxf(x.top[b], x.s[b][i / 16][i % 16]);
+        }
+    };
+
+    // What was fetched for a step has arrived from every wave, and every
+    // wave is done with the step before, whose buffers the next fetches fill.
+    const auto arrived = [&] {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (j + kKeys < last) fetch(j + kKeys, buffer ^ 1);
-        if (j < w_hi && j + kKeys > w_lo) compute(j, buffer);
-        buffer ^= 1;
+    };
+    // Steps of 64 keys; step x has buffers x % 2.  [in0, in1): steps all of
+    // which every row sees, an even number of them.
+    const int32_t steps = first < last ? (last - first + kKeys - 1) / kKeys : 0;
+    int32_t in0 = t.all_lo > first ? (t.all_lo - first + kKeys - 1) / kKeys : 0;
+    int32_t in1 = (t.all_hi < last ? t.all_hi : last) - first;
+    in1 = in1 > 0 ? in1 / kKeys : 0;
+    if (in1 > steps) in1 = steps;
+    if (in0 > in1) in0 = in1;
+    in0 = (in0 + 1) & ~1;  // (even, so that the pipeline's buffers are constants)
+    if (in0 > in1) in0 = in1;
+    in1 -= (in1 - in0) & 1;
+    if (steps > 0) {
+        fetch_k(first, 0);
+        fetch_v(first, 0);
     }
+    int32_t x = 0;
+    bool k_ahead = false;  // the keys of step x + 1 are fetched
+    for (;;) {
+        const int32_t stop = x < in1 && in0 < in1 ? in0 : steps;
+        for (; x < stop; x++) {
+            const int32_t j = first + x * kKeys;
+            arrived();
+            if (x + 1 < steps) {
+                if (!k_ahead) fetch_k(j + kKeys, (x + 1) & 1);
+                fetch_v(j + kKeys, (x + 1) & 1);
+            }
+            k_ahead = false;
+            if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1);
+        }
+        if (x >= steps) break;
+        Scores even, uneven;
+        arrived();
+        fetch_k(first + (x + 1) * kKeys, 1);
+        ahead(even, 0);
+        for (; x < in1; x += 2) {
+            const int32_t j = first + x * kKeys;
+            arrived();
+            fetch_k(j + 2 * kKeys, 0);
+            fetch_v(j + kKeys, 1);
+            inner(even, uneven, 0);
+            arrived();
+            fetch_k(j + 3 * kKeys, 1);
+            fetch_v(j + 2 * kKeys, 0);
+            inner(uneven, even, 1);
+        }
+        k_ahead = true;
+    }
+    // nothing may still be on its way to this workgroup's LDS when it ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
 #pragma unroll
     for (int b = 0; b < QB; b++) {
@@ -1009,18 +1131,27 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
         a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
 }
 
-template <int DP>
+template <int DP, bool CAP>
 hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads)), block(kThreads);
     const Score score = score_of(a);
     if (p.tile_log2 == 4) k_attend_few<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
-    else if (p.tile_log2 == 7) k_attend_chunk<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
+    else if (p.tile_log2 == 7)
+        k_attend_chunk<DP, 1, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
     if constexpr (DP <= 128) {
         if (p.tile_log2 == 5) k_attend_few<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
         else if (p.tile_log2 == 8)
-            k_attend_chunk<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
+            k_attend_chunk<DP, 2, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
     }
     return hipGetLastError();
+}
+
+template <bool CAP>
+hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
+    const uint32_t dim = a.cache.head_dim;
+    return dim <= 64    ? go<64, CAP>(a, p, ws, stream)
+           : dim <= 128 ? go<128, CAP>(a, p, ws, stream)
+                        : go<256, CAP>(a, p, ws, stream);
 }
 
 }  // namespace
@@ -1036,10 +1167,7 @@ hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
     if (a.batch.n_seqs == 0 || a.batch.n_tokens == 0) return hipSuccess;
     const AttendPlan p =
         plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
-    const uint32_t dim = a.cache.head_dim;
-    hipError_t e = dim <= 64    ? go<64>(a, p, ws, stream)
-                   : dim <= 128 ? go<128>(a, p, ws, stream)
-                                : go<256>(a, p, ws, stream);
+    const hipError_t e = a.softcap > 0 ? go<true>(a, p, ws, stream) : go<false>(a, p, ws, stream);
     if (e != hipSuccess || p.splits == 1) return e;
     const uint32_t pieces = (1u << p.tile_log2) / kWaves;
     k_attend_join<<<dim3(p.tiles * a.cache.kv_heads * pieces), dim3(kThreads), 0, stream>>>(a, p,
