@@ -714,24 +714,33 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SZ_LDS uint8_t*)lds;
     const uint64_t table_row = (uint64_t)t.seq * a.cache.table_pitch;
-    // K (which = 0) or V (1) of the step at j to a buffer
-    const auto fetch = [&](const uint64_t* pages, const uint32_t (&off)[kLoads], uint32_t which,
-                           int32_t j, uint32_t buffer) {
+    // The page of this wave's block of the step at j: its address, looked up
+    // a step before it is used (a load that nothing waits for: the step's
+    // own wait covers it).
+    const auto page_at = [&](const uint64_t* pages, int32_t j) {
         const int32_t jb = j + 16 * (int32_t)wave;
-        uint64_t page = 0;
-        if (jb < last && jb + 16 > t.lo)
-            page = pages[table_row + ((uint32_t)jb >> a.cache.page_log2)];
+        return jb < last && jb + 16 > t.lo
+                   ? pages[table_row + ((uint32_t)jb >> a.cache.page_log2)]
+                   : 0;
+    };
+    // K (which = 0) or V (1) of the step at j to a buffer
+    const auto fetch = [&](uint64_t page, const uint32_t (&off)[kLoads], uint32_t which, int32_t j,
+                           uint32_t buffer) {
+        const int32_t jb = j + 16 * (int32_t)wave;
         const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
-        const auto rows = block_rows(a.cache, page, slot, kv, last - jb);
+        const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(page >> 32))
+                                << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)page);
+        const auto rows = block_rows(a.cache, at, slot, kv, last - jb);
         const uint32_t to = lds0 + (2 * which + buffer) * kBuffer + wave * 16 * kRow;
 #pragma unroll
         for (int i = 0; i < kLoads; i++) load_to_lds(rows, off[i], to + 1024 * i);
     };
-    const auto fetch_k = [&](int32_t j, uint32_t buffer) {
-        fetch(a.cache.k_pages, k_off, 0, j, buffer);
-    };
-    const auto fetch_v = [&](int32_t j, uint32_t buffer) {
-        fetch(a.cache.v_pages, v_off, 1, j, buffer);
+    uint64_t next_k = page_at(a.cache.k_pages, first), next_v = page_at(a.cache.v_pages, first);
+    const auto fetch_k = [&](int32_t j, uint32_t buffer) { fetch(next_k, k_off, 0, j, buffer); };
+    const auto fetch_v = [&](int32_t j, uint32_t buffer) { fetch(next_v, v_off, 1, j, buffer); };
+    const auto look_up = [&](int32_t k, int32_t v) {
+        next_k = page_at(a.cache.k_pages, k);
+        next_v = page_at(a.cache.v_pages, v);
     };
 
     // LDS addresses of this lane's reads, before the buffer's
@@ -907,6 +916,9 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             const float y =
                 __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][t16 / 2][i + 1]), by, -m[b]));
             l[b] += x + y;
+            // (kept here: left to itself the compiler puts the additions off
+            // and holds every weight in a register until then)
+            asm volatile("" : "+v"(l[b]));
             weights[b][4 * t16 + u % 4] = pack_bf16(x, y);
         };
         constexpr int kFirst = kUnits * 3 / 4;  // units beside the first product
@@ -1011,6 +1023,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     if (steps > 0) {
         fetch_k(first, 0);
         fetch_v(first, 0);
+        look_up(first + kKeys, first + kKeys);
     }
     int32_t x = 0;
     bool k_ahead = false;  // the keys of step x + 1 are fetched
@@ -1019,27 +1032,32 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
         for (; x < stop; x++) {
             const int32_t j = first + x * kKeys;
             arrived();
-            if (x + 1 < steps) {
-                if (!k_ahead) fetch_k(j + kKeys, (x + 1) & 1);
-                fetch_v(j + kKeys, (x + 1) & 1);
-            }
+            if (!k_ahead) fetch_k(j + kKeys, (x + 1) & 1);
+            fetch_v(j + kKeys, (x + 1) & 1);
+            look_up(j + 2 * kKeys, j + 2 * kKeys);
             k_ahead = false;
             if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1);
         }
         if (x >= steps) break;
         Scores even, uneven;
-        arrived();
-        fetch_k(first + (x + 1) * kKeys, 1);
+        {
+            const int32_t j = first + x * kKeys;
+            arrived();
+            fetch_k(j + kKeys, 1);
+            look_up(j + 2 * kKeys, j + kKeys);
+        }
         ahead(even, 0);
         for (; x < in1; x += 2) {
             const int32_t j = first + x * kKeys;
             arrived();
             fetch_k(j + 2 * kKeys, 0);
             fetch_v(j + kKeys, 1);
+            look_up(j + 3 * kKeys, j + 2 * kKeys);
             inner(even, uneven, 0);
             arrived();
             fetch_k(j + 3 * kKeys, 1);
             fetch_v(j + 2 * kKeys, 0);
+            look_up(j + 4 * kKeys, j + 3 * kKeys);
             inner(uneven, even, 1);
         }
         k_ahead = true;
