@@ -562,10 +562,10 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  *   out       BF16 or F32, as many heads
  *   d_lse     optional device float[n_tokens][q heads]: ln of the sum of
  *             exp(score) over the visible keys
- *   max_len   a host-side bound of d_lens (longer sequences are refused),
- *             1 .. pages_per_seq * page_tokens or 2^30, the lesser; 0 means
- *             that.  Work is split for it, so it should not be far above the
- *             lengths.
+ *   max_len   a host-side bound of d_lens (longer sequences are refused);
+ *             0, or anything past it, means what the pages hold,
+ *             pages_per_seq * page_tokens (2^30 at most).  Work is split for
+ *             this bound, so it should not be far above the lengths.
  *   scale     > 0, finite; softcap >= 0, finite (0: none)
  *   d_workspace, workspace_bytes   256-byte aligned, at least
  *             sz_attend_workspace_size(q->heads, cache, batch, max_len); any

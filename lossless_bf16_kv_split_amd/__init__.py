@@ -392,7 +392,8 @@ def _on_device(t, dtype, what: str, dim: int | None = None):
 
 class _Descriptor(ctypes.Structure):
     def _set(self, device, *keep):
-        self._keep, self._device, self._at = keep, device, ctypes.addressof(self)
+        self._keep, self._at = keep, ctypes.addressof(self)
+        self._index = device.index
 
 
 class Heads(_Descriptor):
@@ -413,7 +414,7 @@ class Heads(_Descriptor):
         strides = [t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
         super().__init__(t.data_ptr(), t.shape[1], strides[0], strides[1],
                          SZ_TYPE_F32 if t.dtype == torch.float32 else SZ_TYPE_BF16)
-        self.tokens, self.head_dim = t.shape[0], t.shape[2]
+        self.tokens, self.dim = t.shape[0], t.shape[2]
         self._set(t.device, t)
 
 
@@ -474,30 +475,36 @@ class Rope(_Descriptor):
 
 
 def _at(x) -> int | None:
-    """Address of a descriptor, or of a tensor (a descriptor of its own is
-    made, and must be kept until the call returns)."""
+    """Address of a descriptor."""
     return None if x is None else x._at
 
 
 def _heads(x):
-    return x if x is None or isinstance(x, Heads) else Heads(x)
+    """A descriptor as it is, or one of a tensor (to be kept until the call
+    returns)."""
+    return x if x is None or type(x) is Heads else Heads(x)
 
 
-def _same_device(*xs):
-    """The device of the descriptors and tensors given (None skipped)."""
-    devices = {x._device if isinstance(x, _Descriptor) else x.device for x in xs
-               if x is not None and not isinstance(x, int)}
-    if len(devices) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-    return devices.pop()
-
-
-def _device_stream(device, stream):
-    """Stream handle, with the tensors' device required to be current."""
+def _call_stream(stream, *xs):
+    """The stream of a call whose descriptors and tensors are given (None and
+    integer addresses skipped): all on the current device, as `stream` must
+    be."""
     import torch
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"the tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    index = None
+    for x in xs:
+        if x is not None and type(x) is not int:
+            i = x._index if isinstance(x, _Descriptor) else x.get_device()
+            if index is None:
+                index = i
+            elif i != index:
+                raise ValueError("the call's tensors are on different devices")
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on device {index}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    if stream is None:
+        # (a tenth of the time of torch.cuda.current_stream(), which counts
+        # beside kernels of a few microseconds)
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
@@ -509,12 +516,12 @@ def _tokens(n: int, *xs) -> None:
 
 def _dims(dim: int, *xs) -> None:
     for x in xs:
-        if x is not None and x.head_dim != dim:
-            raise ValueError(f"rows of {x.head_dim} elements where {dim} are expected")
+        if x is not None and x.dim != dim:
+            raise ValueError(f"rows of {x.dim} elements where {dim} are expected")
 
 
 def _array(x, dtype, n: int, what: str) -> None:
-    if x is not None and not isinstance(x, int) and \
+    if x is not None and type(x) is not int and \
             (x.dtype != dtype or x.numel() < n or not x.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous tensor of at least {n} {dtype}")
 
@@ -544,7 +551,7 @@ def sz_qk_norm_rope(q, q_out, q_weight, k, k_out, k_weight, head_dim: int, n_tok
     Rope or None."""
     import torch
     q, q_out, k, k_out = _heads(q), _heads(q_out), _heads(k), _heads(k_out)
-    device = _same_device(q, q_out, q_weight, k, k_out, k_weight, positions, rope)
+    stream = _call_stream(stream, q, q_out, q_weight, k, k_out, k_weight, positions, rope)
     _tokens(n_tokens, q, q_out, k, k_out)
     _dims(head_dim, q, q_out, k, k_out)
     _array(q_weight, torch.float32, head_dim, "q_weight")
@@ -552,7 +559,7 @@ def sz_qk_norm_rope(q, q_out, q_weight, k, k_out, k_weight, head_dim: int, n_tok
     _array(positions, torch.int32, n_tokens, "positions")
     _check(_lib.sz_qk_norm_rope(_at(q), _at(q_out), _ptr(q_weight), _at(k), _at(k_out),
                                 _ptr(k_weight), head_dim, n_tokens, _ptr(positions), eps,
-                                _at(rope), _device_stream(device, stream)), "sz_qk_norm_rope")
+                                _at(rope), stream), "sz_qk_norm_rope")
 
 
 def _check_batch(cache, batch, d_status) -> None:
@@ -568,8 +575,8 @@ def sz_kv_append(k, v, k_weight, q, q_out, q_weight, eps: float, rope, positions
     KVCache; batch: a Batch; rope: a Rope or None."""
     import torch
     k, v, q, q_out = _heads(k), _heads(v), _heads(q), _heads(q_out)
-    device = _same_device(k, v, k_weight, q, q_out, q_weight, rope, positions, cache, batch,
-                          d_status)
+    stream = _call_stream(stream, k, v, k_weight, q, q_out, q_weight, rope, positions, cache,
+                          batch, d_status)
     _tokens(batch.n_tokens, k, v, q, q_out)
     _dims(cache.head_dim, k, v, q, q_out)
     _array(q_weight, torch.float32, cache.head_dim, "q_weight")
@@ -578,7 +585,7 @@ def sz_kv_append(k, v, k_weight, q, q_out, q_weight, eps: float, rope, positions
     _check_batch(cache, batch, d_status)
     _check(_lib.sz_kv_append(_at(k), _at(v), _ptr(k_weight), _at(q), _at(q_out), _ptr(q_weight),
                              eps, _at(rope), _ptr(positions), _at(cache), _at(batch),
-                             _ptr(d_status), _device_stream(device, stream)), "sz_kv_append")
+                             _ptr(d_status), stream), "sz_kv_append")
 
 
 def sz_attend_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
@@ -592,7 +599,7 @@ def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softc
     tensor [tokens, heads] or None; cache: a KVCache; batch: a Batch."""
     import torch
     q, out = _heads(q), _heads(out)
-    device = _same_device(q, out, lse, cache, batch, workspace, d_status)
+    stream = _call_stream(stream, q, out, lse, cache, batch, workspace, d_status)
     _tokens(batch.n_tokens, q, out)
     _dims(cache.head_dim, q, out)
     _array(lse, torch.float32, batch.n_tokens * q.heads, "lse")
@@ -600,8 +607,7 @@ def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softc
     _check_batch(cache, batch, d_status)
     _check(_lib.sz_attend_pages(_at(q), _at(out), _ptr(lse), _at(cache), _at(batch), max_len,
                                 scale, softcap, int(causal), window, _ptr(workspace),
-                                workspace_bytes, _ptr(d_status), _device_stream(device, stream)),
-           "sz_attend_pages")
+                                workspace_bytes, _ptr(d_status), stream), "sz_attend_pages")
 
 
 # ---- conveniences (torch allocates; the library computes) -----------------

@@ -63,34 +63,58 @@ struct AttendPlan {
     uint32_t tiles;
     uint32_t splits;     // most splits of a tile
     uint32_t split_len;
+    uint32_t bound;      // of splits, whatever the window
+    bool wide;           // few rows, no splits, a CU each: eight waves
     uint64_t units() const { return (uint64_t)tiles * splits; }
-    bool few() const { return tile_log2 <= 5; }
+    bool few() const { return tile_log2 == 4; }
 };
 
 constexpr uint32_t kStep = 128;  // split lengths are multiples of this many keys
 // Workgroups that keep 256 CUs busy and even: of the few-row kernel, and of
 // the chunk kernel.
-constexpr uint64_t kFillFew = 2048, kFillChunk = 512;
+constexpr uint64_t kFillFew = 4096, kFillChunk = 512;
+// The fewest keys of a split; and the bytes of keys and values that one
+// workgroup reads (at about 50 GB/s, what one CU gets) in the time of the
+// second launch that a split would need.
+constexpr uint64_t kLeastFew = 128, kLeastChunk = 256;
+constexpr uint64_t kWholeBytes = 288 * 1024;
+
+constexpr uint64_t kMaxSplits = 64;
+constexpr uint64_t kCus = 256;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
-                       uint64_t max_len) {
+                       uint64_t max_len, uint64_t window) {
     AttendPlan p;
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
     if (rows <= 16 * n_seqs) p.tile_log2 = 4;
-    else if (rows <= 32 * n_seqs && c.head_dim <= 128) p.tile_log2 = 5;
     else p.tile_log2 = rows > 128 * n_seqs && c.head_dim <= 128 ? 8 : 7;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
-    const uint64_t groups = (uint64_t)p.tiles * c.kv_heads;
+    // keys of a tile: a window shows its rows' tokens' own keys and those of
+    // a window before; the first split starts at a multiple of 32 keys
+    uint64_t keys = max_len;
+    const uint64_t tokens = ((1u << p.tile_log2) - 1) / p.group + 2;
+    if (window != 0) {
+        if (window < keys && window + tokens < keys) keys = window + tokens;
+        keys += 31;
+    }
+    // workgroups without splits, as far as can be told here: numbers of tiles
+    // are mostly free where sequences have few rows each
+    const uint64_t full = rows >> p.tile_log2;
+    const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
     const uint64_t fill = p.few() ? kFillFew : kFillChunk;
     uint64_t splits = (fill + groups - 1) / groups;
-    const uint64_t most = (max_len + 2 * kStep - 1) / (2 * kStep);
-    splits = splits < 1 ? 1 : splits > most ? most : splits;
-    // a split starts at a multiple of 32 keys, which a window can put up to
-    // 31 keys before the first visible one
-    const uint64_t len = (max_len + 31 + splits - 1) / splits;
+    const uint64_t least = p.few() ? kLeastFew : kLeastChunk;
+    const uint64_t known = keys < max_len ? keys : max_len;
+    const uint64_t most =
+        p.few() && known * c.head_dim * 4 <= kWholeBytes ? 1 : known / least;
+    splits = splits > most ? most : splits;
+    splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
+    p.bound = (uint32_t)splits;
+    const uint64_t len = (keys + splits - 1) / splits;
     p.split_len = (uint32_t)((len + kStep - 1) / kStep * kStep);
-    p.splits = (uint32_t)((max_len + 31 + p.split_len - 1) / p.split_len);
+    p.splits = (uint32_t)((keys + p.split_len - 1) / p.split_len);
+    p.wide = p.tile_log2 == 4 && p.splits == 1 && groups <= kCus && c.head_dim <= 128;
     return p;
 }
 
@@ -280,8 +304,8 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 
 // ---- few rows: a decode step, drafted tokens ------------------------------
 //
-// One workgroup takes a tile of 16 (or 32) rows and a split of its keys;
-// each wave streams every fourth block of 32 keys straight from the pages
+// One workgroup takes a tile of 16 rows and a split of its keys; each wave
+// streams every fourth (or eighth) block of 32 keys straight from the pages
 // into registers, with the next block's loads in flight, and the waves'
 // results are joined in LDS at the end.  Bound by the bytes of the cache.
 //
@@ -299,19 +323,20 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 //    elements 8 n + i as its rows.
 //  - O^T's result: lane (query n, h) then has, for r < 4, elements
 //    32 h + 8 r + i: 32 consecutive ones.
-template <int DP, int RB>
-__global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Attend a, AttendPlan p,
-                                                                         Score score,
-                                                                         uint8_t* ws) {
+template <int DP, int WAVES, bool STREAM>
+__global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void k_attend_few(
+    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+    constexpr int kStride = 32 * WAVES;    // keys that the workgroup takes at a time
+    constexpr int kAux = STREAM ? 2 : 0;   // (the loads' nt bit)
     constexpr int kSlices = DP / 32;       // of K, 32 elements each
     constexpr int kVec = DP < 128 ? 4 : 8; // elements of a V row per load
     constexpr int kVLoads = DP / (16 * kVec);
     constexpr int kProducts = DP / 16;     // of 16 elements of the output
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
-    const uint32_t rest = blockIdx.x / a.cache.kv_heads;
-    const uint32_t split = rest % p.splits, tile = rest / p.splits;
+    const uint32_t split = blockIdx.x % p.splits;
+    const uint32_t rest = blockIdx.x / p.splits;
+    const uint32_t kv = rest % a.cache.kv_heads, tile = rest / a.cache.kv_heads;
     Tile t;
     if (!find_tile(a, p, tile, t) || split >= t.splits) return;
     const int32_t first = t.from + (int32_t)(split * p.split_len);
@@ -320,22 +345,19 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
 
     // the rows, their queries (slices of 32 elements, zeros past head_dim)
     const uint32_t dim = a.cache.head_dim;
-    bf16x8 q[RB][kSlices];
-    int32_t low[RB], high[RB];
-#pragma unroll
-    for (int b = 0; b < RB; b++) {
-        const Row w = find_row(a, p, t, 16 * b + (int32_t)n);
-        low[b] = w.low;
-        high[b] = w.high;
+    bf16x8 q[kSlices];
+    const Row mine = find_row(a, p, t, (int32_t)n);
+    const int32_t low = mine.low, high = mine.high;
+    {
         const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
-                              (uint64_t)w.token * a.q.token_stride +
-                              (uint64_t)(kv * p.group + w.head) * a.q.head_stride;
+                              (uint64_t)mine.token * a.q.token_stride +
+                              (uint64_t)(kv * p.group + mine.head) * a.q.head_stride;
 #pragma unroll
         for (int s = 0; s < kSlices; s++) {
             u32x4 v = {0, 0, 0, 0};
-            if (w.on && 32 * s + 8 * h < dim)
+            if (mine.on && 32 * s + 8 * h < dim)
                 v = *(const SZ_GLOBAL u32x4*)(row + 32 * s + 8 * h);
-            q[b][s] = __builtin_bit_cast(bf16x8, v);
+            q[s] = __builtin_bit_cast(bf16x8, v);
         }
     }
 
@@ -373,31 +395,26 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
             const auto vr = block_rows(a.cache, v_page, slot, kv, last - jb);
 #pragma unroll
             for (int s = 0; s < kSlices; s++)
-                x.k[b][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, k_off[s], 0, 0);
+                x.k[b][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, k_off[s], 0, kAux);
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
                 for (int u = 0; u < kVLoads; u++) {
                     if constexpr (kVec == 8) {
                         x.v[4 * b + i][u] =
-                            __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[i][u], 0, 0);
+                            __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[i][u], 0, kAux);
                     } else {
-                        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[i][u], 0, 0);
+                        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[i][u], 0, kAux);
                         x.v[4 * b + i][u] = u32x4{w.x, w.y, 0, 0};
                     }
                 }
         }
     };
 
-    float m[RB], l[RB];
-    f32x4 o[RB][kProducts];
+    float m = kNoKey, l = 0;
+    f32x4 o[kProducts];
 #pragma unroll
-    for (int b = 0; b < RB; b++) {
-        m[b] = kNoKey;
-        l[b] = 0;
-#pragma unroll
-        for (int d = 0; d < kProducts; d++) o[b][d] = f32x4{0, 0, 0, 0};
-    }
+    for (int d = 0; d < kProducts; d++) o[d] = f32x4{0, 0, 0, 0};
 
     // operand i of the transposed values
     const auto values = [&](const Block& x, int d) {
@@ -428,9 +445,8 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
             }
             odd = __ballot(odd) != 0;
         }
-        uint32_t weights[RB][4], seen[RB][4];
-#pragma unroll
-        for (int b = 0; b < RB; b++) {
+        uint32_t weights[4], seen[4];
+        {
             float s[8];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
@@ -438,7 +454,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
 #pragma unroll
                 for (int c = 0; c < kSlices; c++)
                     z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, x.k[k][c]), q[b][c], z, 0, 0, 0);
+                        __builtin_bit_cast(bf16x8, x.k[k][c]), q[c], z, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; i++) s[4 * k + i] = z[i];
             }
@@ -453,35 +469,35 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const int32_t key = j + 16 * (i / 4) + 4 * (int32_t)h + i % 4;
-                    if (key < low[b] || key >= high[b]) s[i] = -INFINITY;
+                    if (key < low || key >= high) s[i] = -INFINITY;
                 }
             }
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 8; i++) top = fmaxf(top, s[i]);
-            if (__ballot(top > m[b] + kLag) != 0) {
+            if (__ballot(top > m + kLag) != 0) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                top = fmaxf(top, m[b]);
-                const float keep = __builtin_amdgcn_exp2f(m[b] - top);
-                m[b] = top;
-                l[b] *= keep;
+                top = fmaxf(top, m);
+                const float keep = __builtin_amdgcn_exp2f(m - top);
+                m = top;
+                l *= keep;
 #pragma unroll
-                for (int d = 0; d < kProducts; d++) o[b][d] *= keep;
+                for (int d = 0; d < kProducts; d++) o[d] *= keep;
             }
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                s[i] = __builtin_amdgcn_exp2f(s[i] - m[b]);
-                l[b] += s[i];
+                s[i] = __builtin_amdgcn_exp2f(s[i] - m);
+                l += s[i];
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++) weights[b][i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+            for (int i = 0; i < 4; i++) weights[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
             if (odd) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int32_t key = j + 16 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
-                    seen[b][i] = (key >= low[b] && key < high[b] ? 0x3F80u : 0u) |
-                                 (key + 1 >= low[b] && key + 1 < high[b] ? 0x3F800000u : 0u);
+                    seen[i] = (key >= low && key < high ? 0x3F80u : 0u) |
+                                 (key + 1 >= low && key + 1 < high ? 0x3F800000u : 0u);
                 }
             }
         }
@@ -500,51 +516,43 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
                         x.v[k][u][i] = plain_pair(x.v[k][u][i]);
                     }
 #pragma unroll
-            for (int d = 0; d < kProducts; d++)
-#pragma unroll
-                for (int b = 0; b < RB; b++) {
+            for (int d = 0; d < kProducts; d++) {
                     f32x4 z = {0, 0, 0, 0};
                     z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        values(y, d), words8(seen[b][0], seen[b][1], seen[b][2], seen[b][3]), z, 0,
+                        values(y, d), words8(seen[0], seen[1], seen[2], seen[3]), z, 0,
                         0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) o[b][d][i] += unmark(z[i]);
+                    for (int i = 0; i < 4; i++) o[d][i] += unmark(z[i]);
                 }
         }
 #pragma unroll
         for (int d = 0; d < kProducts; d++) {
-            const bf16x8 v = values(x, d);
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-                o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    v, words8(weights[b][0], weights[b][1], weights[b][2], weights[b][3]), o[b][d],
-                    0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                values(x, d), words8(weights[0], weights[1], weights[2], weights[3]), o[d], 0, 0, 0);
         }
     };
 
     int32_t j = first + 32 * (int32_t)wave;
     Block even, odd;
     load(even, j);
-    for (; j < last; j += 2 * kStep) {
-        load(odd, j + kStep);
+    for (; j < last; j += 2 * kStride) {
+        load(odd, j + kStride);
         compute(even, j);
-        load(even, j + 2 * kStep);
-        if (j + (int32_t)kStep < last) compute(odd, j + kStep);
+        load(even, j + 2 * kStride);
+        if (j + kStride < last) compute(odd, j + kStride);
     }
 
     // join the waves: row by row in LDS
     constexpr int kPitch = DP + 4;
-    __shared__ float join_o[kWaves][16][kPitch];
-    __shared__ float join_m[kWaves][16], join_l[kWaves][16];
+    __shared__ float join_o[WAVES][16][kPitch];
+    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
     constexpr int kRun = 4 * kVec;  // consecutive elements of a lane's result, per 16 kVec
-#pragma unroll
-    for (int b = 0; b < RB; b++) {
-        float sum = l[b];
+    {
+        float sum = l;
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (b > 0) __syncthreads();
         if (h == 0) {
-            join_m[wave][n] = m[b];
+            join_m[wave][n] = m;
             join_l[wave][n] = sum;
         }
 #pragma unroll
@@ -554,18 +562,18 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
 #pragma unroll
                 for (int i = 0; i < kVec; i++)
                     join_o[wave][n][16 * kVec * u + kRun * h + kVec * r + i] =
-                        o[b][kVec * u + i][r];
+                        o[kVec * u + i][r];
         __syncthreads();
-        constexpr int kPer = DP / 16;  // elements of a thread
-        const uint32_t r = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
-        const Row w = find_row(a, p, t, 16 * b + (int32_t)r);
-        if (w.on) {
+        constexpr int kPer = DP / 16;  // elements of a thread, of the first 256
+        const uint32_t r = threadIdx.x / 16 % 16, e = threadIdx.x % 16 * kPer;
+        const Row w = find_row(a, p, t, (int32_t)r);
+        if (w.on && threadIdx.x < kThreads) {
             float top = join_m[0][r];
 #pragma unroll
-            for (int i = 1; i < (int)kWaves; i++) top = fmaxf(top, join_m[i][r]);
+            for (int i = 1; i < WAVES; i++) top = fmaxf(top, join_m[i][r]);
             float total = 0, x[kPer] = {};
 #pragma unroll
-            for (int i = 0; i < (int)kWaves; i++) {
+            for (int i = 0; i < WAVES; i++) {
                 const float keep = __builtin_amdgcn_exp2f(join_m[i][r] - top);
                 total += join_l[i][r] * keep;
 #pragma unroll
@@ -594,13 +602,13 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void k_attend_few(Atten
                 for (int k = 0; k < kPer; k += 4)
                     if (e + k < dim)
                         store_global(reinterpret_cast<uint4*>(
-                                         u.o + (uint64_t)(16 * b + r) * dim + e + k),
+                                         u.o + (uint64_t)r * dim + e + k),
                                      make_uint4(__float_as_uint(x[k]), __float_as_uint(x[k + 1]),
                                                 __float_as_uint(x[k + 2]),
                                                 __float_as_uint(x[k + 3])));
                 if (e == 0) {
-                    u.ml[2 * (16 * b + r)] = top;
-                    u.ml[2 * (16 * b + r) + 1] = total;
+                    u.ml[2 * r] = top;
+                    u.ml[2 * r + 1] = total;
                 }
             }
         }
@@ -1109,8 +1117,12 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     }
 }
 
-// Joins a tile's splits: one wave per row, four elements a lane.
+// Joins a tile's splits (at most kMaxSplits, one per lane): one wave per row.
+// LANES lanes take four elements each of one split's sums, so that a wave
+// reads 64 / LANES splits at a time, with nothing to wait for between them.
+template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
+    constexpr uint32_t kAtOnce = kWave / LANES;
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t pieces = (1u << p.tile_log2) / kWaves;
@@ -1121,44 +1133,61 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     Tile t;
     if (!find_tile(a, p, tile, t) || t.splits == 1 || r >= t.rows) return;
     const Row w = find_row(a, p, t, r);
-    float top = kNoKey;
-    for (uint32_t s = 0; s < t.splits; s++)
-        top = fmaxf(top, partial_of(ws, a, p, tile, kv, s).ml[2 * r]);
-    float total = 0, x[4] = {};
-    const uint32_t e = 4 * lane, dim = a.cache.head_dim;
-    for (uint32_t s = 0; s < t.splits; s++) {
-        const Partial u = partial_of(ws, a, p, tile, kv, s);
-        const float keep = __builtin_amdgcn_exp2f(u.ml[2 * r] - top);
-        total += u.ml[2 * r + 1] * keep;
-        if (e < dim) {
-            const uint4 v = load_global(reinterpret_cast<const uint4*>(u.o + (uint64_t)r * dim + e));
-            x[0] = fmaf(__uint_as_float(v.x), keep, x[0]);
-            x[1] = fmaf(__uint_as_float(v.y), keep, x[1]);
-            x[2] = fmaf(__uint_as_float(v.z), keep, x[2]);
-            x[3] = fmaf(__uint_as_float(v.w), keep, x[3]);
-        }
+    const uint32_t dim = a.cache.head_dim;
+    const Partial u = partial_of(ws, a, p, tile, kv, 0);
+    float top = kNoKey, total = 0;
+    if (lane < t.splits) {
+        top = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
+        total = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
     }
-    const float inv = inverse(total);
+    const float mine = top;
 #pragma unroll
-    for (int i = 0; i < 4; i++) x[i] *= inv;
+    for (int d = 1; d < (int)kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    const float weight = __builtin_amdgcn_exp2f(mine - top);
+    total *= weight;
+#pragma unroll
+    for (int d = 1; d < (int)kWave; d *= 2) total += __shfl_xor(total, d);
+    const uint32_t e = 4 * (lane % LANES);
+    f32x4 x = {0, 0, 0, 0};
+    const float* from = u.o + (uint64_t)r * dim + e;
+    const uint64_t stride = (uint64_t)dim << p.tile_log2;
+#pragma unroll 4
+    for (uint32_t s0 = 0; s0 < t.splits; s0 += kAtOnce) {
+        const uint32_t s = s0 + lane / LANES;
+        const float by = __shfl(weight, s);
+        if (s < t.splits && e < dim) x += *(const SZ_GLOBAL f32x4*)(from + s * stride) * by;
+    }
+#pragma unroll
+    for (int d = LANES; d < (int)kWave; d *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[i] += __shfl_xor(x[i], d);
+    const float inv = inverse(total);
+    const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
     const uint32_t head = kv * p.group + w.head;
-    if (e < dim)
+    if (lane < LANES && e < dim)
         store_out<4>(a.out, (uint64_t)w.token * a.out.token_stride +
-                                (uint64_t)head * a.out.head_stride + e, x);
+                                (uint64_t)head * a.out.head_stride + e, y);
     if (lane == 0 && a.lse != nullptr)
         a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
 }
 
 template <int DP, bool CAP>
 hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
-    const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads)), block(kThreads);
+    const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads));
+    constexpr uint32_t block = kThreads;
     const Score score = score_of(a);
-    if (p.tile_log2 == 4) k_attend_few<DP, 1><<<grid, block, 0, stream>>>(a, p, score, ws);
-    else if (p.tile_log2 == 7)
+    if (p.tile_log2 == 4) {
+        if (p.wide)
+            k_attend_few<DP, 8, false><<<grid, 2 * block, 0, stream>>>(a, p, score, ws);
+        else if (p.splits == 1)
+            k_attend_few<DP, 4, false><<<grid, block, 0, stream>>>(a, p, score, ws);
+        else
+            k_attend_few<DP, 4, true><<<grid, block, 0, stream>>>(a, p, score, ws);
+    } else if (p.tile_log2 == 7) {
         k_attend_chunk<DP, 1, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
+    }
     if constexpr (DP <= 128) {
-        if (p.tile_log2 == 5) k_attend_few<DP, 2><<<grid, block, 0, stream>>>(a, p, score, ws);
-        else if (p.tile_log2 == 8)
+        if (p.tile_log2 == 8)
             k_attend_chunk<DP, 2, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
     }
     return hipGetLastError();
@@ -1176,20 +1205,24 @@ hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t str
 
 uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                           uint64_t max_len) {
-    const AttendPlan p = plan_attend(q_heads, c, n_seqs, n_tokens, max_len);
-    if (p.splits == 1) return 0;
-    return ((p.units() * c.kv_heads << p.tile_log2) * (c.head_dim + 2) * 4 + 255) / 256 * 256;
+    // without a window: with one there are fewer keys to split, never more
+    const AttendPlan p = plan_attend(q_heads, c, n_seqs, n_tokens, max_len, 0);
+    if (p.bound == 1) return 0;
+    const uint64_t units = (uint64_t)p.tiles * p.bound * c.kv_heads;
+    return ((units << p.tile_log2) * (c.head_dim + 2) * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
     if (a.batch.n_seqs == 0 || a.batch.n_tokens == 0) return hipSuccess;
     const AttendPlan p =
-        plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
+        plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len,
+                    a.window);
     const hipError_t e = a.softcap > 0 ? go<true>(a, p, ws, stream) : go<false>(a, p, ws, stream);
     if (e != hipSuccess || p.splits == 1) return e;
-    const uint32_t pieces = (1u << p.tile_log2) / kWaves;
-    k_attend_join<<<dim3(p.tiles * a.cache.kv_heads * pieces), dim3(kThreads), 0, stream>>>(a, p,
-                                                                                            ws);
+    const dim3 grid(p.tiles * a.cache.kv_heads * ((1u << p.tile_log2) / kWaves)), block(kThreads);
+    if (a.cache.head_dim <= 64) k_attend_join<16><<<grid, block, 0, stream>>>(a, p, ws);
+    else if (a.cache.head_dim <= 128) k_attend_join<32><<<grid, block, 0, stream>>>(a, p, ws);
+    else k_attend_join<64><<<grid, block, 0, stream>>>(a, p, ws);
     return hipGetLastError();
 }
 

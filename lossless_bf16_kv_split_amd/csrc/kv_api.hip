@@ -294,11 +294,11 @@ uint64_t sz_attend_workspace_size(uint64_t q_heads, const sz_kv_cache* cache,
         cache->pages_per_seq > kMaxTokens || cache->page_tokens > 65536)
         return 0;
     const uint64_t most = most_len(*cache);
-    if (max_len > most || !attend_fits(batch->n_seqs, batch->n_tokens, q_heads, cache->kv_heads))
-        return 0;
+    if (!attend_fits(batch->n_seqs, batch->n_tokens, q_heads, cache->kv_heads)) return 0;
     if (batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
     return sz::attend_workspace((uint32_t)q_heads, cache_of(*cache), batch->n_seqs,
-                                batch->n_tokens, max_len == 0 ? most : max_len);
+                                batch->n_tokens,
+                                max_len == 0 || max_len > most ? most : max_len);
 }
 
 sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
@@ -318,8 +318,7 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
         (window != 0 && !causal) || !aligned(d_lse, 4) || !aligned(d_status, 4))
         return SZ_ERR_INVALID_ARGUMENT;
     const uint64_t most = most_len(*cache);
-    if (max_len > most) return SZ_ERR_INVALID_ARGUMENT;
-    if (max_len == 0) max_len = most;
+    if (max_len == 0 || max_len > most) max_len = most;
     if (overlap(d_lse, d_lse == nullptr ? 0 : 4 * n * q->heads, span(*q, n, dim)) ||
         overlap(d_lse, d_lse == nullptr ? 0 : 4 * n * q->heads, span(*out, n, dim)))
         return SZ_ERR_INVALID_ARGUMENT;
