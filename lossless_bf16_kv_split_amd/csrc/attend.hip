@@ -51,104 +51,91 @@ __device__ __forceinline__ bf16x8 words8(uint32_t a, uint32_t b, uint32_t c, uin
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// How a call is cut up.  Tiles: the rows of sequence s for one KV head,
-// tile_rows at a time; the first tile of sequence s has number
-// floor(starts[s] * G / tile_rows) + s, which leaves room for every tile
-// whatever the lengths and needs no sum over the sequences.  Splits: a
-// tile's visible keys, split_len at a time, joined by a second launch where
-// there can be more than one.
+// How a call is cut up.  Tiles: the rows of a sequence for one KV head,
+// tile_rows at a time.  Either each tile is one workgroup's, with all its
+// keys; tile number floor(starts[s] * G / tile_rows) + s is then the first
+// of sequence s, which leaves room for every tile whatever the lengths and
+// needs no sum over the sequences.  Or (shares > 0) the work is shared out:
+// all tiles' keys, in steps of kStep, laid end to end and cut into equal
+// parts, one for each workgroup of a KV head, so that uneven lengths leave
+// no workgroup behind; a tile cut by such a border is joined by a second
+// launch.  Tiles are then numbered without gaps.
 struct AttendPlan {
     uint32_t group;      // G
     uint32_t tile_log2;
-    uint32_t tiles;
-    uint32_t splits;     // most splits of a tile
-    uint32_t split_len;
-    uint32_t bound;      // of splits, whatever the window
-    bool wide;           // few rows, no splits, a CU each: eight waves
-    uint64_t units() const { return (uint64_t)tiles * splits; }
+    uint32_t tiles;      // a bound of the tiles' numbers
+    uint32_t shares;     // workgroups that share it out for a KV head; 0: whole tiles
+    uint32_t least;      // the fewest steps of a share
+    bool wide;           // few rows, whole tiles, a CU each: eight waves
     bool few() const { return tile_log2 == 4; }
 };
 
-constexpr uint32_t kStep = 128;  // split lengths are multiples of this many keys
-// Workgroups that keep 256 CUs busy and even: of the few-row kernel, and of
-// the chunk kernel.
-constexpr uint64_t kFillFew = 4096, kFillChunk = 512;
-// The fewest keys of a split; and the bytes of keys and values that one
-// workgroup reads (at about 50 GB/s, what one CU gets) in the time of the
-// second launch that a split would need.
-constexpr uint64_t kLeastFew = 128, kLeastChunk = 256;
-constexpr uint64_t kWholeBytes = 288 * 1024;
-
-constexpr uint64_t kMaxSplits = 64;
+constexpr uint32_t kStep = 128;  // keys
 constexpr uint64_t kCus = 256;
+// The work is shared out among as many workgroups as the chip holds at once:
+// two a CU, one with 256-element heads.  Whole tiles where there are enough
+// of them to even out, or where a tile's keys and values are few bytes: one
+// workgroup reads them (at about 50 GB/s, what one CU gets) in the time that
+// the second launch would take.
+constexpr uint64_t kManyFew = 4096, kManyTiles = 512;
+constexpr uint64_t kWholeBytes = 288 * 1024;
+// Sharing out looks at every sequence in every workgroup, 64 at a time.
+constexpr uint64_t kShareSeqs = 1024;
+// and counts steps in 32 bits, times workgroups
+constexpr uint64_t kMostSteps = uint64_t{1} << 22;
+constexpr uint32_t kLeastFew = 1, kLeastTiles = 4;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                        uint64_t max_len, uint64_t window) {
     AttendPlan p;
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
-    if (rows <= 16 * n_seqs) p.tile_log2 = 4;
-    else p.tile_log2 = rows > 128 * n_seqs && c.head_dim <= 128 ? 8 : 7;
+    p.tile_log2 = rows <= 16 * n_seqs ? 4 : 7;
+    if (c.head_dim <= 128 && (rows >> 8) * c.kv_heads >= kManyTiles) p.tile_log2 = 8;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     // keys of a tile: a window shows its rows' tokens' own keys and those of
-    // a window before; the first split starts at a multiple of 32 keys
+    // a window before
     uint64_t keys = max_len;
     const uint64_t tokens = ((1u << p.tile_log2) - 1) / p.group + 2;
-    if (window != 0) {
-        if (window < keys && window + tokens < keys) keys = window + tokens;
-        keys += 31;
-    }
-    // workgroups without splits, as far as can be told here: numbers of tiles
-    // are mostly free where sequences have few rows each
+    if (window < keys && window != 0 && window + tokens < keys) keys = window + tokens;
+    // workgroups with whole tiles, as far as can be told here: numbers of
+    // tiles are mostly free where sequences have few rows each
     const uint64_t full = rows >> p.tile_log2;
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
-    const uint64_t fill = p.few() ? kFillFew : kFillChunk;
-    uint64_t splits = (fill + groups - 1) / groups;
-    const uint64_t least = p.few() ? kLeastFew : kLeastChunk;
-    const uint64_t known = keys < max_len ? keys : max_len;
-    const uint64_t most =
-        p.few() && known * c.head_dim * 4 <= kWholeBytes ? 1 : known / least;
-    splits = splits > most ? most : splits;
-    splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
-    p.bound = (uint32_t)splits;
-    const uint64_t len = (keys + splits - 1) / splits;
-    p.split_len = (uint32_t)((len + kStep - 1) / kStep * kStep);
-    p.splits = (uint32_t)((keys + p.split_len - 1) / p.split_len);
-    p.wide = p.tile_log2 == 4 && p.splits == 1 && groups <= kCus && c.head_dim <= 128;
+    const uint64_t resident = c.head_dim > 128 ? kCus : 2 * kCus;
+    const bool whole = p.tile_log2 == 8 || n_seqs > kShareSeqs || c.kv_heads > resident ||
+                       groups >= (p.few() ? kManyFew : kManyTiles) ||
+                       p.tiles * (max_len / kStep + 2) >= kMostSteps ||
+                       keys * c.head_dim * 4 <= kWholeBytes;
+    p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
+    p.least = p.few() ? kLeastFew : kLeastTiles;
+    p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
     return p;
 }
 
-// What a workgroup works on, all uniform.
+// A tile, all uniform.
 struct Tile {
     uint32_t seq;
+    uint32_t number;
     int32_t begin;      // first token of the sequence
     int32_t row0, rows; // rows row0 .. row0 + rows - 1 of the sequence
     int32_t c0;         // position of the sequence's first new token
-    int32_t len;
     int32_t lo, hi;     // keys visible to any row of the tile: lo .. hi - 1
     int32_t all_lo, all_hi;  // keys visible to every row
     int32_t from;       // lo rounded down to a multiple of 32
-    uint32_t splits;    // of this tile, at least 1
 };
 
-__device__ __forceinline__ bool find_tile(const Attend& a, const AttendPlan& p, uint32_t tile,
-                                          Tile& t) {
-    const auto first = [&](uint32_t s) {
-        return (((int64_t)a.batch.starts[s] * p.group) >> p.tile_log2) + s;
-    };
-    t.seq = find_seq(a.batch.n_seqs, tile, first);
-    const Seq q = load_seq(a.batch, t.seq, a.max_len);
-    if (!q.good) return false;
-    const int64_t at = (int64_t)tile - ((((int64_t)q.begin * p.group) >> p.tile_log2) + t.seq);
-    const int64_t row0 = at << p.tile_log2;
-    const int64_t all = (int64_t)(q.end - q.begin) * p.group;
-    if (at < 0 || row0 >= all) return false;
+// The tile of row row0 on, of a sequence that holds it.
+__device__ __forceinline__ Tile make_tile(const Attend& a, const AttendPlan& p, uint32_t seq,
+                                          uint32_t number, const Seq& q, int64_t row0) {
+    Tile t;
+    t.seq = seq;
+    t.number = number;
     t.begin = q.begin;
-    t.len = q.len;
     t.c0 = q.len - (q.end - q.begin);
     // (row numbers fit 32 bits: the host keeps n_tokens * q heads below 2^31)
     t.row0 = (int32_t)row0;
-    const int64_t left = all - row0, most = 1ll << p.tile_log2;
+    const int64_t left = (int64_t)(q.end - q.begin) * p.group - row0, most = 1ll << p.tile_log2;
     t.rows = (int32_t)(left < most ? left : most);
     t.lo = t.all_lo = 0;
     t.hi = t.all_hi = q.len;
@@ -163,9 +150,215 @@ __device__ __forceinline__ bool find_tile(const Attend& a, const AttendPlan& p, 
         }
     }
     t.from = t.lo & ~31;
-    t.splits = t.hi > t.lo ? (uint32_t)(t.hi - t.from + p.split_len - 1) / p.split_len : 1;
+    return t;
+}
+
+// Whole tiles: the tile of a number, if there is one.
+__device__ __forceinline__ bool find_tile(const Attend& a, const AttendPlan& p, uint32_t tile,
+                                          Tile& t) {
+    const auto first = [&](uint32_t s) {
+        return (((int64_t)a.batch.starts[s] * p.group) >> p.tile_log2) + s;
+    };
+    const uint32_t s = find_seq(a.batch.n_seqs, tile, first);
+    const Seq q = load_seq(a.batch, s, a.max_len);
+    if (!q.good) return false;
+    const int64_t at = (int64_t)tile - ((((int64_t)q.begin * p.group) >> p.tile_log2) + s);
+    const int64_t row0 = at << p.tile_log2;
+    if (at < 0 || row0 >= (int64_t)(q.end - q.begin) * p.group) return false;
+    t = make_tile(a, p, s, tile, q, row0);
     return true;
 }
+
+// Work shared out: worker i takes steps i * quota .. (i + 1) * quota - 1 of
+// all tiles' steps laid end to end.  Every wave adds up the sequences' steps
+// for itself: lane i takes `each` consecutive sequences (one, up to 64 of
+// them), a scan over the lanes gives where each lane's begin, and a second
+// one, over the sequences of one lane, where each of those does.  (The host
+// keeps the sum below kMostSteps.)
+struct Shares {
+    struct Load {
+        Seq q;
+        uint32_t tiles;   // of the sequence, 0 where it is faulty or has no rows
+        uint32_t steps;   // of each of its tiles, at least 1
+        int32_t from;     // the key of step 0
+    };
+    uint32_t each;
+    uint32_t total;       // steps
+    uint32_t quota;
+    // this lane's sequences: steps and tiles before them, and with them
+    uint32_t steps0, steps1, tiles0, tiles1;
+    Load own;             // each == 1: the lane's sequence
+
+    static __device__ __forceinline__ Load load(const Attend& a, const AttendPlan& p, uint32_t s) {
+        Load x{};
+        if (s >= a.batch.n_seqs) return x;
+        x.q.begin = a.batch.starts[s];
+        x.q.end = a.batch.starts[s + 1];
+        x.q.len = a.batch.lens[s];
+        x.q.good = x.q.begin >= 0 && x.q.begin < x.q.end &&
+                   x.q.end <= (int64_t)a.batch.n_tokens && x.q.len >= 0 && x.q.len <= a.max_len;
+        if (!x.q.good) return x;
+        const int64_t rows = (int64_t)(x.q.end - x.q.begin) * p.group;
+        x.tiles = (uint32_t)((rows + (1 << p.tile_log2) - 1) >> p.tile_log2);
+        const int32_t c0 = x.q.len - (x.q.end - x.q.begin);
+        if (a.causal && a.window != 0 && (int64_t)c0 + 1 > (int64_t)a.window)
+            x.from = (c0 + 1 - (int32_t)a.window) & ~31;
+        x.steps = (uint32_t)(x.q.len - x.from + kStep - 1) / kStep;
+        x.steps = x.steps == 0 ? 1 : x.steps;
+        return x;
+    }
+
+    // running sums over the lanes (rows of 16 lanes, then across the rows)
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ uint32_t plus(uint32_t x) {
+        return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+    }
+    static __device__ __forceinline__ uint32_t scan(uint32_t x) {
+        x = plus<0x111, 0xF>(x);  // row_shr:1
+        x = plus<0x112, 0xF>(x);
+        x = plus<0x114, 0xF>(x);
+        x = plus<0x118, 0xF>(x);
+        x = plus<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+        x = plus<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+        return x;
+    }
+
+    static __device__ __forceinline__ uint32_t from_lane(uint32_t x, uint32_t lane) {
+        return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+    }
+
+    __device__ __forceinline__ Shares(const Attend& a, const AttendPlan& p) {
+        const uint32_t lane = threadIdx.x % kWave;
+        each = (a.batch.n_seqs + kWave - 1) / kWave;
+        uint32_t steps = 0, tiles = 0;
+        if (each == 1) {
+            own = load(a, p, lane);
+            steps = own.tiles * own.steps;
+            tiles = own.tiles;
+        } else {
+            for (uint32_t i = 0; i < each; i++) {
+                const Load x = load(a, p, lane * each + i);
+                steps += x.tiles * x.steps;
+                tiles += x.tiles;
+            }
+        }
+        steps1 = scan(steps);
+        tiles1 = scan(tiles);
+        steps0 = steps1 - steps;
+        tiles0 = tiles1 - tiles;
+        total = from_lane(steps1, kWave - 1);
+        quota = (total + p.shares - 1) / p.shares;
+        quota = quota < p.least ? p.least : quota;
+    }
+
+    // A sequence: by one of its steps, or one of its tiles
+    struct Found {
+        uint32_t seq;
+        Load x;
+        uint32_t steps0, tiles0;  // steps and tiles before the sequence's
+    };
+    __device__ __forceinline__ Found find(const Attend& a, const AttendPlan& p, bool by_tile,
+                                          uint32_t number) const {
+        const auto first_past = [&](uint32_t steps, uint32_t tiles) {
+            return (uint32_t)__builtin_ctzll(__ballot((by_tile ? tiles : steps) > number) |
+                                             1ull << (kWave - 1));
+        };
+        uint32_t lane = first_past(steps1, tiles1);
+        Found f;
+        f.seq = lane;
+        f.steps0 = from_lane(steps0, lane);
+        f.tiles0 = from_lane(tiles0, lane);
+        Load x = own;
+        if (each > 1) {
+            const uint32_t mine = threadIdx.x % kWave, first = lane * each;
+            x = load(a, p, mine < each ? first + mine : a.batch.n_seqs);
+            const uint32_t steps = x.tiles * x.steps;
+            const uint32_t s1 = scan(steps) + f.steps0, t1 = scan(x.tiles) + f.tiles0;
+            lane = first_past(s1, t1);
+            f.seq = first + lane;
+            f.steps0 = from_lane(s1 - steps, lane);
+            f.tiles0 = from_lane(t1 - x.tiles, lane);
+        }
+        f.x.q.begin = (int32_t)from_lane((uint32_t)x.q.begin, lane);
+        f.x.q.end = (int32_t)from_lane((uint32_t)x.q.end, lane);
+        f.x.q.len = (int32_t)from_lane((uint32_t)x.q.len, lane);
+        f.x.q.good = true;
+        f.x.tiles = from_lane(x.tiles, lane);
+        f.x.steps = from_lane(x.steps, lane);
+        f.x.from = (int32_t)from_lane((uint32_t)x.from, lane);
+        return f;
+    }
+};
+
+// What a workgroup works on at a time: a tile and a range of its keys, first
+// .. last - 1 (first a multiple of 32, last - first one of kStep unless last
+// is the tile's last key's; none where last <= first).
+struct Part {
+    Tile t;
+    int32_t first, last;
+    bool alone;      // the tile's only part
+    uint32_t slot;   // of the results otherwise
+};
+
+// A workgroup's parts, one after the other.  Shared out, worker i's part of
+// tile T has slot i + T: both only grow, so no two parts have the same one.
+template <bool SHARED>
+struct Walk;
+template <>
+struct Walk<false> {
+    __device__ __forceinline__ Walk(const Attend&, const AttendPlan&) {}
+    __device__ __forceinline__ bool first(const Attend& a, const AttendPlan& p, uint32_t index,
+                                          Part& part) {
+        if (!find_tile(a, p, index, part.t)) return false;
+        part.first = part.t.from;
+        part.last = part.t.hi;
+        part.alone = true;
+        part.slot = 0;
+        return true;
+    }
+    __device__ __forceinline__ bool next(const Attend&, const AttendPlan&, uint32_t, Part&) {
+        return false;
+    }
+};
+template <>
+struct Walk<true> {
+    uint32_t step, end;
+    __device__ __forceinline__ Walk(const Attend&, const AttendPlan&) {}
+    __device__ __forceinline__ bool first(const Attend& a, const AttendPlan& p, uint32_t index,
+                                          Part& part) {
+        const Shares shares(a, p);
+        step = index * shares.quota;
+        end = step + shares.quota < shares.total ? step + shares.quota : shares.total;
+        if (step >= end) return false;
+        take(shares, a, p, index, part);
+        return true;
+    }
+    // (the sums are made anew: they would hold registers through the part)
+    __device__ __forceinline__ bool next(const Attend& a, const AttendPlan& p, uint32_t index,
+                                         Part& part) {
+        if (step >= end) return false;
+        take(Shares(a, p), a, p, index, part);
+        return true;
+    }
+    __device__ __forceinline__ void take(const Shares& shares, const Attend& a,
+                                         const AttendPlan& p, uint32_t index, Part& part) {
+        const Shares::Found f = shares.find(a, p, false, step);
+        const uint32_t at = (step - f.steps0) / f.x.steps;
+        const uint32_t base = f.steps0 + at * f.x.steps, stop = base + f.x.steps;
+        const uint32_t upto = stop < end ? stop : end;
+        part.t = make_tile(a, p, f.seq, f.tiles0 + at, f.x.q, (int64_t)at << p.tile_log2);
+        // (a part begins at one of the steps, even where a window shows the
+        // tile's rows fewer keys than the sequence's first one: whole steps
+        // up to the part's end, which masks nothing)
+        const uint32_t skip = (uint32_t)(part.t.from - f.x.from) / kStep;
+        part.first = f.x.from + (int32_t)((step - base > skip ? step - base : skip) * kStep);
+        const int32_t last = f.x.from + (int32_t)((upto - base) * kStep);
+        part.last = last < part.t.hi ? last : part.t.hi;
+        part.alone = step == base && upto == stop;
+        part.slot = index + part.t.number;
+        step = upto;
+    }
+};
 
 // Keys that a row sees: low .. high - 1.  Rows past the tile's end are given
 // all of the tile's (nothing of them is stored).
@@ -240,6 +433,14 @@ __device__ __forceinline__ float unmark(float marks) {
     return x;
 }
 
+// A page's address from a table, through the scalar cache: the tables do not
+// change while a kernel runs, which the compiler cannot tell by itself in
+// kernels that store inside a loop (a vector load there would wait for the
+// loads of keys and values before it).
+__device__ __forceinline__ uint64_t page_address(const uint64_t* table, uint64_t entry) {
+    return *(const __attribute__((address_space(4))) uint64_t*)(uintptr_t)(table + entry);
+}
+
 // The resource of a block of 16 keys' rows in a page: rows from `skip` on
 // (a page that no visible key lies in, or a bad page address: none) up to
 // `rows`.  Offsets past the end read as zeros, so keys past the last visible
@@ -255,18 +456,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const Cache& c, uin
                                              kBufferFlags);
 }
 
-// Partial results of the splits: for unit (tile, KV head, split), tile_rows
-// rows of head_dim sums and of (maximum, sum of weights).
+// Results of a part: for (KV head, slot), tile_rows rows of head_dim sums and
+// of (maximum, sum of weights).
 struct Partial {
     float* o;
     float* ml;
 };
+__host__ __device__ inline uint64_t partial_slots(const AttendPlan& p) {
+    return (uint64_t)p.tiles + p.shares;
+}
 __device__ __forceinline__ Partial partial_of(uint8_t* ws, const Attend& a, const AttendPlan& p,
-                                              uint32_t tile, uint32_t kv, uint32_t split) {
-    const uint64_t units = (uint64_t)p.tiles * a.cache.kv_heads * p.splits;
-    const uint64_t unit = ((uint64_t)tile * a.cache.kv_heads + kv) * p.splits + split;
+                                              uint32_t kv, uint32_t slot) {
+    const uint64_t slots = partial_slots(p);
+    const uint64_t unit = kv * slots + slot;
     float* f = reinterpret_cast<float*>(ws);
-    return Partial{f + 2 * (units << p.tile_log2) + (unit << p.tile_log2) * a.cache.head_dim,
+    return Partial{f + 2 * (a.cache.kv_heads * slots << p.tile_log2) +
+                       (unit << p.tile_log2) * a.cache.head_dim,
                    f + 2 * (unit << p.tile_log2)};
 }
 
@@ -323,25 +528,28 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 //    elements 8 n + i as its rows.
 //  - O^T's result: lane (query n, h) then has, for r < 4, elements
 //    32 h + 8 r + i: 32 consecutive ones.
-template <int DP, int WAVES, bool STREAM>
+template <int DP, int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void k_attend_few(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     constexpr int kStride = 32 * WAVES;    // keys that the workgroup takes at a time
-    constexpr int kAux = STREAM ? 2 : 0;   // (the loads' nt bit)
+    constexpr int kAux = SHARED ? 2 : 0;   // the loads' nt bit
     constexpr int kSlices = DP / 32;       // of K, 32 elements each
     constexpr int kVec = DP < 128 ? 4 : 8; // elements of a V row per load
     constexpr int kVLoads = DP / (16 * kVec);
     constexpr int kProducts = DP / 16;     // of 16 elements of the output
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t split = blockIdx.x % p.splits;
-    const uint32_t rest = blockIdx.x / p.splits;
-    const uint32_t kv = rest % a.cache.kv_heads, tile = rest / a.cache.kv_heads;
-    Tile t;
-    if (!find_tile(a, p, tile, t) || split >= t.splits) return;
-    const int32_t first = t.from + (int32_t)(split * p.split_len);
-    const int32_t last = t.splits == 1 || split == t.splits - 1 ? t.hi
-                                                                : first + (int32_t)p.split_len;
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
+    constexpr int kPitch = DP + 4;
+    __shared__ float join_o[WAVES][16][kPitch];
+    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
+    const uint32_t index = blockIdx.x / a.cache.kv_heads;
+    Walk<SHARED> walk(a, p);
+    Part part;
+    if (!walk.first(a, p, index, part)) return;
+    do {
+    const Tile& t = part.t;
+    const int32_t first = part.first, last = part.last;
 
     // the rows, their queries (slices of 32 elements, zeros past head_dim)
     const uint32_t dim = a.cache.head_dim;
@@ -387,8 +595,8 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
             uint64_t k_page = 0, v_page = 0;
             if (jb < last && jb + 16 > t.lo) {
                 const uint64_t entry = table_row + ((uint32_t)jb >> a.cache.page_log2);
-                k_page = a.cache.k_pages[entry];
-                v_page = a.cache.v_pages[entry];
+                k_page = page_address(a.cache.k_pages, entry);
+                v_page = page_address(a.cache.v_pages, entry);
             }
             const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
             const auto kr = block_rows(a.cache, k_page, slot, kv, last - jb);
@@ -543,9 +751,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
     }
 
     // join the waves: row by row in LDS
-    constexpr int kPitch = DP + 4;
-    __shared__ float join_o[WAVES][16][kPitch];
-    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
+    if (SHARED) __syncthreads();  // (the part before has been read)
     constexpr int kRun = 4 * kVec;  // consecutive elements of a lane's result, per 16 kVec
     {
         float sum = l;
@@ -580,7 +786,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
                 for (int k = 0; k < kPer; k++) x[k] = fmaf(join_o[i][r][e + k], keep, x[k]);
             }
             const uint32_t head = kv * p.group + w.head;
-            if (t.splits == 1) {
+            if (!SHARED || part.alone) {
                 const float inv = inverse(total);
 #pragma unroll
                 for (int k = 0; k < kPer; k++) x[k] *= inv;
@@ -597,7 +803,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
                 if (e == 0 && a.lse != nullptr)
                     a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
             } else {
-                const Partial u = partial_of(ws, a, p, tile, kv, split);
+                const Partial u = partial_of(ws, a, p, kv, part.slot);
 #pragma unroll
                 for (int k = 0; k < kPer; k += 4)
                     if (e + k < dim)
@@ -613,6 +819,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
             }
         }
     }
+    } while (walk.next(a, p, index, part));
 }
 
 // ---- chunks: a part of a prompt, or all of it -----------------------------
@@ -659,7 +866,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                  : "memory");
 }
 
-template <int DP, int QB, bool CAP>
+template <int DP, int QB, bool CAP, bool SHARED>
 __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     constexpr int kKeys = 64;
@@ -671,14 +878,14 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 
     const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
-    const uint32_t rest = blockIdx.x / a.cache.kv_heads;
-    // the last tiles of a prompt see the most keys: they go first
-    const uint32_t split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits;
-    Tile t;
-    if (!find_tile(a, p, tile, t) || split >= t.splits) return;
-    const int32_t first = t.from + (int32_t)(split * p.split_len);
-    const int32_t last = split == t.splits - 1 ? t.hi : first + (int32_t)p.split_len;
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
+    // whole tiles: the last ones of a prompt see the most keys and go first
+    Walk<SHARED> walk(a, p);
+    Part part;
+    if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
+    do {
+    const Tile& t = part.t;
+    const int32_t first = part.first, last = part.last;
 
     const uint32_t dim = a.cache.head_dim;
     bf16x8 q[QB][kSlices];
@@ -1028,6 +1235,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     in0 = (in0 + 1) & ~1;  // (even, so that the pipeline's buffers are constants)
     if (in0 > in1) in0 = in1;
     in1 -= (in1 - in0) & 1;
+    if (SHARED) arrived();  // (every wave is done with the part before)
     if (steps > 0) {
         fetch_k(first, 0);
         fetch_v(first, 0);
@@ -1080,7 +1288,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
         const float total = l[b] + __shfl_xor(l[b], 32);
         if (!w.on) continue;
         const uint32_t head = kv * p.group + w.head;
-        if (t.splits == 1) {
+        if (!SHARED || part.alone) {
             const float inv = inverse(total);
             const uint64_t at = (uint64_t)w.token * a.out.token_stride +
                                 (uint64_t)head * a.out.head_stride;
@@ -1096,7 +1304,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             if (h == 0 && a.lse != nullptr)
                 a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(m[b], total);
         } else {
-            const Partial u = partial_of(ws, a, p, tile, kv, split);
+            const Partial u = partial_of(ws, a, p, kv, part.slot);
 #pragma unroll
             for (int d = 0; d < kParts; d++)
 #pragma unroll
@@ -1115,11 +1323,13 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             }
         }
     }
+    } while (walk.next(a, p, index, part));
 }
 
-// Joins a tile's splits (at most kMaxSplits, one per lane): one wave per row.
-// LANES lanes take four elements each of one split's sums, so that a wave
-// reads 64 / LANES splits at a time, with nothing to wait for between them.
+// Joins the parts of the tiles that were cut: one wave per row.  64 parts at
+// a time, a lane holds one's maximum and sum; LANES lanes take four elements
+// each of one's sums, so that a wave reads 64 / LANES of them at a time, with
+// nothing to wait for between them.
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
     constexpr uint32_t kAtOnce = kWave / LANES;
@@ -1129,33 +1339,55 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     const uint32_t kv = blockIdx.x % a.cache.kv_heads;
     const uint32_t rest = blockIdx.x / a.cache.kv_heads;
     const int32_t r = (int32_t)(rest % pieces * kWaves + wave);
-    const uint32_t tile = rest / pieces;
-    Tile t;
-    if (!find_tile(a, p, tile, t) || t.splits == 1 || r >= t.rows) return;
+    const uint32_t number = rest / pieces;
+    const Shares shares(a, p);
+    if (number >= Shares::from_lane(shares.tiles1, kWave - 1)) return;
+    const Shares::Found f = shares.find(a, p, true, number);
+    const uint32_t at = number - f.tiles0;
+    const uint32_t step = f.steps0 + at * f.x.steps;
+    const uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
+    const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
+    if (from == upto || r >= t.rows) return;
     const Row w = find_row(a, p, t, r);
     const uint32_t dim = a.cache.head_dim;
-    const Partial u = partial_of(ws, a, p, tile, kv, 0);
-    float top = kNoKey, total = 0;
-    if (lane < t.splits) {
-        top = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
-        total = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
-    }
-    const float mine = top;
-#pragma unroll
-    for (int d = 1; d < (int)kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    const float weight = __builtin_amdgcn_exp2f(mine - top);
-    total *= weight;
-#pragma unroll
-    for (int d = 1; d < (int)kWave; d *= 2) total += __shfl_xor(total, d);
     const uint32_t e = 4 * (lane % LANES);
+    float top = kNoKey, total = 0;
     f32x4 x = {0, 0, 0, 0};
-    const float* from = u.o + (uint64_t)r * dim + e;
-    const uint64_t stride = (uint64_t)dim << p.tile_log2;
-#pragma unroll 4
-    for (uint32_t s0 = 0; s0 < t.splits; s0 += kAtOnce) {
-        const uint32_t s = s0 + lane / LANES;
-        const float by = __shfl(weight, s);
-        if (s < t.splits && e < dim) x += *(const SZ_GLOBAL f32x4*)(from + s * stride) * by;
+    for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
+        const uint32_t parts = upto - i0 + 1 < kWave ? upto - i0 + 1 : kWave;
+        const Partial u = partial_of(ws, a, p, kv, i0 + number);
+        float m = kNoKey, l = 0;
+        if (lane < parts) {
+            m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
+            l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
+        }
+        float most = fmaxf(m, top);
+#pragma unroll
+        for (int d = 1; d < (int)kWave; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+        const float weight = __builtin_amdgcn_exp2f(m - most);
+        const float keep = __builtin_amdgcn_exp2f(top - most);
+        top = most;
+        l *= weight;
+#pragma unroll
+        for (int d = 1; d < (int)kWave; d *= 2) l += __shfl_xor(l, d);
+        total = total * keep + l;
+        x *= keep;
+        const float* o = u.o + (uint64_t)r * dim + e;
+        const uint64_t stride = (uint64_t)dim << p.tile_log2;
+        for (uint32_t s0 = 0; s0 < parts; s0 += 4 * kAtOnce) {
+            f32x4 v[4];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) {
+                const uint32_t s = s0 + k * kAtOnce + lane / LANES;
+                v[k] = f32x4{0, 0, 0, 0};
+                if (s < parts && e < dim) v[k] = *(const SZ_GLOBAL f32x4*)(o + s * stride);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) {
+                const float by = __shfl(weight, (s0 + k * kAtOnce + lane / LANES) % kWave);
+                x += v[k] * by;
+            }
+        }
     }
 #pragma unroll
     for (int d = LANES; d < (int)kWave; d *= 2)
@@ -1173,23 +1405,29 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
 
 template <int DP, bool CAP>
 hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
-    const dim3 grid((uint32_t)(p.units() * a.cache.kv_heads));
+    const dim3 grid((p.shares != 0 ? p.shares : p.tiles) * a.cache.kv_heads);
     constexpr uint32_t block = kThreads;
     const Score score = score_of(a);
-    if (p.tile_log2 == 4) {
-        if (p.wide)
-            k_attend_few<DP, 8, false><<<grid, 2 * block, 0, stream>>>(a, p, score, ws);
-        else if (p.splits == 1)
-            k_attend_few<DP, 4, false><<<grid, block, 0, stream>>>(a, p, score, ws);
-        else
+    if (p.few()) {
+        if (p.shares != 0)
             k_attend_few<DP, 4, true><<<grid, block, 0, stream>>>(a, p, score, ws);
-    } else if (p.tile_log2 == 7) {
-        k_attend_chunk<DP, 1, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
+        else if (DP <= 128 && p.wide)
+            k_attend_few<DP <= 128 ? DP : 128, 8, false>
+                <<<grid, 2 * block, 0, stream>>>(a, p, score, ws);
+        else
+            k_attend_few<DP, 4, false><<<grid, block, 0, stream>>>(a, p, score, ws);
+        return hipGetLastError();
     }
     if constexpr (DP <= 128) {
-        if (p.tile_log2 == 8)
-            k_attend_chunk<DP, 2, CAP><<<grid, block, 0, stream>>>(a, p, score, ws);
+        if (p.tile_log2 == 8) {
+            k_attend_chunk<DP, 2, CAP, false><<<grid, block, 0, stream>>>(a, p, score, ws);
+            return hipGetLastError();
+        }
     }
+    if (p.shares != 0)
+        k_attend_chunk<DP, 1, CAP, true><<<grid, block, 0, stream>>>(a, p, score, ws);
+    else
+        k_attend_chunk<DP, 1, CAP, false><<<grid, block, 0, stream>>>(a, p, score, ws);
     return hipGetLastError();
 }
 
@@ -1205,11 +1443,12 @@ hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t str
 
 uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                           uint64_t max_len) {
-    // without a window: with one there are fewer keys to split, never more
+    // without a window: with one the work may stay in whole tiles, and is
+    // shared out the same otherwise
     const AttendPlan p = plan_attend(q_heads, c, n_seqs, n_tokens, max_len, 0);
-    if (p.bound == 1) return 0;
-    const uint64_t units = (uint64_t)p.tiles * p.bound * c.kv_heads;
-    return ((units << p.tile_log2) * (c.head_dim + 2) * 4 + 255) / 256 * 256;
+    if (p.shares == 0) return 0;
+    const uint64_t rows = c.kv_heads * partial_slots(p) << p.tile_log2;
+    return (rows * (c.head_dim + 2) * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
@@ -1218,7 +1457,7 @@ hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
         plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len,
                     a.window);
     const hipError_t e = a.softcap > 0 ? go<true>(a, p, ws, stream) : go<false>(a, p, ws, stream);
-    if (e != hipSuccess || p.splits == 1) return e;
+    if (e != hipSuccess || p.shares == 0) return e;
     const dim3 grid(p.tiles * a.cache.kv_heads * ((1u << p.tile_log2) / kWaves)), block(kThreads);
     if (a.cache.head_dim <= 64) k_attend_join<16><<<grid, block, 0, stream>>>(a, p, ws);
     else if (a.cache.head_dim <= 128) k_attend_join<32><<<grid, block, 0, stream>>>(a, p, ws);

@@ -176,6 +176,26 @@ def test_attend_long(torch, sz, pairs, max_len, shape):
     check_attend(torch, sz, S, f"long {pairs} {shape}", max_len=max_len)
 
 
+@pytest.mark.parametrize("window", [600, 3000])
+@pytest.mark.parametrize("shape", [(8, 1, 128, 64), (8, 1, 64, 16), (4, 1, 256, 16)], ids=str)
+def test_attend_shared_out_under_a_window(torch, sz, shape, window):
+    """Several tiles of one sequence whose keys begin at different places,
+    cut into parts."""
+    S = Setup(torch, sz, [(130, 5000), (40, 900), (1, 4000), (7, 4100)], *shape, seed=15)
+    check_attend(torch, sz, S, f"shared out {shape} {window}", window=window)
+    S = Setup(torch, sz, [(1, 700), (3, 5000), (2, 2222)], *shape, seed=16)
+    check_attend(torch, sz, S, f"shared out, few rows {shape} {window}", window=window)
+
+
+@pytest.mark.parametrize("n", [65, 130, 700, 1025])
+def test_attend_many_sequences(torch, sz, n):
+    """More sequences than lanes of a wave, empty ones among them."""
+    pairs = [((i * 7) % 3 and 1 + (i % 11 == 5), 2 + (i * 37) % 90) for i in range(n)]
+    pairs[n // 2] = (2, 4000)
+    S = Setup(torch, sz, pairs, 4, 1, 64, 16, seed=17, behind=1)
+    check_attend(torch, sz, S, f"many {n}")
+
+
 def test_attend_f32_output_and_large_scores(torch, sz):
     S = Setup(torch, sz, [(1, 300), (9, 500)], 16, 4, 128, 16, seed=6)
     check_attend(torch, sz, S, "f32 out", out_type=torch.float32)
