@@ -91,7 +91,6 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
     p.tile_log2 = rows <= 16 * n_seqs ? 4 : 7;
-    if (c.head_dim <= 128 && (rows >> 8) * c.kv_heads >= kManyTiles) p.tile_log2 = 8;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     // keys of a tile: a window shows its rows' tokens' own keys and those of
     // a window before
@@ -103,7 +102,7 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     const uint64_t full = rows >> p.tile_log2;
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
     const uint64_t resident = c.head_dim > 128 ? kCus : 2 * kCus;
-    const bool whole = p.tile_log2 == 8 || n_seqs > kShareSeqs || c.kv_heads > resident ||
+    const bool whole = n_seqs > kShareSeqs || c.kv_heads > resident ||
                        groups >= (p.few() ? kManyFew : kManyTiles) ||
                        p.tiles * (max_len / kStep + 2) >= kMostSteps ||
                        keys * c.head_dim * 4 <= kWholeBytes;
@@ -874,7 +873,8 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     constexpr uint32_t kBuffer = kKeys * kRow;    // K or V of a step
     constexpr int kLoads = DP / 32;               // per wave, of K or V
     constexpr int kSlices = DP / 16, kParts = DP / 32;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBuffer];  // K, K, V, V
+    // K of two steps, V of three
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kBuffer];
 
     const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -938,46 +938,46 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
                    ? pages[table_row + ((uint32_t)jb >> a.cache.page_log2)]
                    : 0;
     };
-    // K (which = 0) or V (1) of the step at j to a buffer
-    const auto fetch = [&](uint64_t page, const uint32_t (&off)[kLoads], uint32_t which, int32_t j,
+    // K or V of the step at j to a buffer (V's are 2, 3 and 4)
+    const auto fetch = [&](uint64_t page, const uint32_t (&off)[kLoads], int32_t j,
                            uint32_t buffer) {
         const int32_t jb = j + 16 * (int32_t)wave;
         const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
         const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(page >> 32))
                                 << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)page);
         const auto rows = block_rows(a.cache, at, slot, kv, last - jb);
-        const uint32_t to = lds0 + (2 * which + buffer) * kBuffer + wave * 16 * kRow;
+        const uint32_t to = lds0 + buffer * kBuffer + wave * 16 * kRow;
 #pragma unroll
         for (int i = 0; i < kLoads; i++) load_to_lds(rows, off[i], to + 1024 * i);
     };
     uint64_t next_k = page_at(a.cache.k_pages, first), next_v = page_at(a.cache.v_pages, first);
-    const auto fetch_k = [&](int32_t j, uint32_t buffer) { fetch(next_k, k_off, 0, j, buffer); };
-    const auto fetch_v = [&](int32_t j, uint32_t buffer) { fetch(next_v, v_off, 1, j, buffer); };
-    const auto look_up = [&](int32_t k, int32_t v) {
-        next_k = page_at(a.cache.k_pages, k);
-        next_v = page_at(a.cache.v_pages, v);
+    const auto fetch_step = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer) {
+        fetch(next_k, k_off, j, k_buffer);
+        fetch(next_v, v_off, j, 2 + v_buffer);
+        next_k = page_at(a.cache.k_pages, j + kKeys);
+        next_v = page_at(a.cache.v_pages, j + kKeys);
     };
 
-    // LDS addresses of this lane's reads, before the buffer's
-    uint32_t k_at[kSlices], v_at[kParts];
-#pragma unroll
-    for (int s = 0; s < kSlices; s++) k_at[s] = n * kRow + ((2 * s + h) ^ k_mix<DP>(n)) * 16;
-    {
-        const uint32_t key = lane % 16 / 4, piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
-#pragma unroll
-        for (int d = 0; d < kParts; d++)
-            v_at[d] = (4 * h + key) * kRow + ((4 * d + piece) ^ v_mix<DP>(key)) * 16 + lane % 2 * 8;
-    }
-    const auto keys_at = [&](uint32_t buffer, int b, int s) {
-        return *(const SZ_LDS bf16x8*)(uintptr_t)(lds0 + buffer * kBuffer + 32 * b * kRow + k_at[s]);
+    // LDS addresses of this lane's reads.  Slice s of K is at its first
+    // slice's address with 32 s exclusive-or-ed in, part d of V at the first
+    // part's with 64 d (the permutations only touch bits that a row's start
+    // has as zeros).
+    const uint32_t k_lane = lds0 + n * kRow + (h ^ k_mix<DP>(n)) * 16;
+    const uint32_t v_key = lane % 16 / 4;
+    const uint32_t v_lane = lds0 + 2 * kBuffer + (4 * h + v_key) * kRow +
+                            ((2 * (lane / 16 % 2) + lane % 4 / 2) ^ v_mix<DP>(v_key)) * 16 +
+                            lane % 2 * 8;
+    // K of 32 keys (block of a buffer) at `at`, V of 16 keys
+    const auto keys_at = [&](uint32_t at, int s) {
+        return *(const SZ_LDS bf16x8*)(uintptr_t)(at ^ 32 * s);
     };
-    const auto value_words = [&](uint32_t buffer, int t16, int d) {
-        const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * t16 * kRow + v_at[d];
+    const auto value_words = [&](uint32_t at, int t16, int d) {
+        const uint32_t from = (at ^ 64 * d) + 16 * t16 * kRow;
         const u32x2 x = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SZ_LDS s16x4*)(uintptr_t)at));
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SZ_LDS s16x4*)(uintptr_t)from));
         const u32x2 y = __builtin_bit_cast(
             u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                       (SZ_LDS s16x4*)(uintptr_t)(at + 8 * kRow)));
+                       (SZ_LDS s16x4*)(uintptr_t)(from + 8 * kRow)));
         return u32x4{x.x, x.y, y.x, y.y};
     };
 
@@ -995,11 +995,10 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 
     const float by = CAP ? 1.0f : score.by;
     const auto scored = [&](float x) { return CAP ? capped(score, x) : x; };
-    // follow(top): the running maximum and what hangs on it, where a score
-    // of block b (its largest in this lane: top, a multiple of 1 / by) is
-    // too far above it
+    // The running maximum of block b of 32 rows, and what hangs on it, where
+    // a score of it (its largest in this lane: top, in powers of two) is too
+    // far above it
     const auto follow = [&](int b, float top) {
-        top = scored(top) * by;
         if (__ballot(top > m[b] + kLag) == 0) return;
         top = fmaxf(top, __shfl_xor(top, 32));
         top = fmaxf(top, m[b]);
@@ -1013,18 +1012,31 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
     };
 
     // A step at the rim of what the wave's rows see, one block of 32 rows
-    // at a time.
-    const auto rim = [&](int32_t j, uint32_t buffer) {
+    // at a time.  An infinity or a NaN among its values must reach the rows
+    // that see it and no other, and 0 times it would be NaN: the product then
+    // reads a copy of the values without them (in the buffer that no step is
+    // using; every wave makes all of it, so none waits for another), and they
+    // are added afterwards, key by key.
+    const auto rim = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer, uint32_t spare) {
+        const uint32_t ka = k_lane + k_buffer * kBuffer;
+        const uint32_t values = lds0 + (2 + v_buffer) * kBuffer;
         bool odd = false;
-        {
-            const uint32_t at = lds0 + (2 + buffer) * kBuffer + 16 * lane;
-#pragma unroll
-            for (int i = 0; i < (int)(kBuffer / 1024); i++) {
-                const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(at + 1024 * i);
-                odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
-            }
-            odd = __ballot(odd) != 0;
+#pragma unroll 4
+        for (int i = 0; i < (int)(kBuffer / 1024); i++) {
+            const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(values + 1024 * i + 16 * lane);
+            odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
         }
+        odd = __ballot(odd) != 0;
+        if (odd) {
+#pragma unroll 1
+            for (int i = 0; i < (int)(kBuffer / 1024); i++) {
+                const uint32_t at = 1024 * i + 16 * lane;
+                const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(values + at);
+                *(SZ_LDS u32x4*)(uintptr_t)(lds0 + (2 + spare) * kBuffer + at) =
+                    u32x4{plain_pair(x.x), plain_pair(x.y), plain_pair(x.z), plain_pair(x.w)};
+            }
+        }
+        const uint32_t va = v_lane + (odd ? spare : v_buffer) * kBuffer;
 #pragma unroll
         for (int b = 0; b < QB; b++) {
             f32x16 s[2];
@@ -1033,9 +1045,13 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 #pragma unroll
                 for (int i = 0; i < 16; i++) s[k][i] = 0;
 #pragma unroll
-                for (int c = 0; c < kSlices; c++)
-                    s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(keys_at(buffer, k, c), q[b][c],
-                                                                   s[k], 0, 0, 0);
+                for (int c = 0; c < kSlices; c++) {
+                    s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        keys_at(ka + 32 * k * kRow, c), q[b][c], s[k], 0, 0, 0);
+                    // (or all the operands are read at once, into registers
+                    // that the other loop misses)
+                    if (c % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
             }
             float top = -INFINITY;
 #pragma unroll
@@ -1046,18 +1062,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
                     s[k][i] = key < low[b] || key >= high[b] ? -INFINITY : scored(s[k][i]);
                     top = fmaxf(top, s[k][i]);
                 }
-            top *= by;
-            if (__ballot(top > m[b] + kLag) != 0) {
-                top = fmaxf(top, __shfl_xor(top, 32));
-                top = fmaxf(top, m[b]);
-                const float keep = __builtin_amdgcn_exp2f(m[b] - top);
-                m[b] = top;
-                l[b] *= keep;
-#pragma unroll
-                for (int d = 0; d < kParts; d++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) o[b][d][i] *= keep;
-            }
+            follow(b, top * by);
             uint32_t weights[16];
 #pragma unroll
             for (int k = 0; k < 2; k++)
@@ -1069,67 +1074,71 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
                     weights[8 * k + i / 2] = pack_bf16(x, y);
                 }
 #pragma unroll
-            for (int d = 0; d < kParts; d++) {
-                if (odd) {
-                    // (as in the few-row kernel)
-                    f32x16 marks;
+            for (int t16 = 0; t16 < 4; t16++) {
 #pragma unroll
-                    for (int i = 0; i < 16; i++) marks[i] = 0;
-#pragma unroll
-                    for (int t16 = 0; t16 < 4; t16++) {
-                        const u32x4 v = value_words(buffer, t16, d);
-                        uint32_t seen[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int32_t key =
-                                j + 16 * t16 + 8 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
-                            seen[i] = (key >= low[b] && key < high[b] ? 0x3F80u : 0u) |
-                                      (key + 1 >= low[b] && key + 1 < high[b] ? 0x3F800000u : 0u);
-                        }
-                        marks = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            words8(mark_pair(v.x), mark_pair(v.y), mark_pair(v.z), mark_pair(v.w)),
-                            words8(seen[0], seen[1], seen[2], seen[3]), marks, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) o[b][d][i] += unmark(marks[i]);
-                }
-#pragma unroll
-                for (int t16 = 0; t16 < 4; t16++) {
-                    u32x4 v = value_words(buffer, t16, d);
-                    if (odd)
-                        v = u32x4{plain_pair(v.x), plain_pair(v.y), plain_pair(v.z),
-                                  plain_pair(v.w)};
+                for (int d = 0; d < kParts; d++)
                     o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, v),
+                        __builtin_bit_cast(bf16x8, value_words(va, t16, d)),
                         words8(weights[4 * t16], weights[4 * t16 + 1], weights[4 * t16 + 2],
                                weights[4 * t16 + 3]),
                         o[b][d], 0, 0, 0);
+                if (t16 % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
+            if (odd) {
+#pragma unroll 1
+                for (int k = 0; k < kKeys; k++) {
+                    const bool sees = j + k >= low[b] && j + k < high[b];
+#pragma unroll
+                    for (int d = 0; d < kParts; d++)
+#pragma unroll
+                        for (int g = 0; g < 4; g++) {
+                            const u32x2 w = *(const SZ_LDS u32x2*)(uintptr_t)(
+                                values + k * kRow + ((4 * d + g) ^ v_mix<DP>(k)) * 16 + 8 * h);
+                            if (__ballot(sees && (odd_pair(w.x) || odd_pair(w.y))) == 0) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const float x = __uint_as_float(
+                                    e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+                                if (sees && !(fabsf(x) <= FLT_MAX)) o[b][d][4 * g + e] += x;
+                            }
+                        }
                 }
             }
         }
     };
 
-    // A step that every row sees all of, in a pipeline: while the softmax of
-    // this step's scores (now) runs on the vector units, the matrix cores
-    // form the next step's (next); then they add this step's values.  The
-    // order is laid down instruction group by instruction group, so that
-    // each product has its share of the softmax beside it and its operand
-    // read two groups ahead.
-    struct Scores {
-        f32x16 s[QB][2];
+    // Steps that every row sees all of, in a pipeline of halves (32 keys):
+    // while the softmax of one half's scores (now) runs on the vector units,
+    // the matrix cores form the next half's (next); then they add the one
+    // half's values.  The order is laid down instruction group by instruction
+    // group, so that each product has its share of the softmax beside it and
+    // its operand read some groups ahead.
+    struct Half {
+        f32x16 s[QB];
         float top[QB];
     };
-    constexpr int kGroupsA = 2 * kSlices, kGroupsB = 4 * kParts, kUnits = 16 * QB;
-    const auto inner = [&](Scores& now, Scores& next, uint32_t buffer) {
+    constexpr int kGroups = 2 * kParts;  // of either product: DP / 16 slices; 2 x DP / 32 parts
+    static_assert(kGroups == kSlices, "");
+    constexpr int kUnits = 8 * QB;       // pairs of weights in a lane
+    constexpr int kAhead = 3;            // groups that operands are read ahead
+    const auto zero = [&](Half& x) {
 #pragma unroll
-        for (int b = 0; b < QB; b++) follow(b, now.top[b]);
-        uint32_t weights[QB][16];
+        for (int b = 0; b < QB; b++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) x.s[b][i] = 0;
+    };
+    // ka: the next half's keys; va: this half's values.  PRODUCT: there is a
+    // next half.
+    const auto inner = [&](Half& now, Half& next, uint32_t ka, uint32_t va, auto product) {
+        constexpr bool kProduct = decltype(product)::value;
+#pragma unroll
+        for (int b = 0; b < QB; b++) follow(b, scored(now.top[b]) * by);
+        uint32_t weights[QB][8];
         // two weights: of 16 keys u / (4 QB), rows' block u / 4 % QB
         const auto unit = [&](int u) {
-            const int t16 = u / (4 * QB), b = u / 4 % QB, i = 8 * (t16 % 2) + 2 * (u % 4);
-            const float x = __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][t16 / 2][i]), by, -m[b]));
-            const float y =
-                __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][t16 / 2][i + 1]), by, -m[b]));
+            const int t16 = u / (4 * QB), b = u / 4 % QB, i = 8 * t16 + 2 * (u % 4);
+            const float x = __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][i]), by, -m[b]));
+            const float y = __builtin_amdgcn_exp2f(fmaf(scored(now.s[b][i + 1]), by, -m[b]));
             l[b] += x + y;
             // (kept here: left to itself the compiler puts the additions off
             // and holds every weight in a register until then)
@@ -1137,146 +1146,131 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             weights[b][4 * t16 + u % 4] = pack_bf16(x, y);
         };
         constexpr int kFirst = kUnits * 3 / 4;  // units beside the first product
-        bf16x8 kf[3];
-        u32x4 vf[3];
-        kf[0] = keys_at(buffer ^ 1, 0, 0);
-        kf[1] = keys_at(buffer ^ 1, 1 / kSlices, 1 % kSlices);
+        bf16x8 kf[kAhead + 1];
+        u32x4 vf[kAhead + 1];
+        const auto read = [&](int g) {  // group g's operand
+            if (g < kGroups) {
+                if constexpr (kProduct) kf[g % (kAhead + 1)] = keys_at(ka, g);
+            } else if (g < 2 * kGroups) {
+                vf[g % (kAhead + 1)] =
+                    value_words(va, (g - kGroups) / kParts, (g - kGroups) % kParts);
+            }
+        };
 #pragma unroll
-        for (int b = 0; b < QB; b++)
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) next.s[b][k][i] = 0;
+        for (int g = 0; g < kAhead; g++) read(g);
+        if constexpr (kProduct) zero(next);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int g = 0; g < kGroupsA; g++) {
-            if (g + 2 < kGroupsA)
-                kf[(g + 2) % 3] = keys_at(buffer ^ 1, (g + 2) / kSlices, (g + 2) % kSlices);
-            else
-                vf[g + 2 - kGroupsA] = value_words(buffer, 0, g + 2 - kGroupsA);
+        for (int g = 0; g < kGroups; g++) {
+            read(g + kAhead);
+            if constexpr (kProduct) {
 #pragma unroll
-            for (int b = 0; b < QB; b++)
-                next.s[b][g / kSlices] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    kf[g % 3], q[b][g % kSlices], next.s[b][g / kSlices], 0, 0, 0);
+                for (int b = 0; b < QB; b++)
+                    next.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        kf[g % (kAhead + 1)], q[b][g], next.s[b], 0, 0, 0);
+            }
 #pragma unroll
-            for (int u = g * kFirst / kGroupsA; u < (g + 1) * kFirst / kGroupsA; u++) unit(u);
+            for (int u = g * kFirst / kGroups; u < (g + 1) * kFirst / kGroups; u++) unit(u);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (kProduct) {
 #pragma unroll
-        for (int b = 0; b < QB; b++) next.top[b] = next.s[b][0][0];
+            for (int b = 0; b < QB; b++) next.top[b] = -INFINITY;
+        }
 #pragma unroll
-        for (int g = 0; g < kGroupsB; g++) {
-            if (g + 2 < kGroupsB)
-                vf[(g + 2) % 3] = value_words(buffer, (g + 2) / kParts, (g + 2) % kParts);
+        for (int g = 0; g < kGroups; g++) {
+            read(kGroups + g + kAhead);
             const int t16 = g / kParts, d = g % kParts;
 #pragma unroll
             for (int b = 0; b < QB; b++)
                 o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, vf[g % 3]),
+                    __builtin_bit_cast(bf16x8, vf[(kGroups + g) % (kAhead + 1)]),
                     words8(weights[b][4 * t16], weights[b][4 * t16 + 1], weights[b][4 * t16 + 2],
                            weights[b][4 * t16 + 3]),
                     o[b][d], 0, 0, 0);
-            if (g < kGroupsB / 2) {
+            if (g < kParts) {
 #pragma unroll
-                for (int u = kFirst + g * (kUnits - kFirst) / (kGroupsB / 2);
-                     u < kFirst + (g + 1) * (kUnits - kFirst) / (kGroupsB / 2); u++)
+                for (int u = kFirst + g * (kUnits - kFirst) / kParts;
+                     u < kFirst + (g + 1) * (kUnits - kFirst) / kParts; u++)
                     unit(u);
-            } else {
-                constexpr int kHalf = kGroupsB / 2;
+            } else if constexpr (kProduct) {
 #pragma unroll
-                for (int u = (g - kHalf) * 32 / kHalf; u < (g - kHalf + 1) * 32 / kHalf; u++)
+                for (int i = (g - kParts) * 16 / kParts; i < (g - kParts + 1) * 16 / kParts; i++)
 #pragma unroll
                     for (int b = 0; b < QB; b++)
-                        next.top[b] = fmaxf(next.top[b], next.s[b][u / 16][u % 16]);
+                        next.top[b] = fmaxf(next.top[b], next.s[b][i]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // The scores of the first such step
-    const auto ahead = [&](Scores& x, uint32_t buffer) {
+    // The scores of the first half
+    const auto ahead = [&](Half& x, uint32_t ka) {
+        zero(x);
 #pragma unroll
-        for (int b = 0; b < QB; b++) {
+        for (int c = 0; c < kSlices; c++) {
+            const bf16x8 f = keys_at(ka, c);
 #pragma unroll
-            for (int k = 0; k < 2; k++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) x.s[b][k][i] = 0;
+            for (int b = 0; b < QB; b++)
+                x.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][c], x.s[b], 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < 2; k++)
-#pragma unroll
-            for (int c = 0; c < kSlices; c++) {
-                const bf16x8 f = keys_at(buffer, k, c);
-#pragma unroll
-                for (int b = 0; b < QB; b++)
-                    x.s[b][k] =
-                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][c], x.s[b][k], 0, 0, 0);
-            }
-#pragma unroll
         for (int b = 0; b < QB; b++) {
-            x.top[b] = x.s[b][0][0];
+            x.top[b] = x.s[b][0];
 #pragma unroll
-            for (int i = 1; i < 32; i++) x.top[b] = fmaxf(x.top[b], x.s[b][i / 16][i % 16]);
+            for (int i = 1; i < 16; i++) x.top[b] = fmaxf(x.top[b], x.s[b][i]);
         }
     };
 
     // What was fetched for a step has arrived from every wave, and every
-    // wave is done with the step before, whose buffers the next fetches fill.
+    // wave is done with the step before: with its keys, and with the values
+    // of the one before that, which the next fetch replaces.
     const auto arrived = [&] {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
-    // Steps of 64 keys; step x has buffers x % 2.  [in0, in1): steps all of
-    // which every row sees, an even number of them.
+    // Steps of 64 keys; step x has K's buffer x % 2 and V's x % 3.
+    // [in0, in1): steps all of which every row sees.
     const int32_t steps = first < last ? (last - first + kKeys - 1) / kKeys : 0;
     int32_t in0 = t.all_lo > first ? (t.all_lo - first + kKeys - 1) / kKeys : 0;
     int32_t in1 = (t.all_hi < last ? t.all_hi : last) - first;
     in1 = in1 > 0 ? in1 / kKeys : 0;
     if (in1 > steps) in1 = steps;
-    if (in0 > in1) in0 = in1;
-    in0 = (in0 + 1) & ~1;  // (even, so that the pipeline's buffers are constants)
-    if (in0 > in1) in0 = in1;
-    in1 -= (in1 - in0) & 1;
+    if (in0 >= in1) in0 = in1 = steps;
     if (SHARED) arrived();  // (every wave is done with the part before)
-    if (steps > 0) {
-        fetch_k(first, 0);
-        fetch_v(first, 0);
-        look_up(first + kKeys, first + kKeys);
-    }
+    if (steps > 0) fetch_step(first, 0, 0);
     int32_t x = 0;
-    bool k_ahead = false;  // the keys of step x + 1 are fetched
-    for (;;) {
-        const int32_t stop = x < in1 && in0 < in1 ? in0 : steps;
-        for (; x < stop; x++) {
+    uint32_t vb = 0;  // x % 3
+    const auto begin_step = [&] {
+        arrived();
+        fetch_step(first + (x + 1) * kKeys, (x + 1) & 1, vb == 2 ? 0 : vb + 1);
+    };
+    const auto end_step = [&] {
+        x++;
+        vb = vb == 2 ? 0 : vb + 1;
+    };
+    for (int pass = 0; pass < 2; pass++) {
+        const int32_t stop = pass == 0 ? in0 : steps;
+        while (x < stop) {
             const int32_t j = first + x * kKeys;
-            arrived();
-            if (!k_ahead) fetch_k(j + kKeys, (x + 1) & 1);
-            fetch_v(j + kKeys, (x + 1) & 1);
-            look_up(j + 2 * kKeys, j + 2 * kKeys);
-            k_ahead = false;
-            if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1);
+            begin_step();
+            if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1, vb, vb == 0 ? 2 : vb - 1);
+            end_step();
         }
-        if (x >= steps) break;
-        Scores even, uneven;
-        {
-            const int32_t j = first + x * kKeys;
-            arrived();
-            fetch_k(j + kKeys, 1);
-            look_up(j + 2 * kKeys, j + kKeys);
+        if (pass == 1 || in0 == in1) continue;
+        Half even, uneven;
+        uint32_t va = v_lane + vb * kBuffer;
+        begin_step();
+        ahead(even, k_lane + (x & 1) * kBuffer);
+        inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
+        end_step();
+        while (x < in1) {
+            const uint32_t ka = k_lane + (x & 1) * kBuffer;
+            begin_step();
+            inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
+            va = v_lane + vb * kBuffer;
+            inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
+            end_step();
         }
-        ahead(even, 0);
-        for (; x < in1; x += 2) {
-            const int32_t j = first + x * kKeys;
-            arrived();
-            fetch_k(j + 2 * kKeys, 0);
-            fetch_v(j + kKeys, 1);
-            look_up(j + 3 * kKeys, j + 2 * kKeys);
-            inner(even, uneven, 0);
-            arrived();
-            fetch_k(j + 3 * kKeys, 1);
-            fetch_v(j + 2 * kKeys, 0);
-            look_up(j + 4 * kKeys, j + 3 * kKeys);
-            inner(uneven, even, 1);
-        }
-        k_ahead = true;
+        inner(uneven, even, 0, va + 32 * kRow, std::false_type{});
     }
     // nothing may still be on its way to this workgroup's LDS when it ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1417,12 +1411,6 @@ hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t str
         else
             k_attend_few<DP, 4, false><<<grid, block, 0, stream>>>(a, p, score, ws);
         return hipGetLastError();
-    }
-    if constexpr (DP <= 128) {
-        if (p.tile_log2 == 8) {
-            k_attend_chunk<DP, 2, CAP, false><<<grid, block, 0, stream>>>(a, p, score, ws);
-            return hipGetLastError();
-        }
     }
     if (p.shares != 0)
         k_attend_chunk<DP, 1, CAP, true><<<grid, block, 0, stream>>>(a, p, score, ws);
