@@ -485,19 +485,16 @@ def _heads(x):
     return x if x is None or type(x) is Heads else Heads(x)
 
 
-def _call_stream(stream, *xs):
+def _call_stream(stream, first, *rest):
     """The stream of a call whose descriptors and tensors are given (None and
     integer addresses skipped): all on the current device, as `stream` must
     be."""
     import torch
-    index = None
-    for x in xs:
-        if x is not None and type(x) is not int:
-            i = x._index if isinstance(x, _Descriptor) else x.get_device()
-            if index is None:
-                index = i
-            elif i != index:
-                raise ValueError("the call's tensors are on different devices")
+    index = first._index
+    for x in rest:
+        # (descriptors before tensors: one attribute)
+        if x is not None and getattr(x, "_index", index) != index:
+            raise ValueError("the call's tensors are on different devices")
     if torch.cuda.current_device() != index:
         raise ValueError(f"the tensors are on device {index}, the current device is "
                          f"{torch.cuda.current_device()}")
@@ -520,10 +517,17 @@ def _dims(dim: int, *xs) -> None:
             raise ValueError(f"rows of {x.dim} elements where {dim} are expected")
 
 
-def _array(x, dtype, n: int, what: str) -> None:
-    if x is not None and type(x) is not int and \
-            (x.dtype != dtype or x.numel() < n or not x.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous tensor of at least {n} {dtype}")
+def _array(x, dtype: str, n: int, index: int, what: str) -> int | None:
+    """Address of a device array of at least n elements (None and integer
+    addresses as they are)."""
+    if x is None or type(x) is int:
+        return x
+    import torch
+    if x.dtype is not getattr(torch, dtype) or x.numel() < n or not x.is_contiguous() or \
+            x.get_device() != index:
+        raise ValueError(f"{what} must be a contiguous tensor of at least {n} {dtype}s on the "
+                         "call's device")
+    return x.data_ptr()
 
 
 def sz_rope_frequencies(rotary_dim: int, base: float, stretch: int = SZ_ROPE_PLAIN,
@@ -549,43 +553,41 @@ def sz_qk_norm_rope(q, q_out, q_weight, k, k_out, k_weight, head_dim: int, n_tok
                     positions, eps: float, rope, stream=None) -> None:
     """q, q_out, k, k_out: Heads, or tensors [tokens, heads, head_dim]; rope: a
     Rope or None."""
-    import torch
     q, q_out, k, k_out = _heads(q), _heads(q_out), _heads(k), _heads(k_out)
-    stream = _call_stream(stream, q, q_out, q_weight, k, k_out, k_weight, positions, rope)
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("neither queries nor keys")
+    stream = _call_stream(stream, some, q_out, k, k_out, rope)
+    index = some._index
     _tokens(n_tokens, q, q_out, k, k_out)
     _dims(head_dim, q, q_out, k, k_out)
-    _array(q_weight, torch.float32, head_dim, "q_weight")
-    _array(k_weight, torch.float32, head_dim, "k_weight")
-    _array(positions, torch.int32, n_tokens, "positions")
-    _check(_lib.sz_qk_norm_rope(_at(q), _at(q_out), _ptr(q_weight), _at(k), _at(k_out),
-                                _ptr(k_weight), head_dim, n_tokens, _ptr(positions), eps,
-                                _at(rope), stream), "sz_qk_norm_rope")
+    _check(_lib.sz_qk_norm_rope(
+        _at(q), _at(q_out), _array(q_weight, "float32", head_dim, index, "q_weight"),
+        _at(k), _at(k_out), _array(k_weight, "float32", head_dim, index, "k_weight"),
+        head_dim, n_tokens, _array(positions, "int32", n_tokens, index, "positions"), eps,
+        _at(rope), stream), "sz_qk_norm_rope")
 
 
-def _check_batch(cache, batch, d_status) -> None:
-    import torch
+def _check_rows(cache, batch) -> None:
     if batch.n_seqs > cache.rows:
         raise ValueError(f"{batch.n_seqs} sequences, {cache.rows} rows in the page tables")
-    _array(d_status, torch.int32, batch.n_seqs, "d_status")
 
 
 def sz_kv_append(k, v, k_weight, q, q_out, q_weight, eps: float, rope, positions, cache, batch,
                  d_status=None, stream=None) -> None:
     """k, v, q, q_out: Heads, or tensors [tokens, heads, head_dim]; cache: a
     KVCache; batch: a Batch; rope: a Rope or None."""
-    import torch
     k, v, q, q_out = _heads(k), _heads(v), _heads(q), _heads(q_out)
-    stream = _call_stream(stream, k, v, k_weight, q, q_out, q_weight, rope, positions, cache,
-                          batch, d_status)
-    _tokens(batch.n_tokens, k, v, q, q_out)
-    _dims(cache.head_dim, k, v, q, q_out)
-    _array(q_weight, torch.float32, cache.head_dim, "q_weight")
-    _array(k_weight, torch.float32, cache.head_dim, "k_weight")
-    _array(positions, torch.int32, batch.n_tokens, "positions")
-    _check_batch(cache, batch, d_status)
-    _check(_lib.sz_kv_append(_at(k), _at(v), _ptr(k_weight), _at(q), _at(q_out), _ptr(q_weight),
-                             eps, _at(rope), _ptr(positions), _at(cache), _at(batch),
-                             _ptr(d_status), stream), "sz_kv_append")
+    stream = _call_stream(stream, cache, batch, k, v, q, q_out, rope)
+    index, dim, n = cache._index, cache.head_dim, batch.n_tokens
+    _tokens(n, k, v, q, q_out)
+    _dims(dim, k, v, q, q_out)
+    _check_rows(cache, batch)
+    _check(_lib.sz_kv_append(
+        _at(k), _at(v), _array(k_weight, "float32", dim, index, "k_weight"), _at(q), _at(q_out),
+        _array(q_weight, "float32", dim, index, "q_weight"), eps, _at(rope),
+        _array(positions, "int32", n, index, "positions"), cache._at, batch._at,
+        _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_kv_append")
 
 
 def sz_attend_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
@@ -597,17 +599,17 @@ def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softc
                     workspace_bytes: int = 0, d_status=None, stream=None) -> None:
     """q, out: Heads, or tensors [tokens, heads, head_dim]; lse: a float32
     tensor [tokens, heads] or None; cache: a KVCache; batch: a Batch."""
-    import torch
     q, out = _heads(q), _heads(out)
-    stream = _call_stream(stream, q, out, lse, cache, batch, workspace, d_status)
-    _tokens(batch.n_tokens, q, out)
+    stream = _call_stream(stream, cache, batch, q, out)
+    index, n = cache._index, batch.n_tokens
+    _tokens(n, q, out)
     _dims(cache.head_dim, q, out)
-    _array(lse, torch.float32, batch.n_tokens * q.heads, "lse")
-    _array(workspace, torch.uint8, workspace_bytes, "workspace")
-    _check_batch(cache, batch, d_status)
-    _check(_lib.sz_attend_pages(_at(q), _at(out), _ptr(lse), _at(cache), _at(batch), max_len,
-                                scale, softcap, int(causal), window, _ptr(workspace),
-                                workspace_bytes, _ptr(d_status), stream), "sz_attend_pages")
+    _check_rows(cache, batch)
+    _check(_lib.sz_attend_pages(
+        q._at, out._at, _array(lse, "float32", n * q.heads, index, "lse"), cache._at, batch._at,
+        max_len, scale, softcap, int(causal), window,
+        _array(workspace, "uint8", workspace_bytes, index, "workspace"), workspace_bytes,
+        _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_attend_pages")
 
 
 # ---- conveniences (torch allocates; the library computes) -----------------

@@ -51,6 +51,35 @@ __device__ __forceinline__ bf16x8 words8(uint32_t a, uint32_t b, uint32_t c, uin
     return __builtin_bit_cast(bf16x8, v);
 }
 
+// The largest value of a wave's lanes, and their sum, in every lane: along
+// rows of 16 lanes, then across them, without a pass through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float x, float other) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(x),
+                                                      CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float x) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kWave - 1));
+}
+__device__ __forceinline__ float wave_max(float x) {
+    x = fmaxf(x, moved<0x111, 0xF>(x, x));  // row_shr:1
+    x = fmaxf(x, moved<0x112, 0xF>(x, x));
+    x = fmaxf(x, moved<0x114, 0xF>(x, x));
+    x = fmaxf(x, moved<0x118, 0xF>(x, x));
+    x = fmaxf(x, moved<0x142, 0xA>(x, x));  // row_bcast:15 into rows 1 and 3
+    x = fmaxf(x, moved<0x143, 0xC>(x, x));  // row_bcast:31 into rows 2 and 3
+    return last_lane(x);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x += moved<0x111, 0xF>(x, 0);
+    x += moved<0x112, 0xF>(x, 0);
+    x += moved<0x114, 0xF>(x, 0);
+    x += moved<0x118, 0xF>(x, 0);
+    x += moved<0x142, 0xA>(x, 0);
+    x += moved<0x143, 0xC>(x, 0);
+    return last_lane(x);
+}
+
 // How a call is cut up.  Tiles: the rows of a sequence for one KV head,
 // tile_rows at a time.  Either each tile is one workgroup's, with all its
 // keys; tile number floor(starts[s] * G / tile_rows) + s is then the first
@@ -91,6 +120,9 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
     p.tile_log2 = rows <= 16 * n_seqs ? 4 : 7;
+    // (256 rows where even they are many: half the reads of LDS and L2 for
+    // the same products)
+    if (c.head_dim <= 128 && (rows >> 8) * c.kv_heads >= kManyTiles) p.tile_log2 = 8;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     // keys of a tile: a window shows its rows' tokens' own keys and those of
     // a window before
@@ -103,7 +135,7 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
     const uint64_t resident = c.head_dim > 128 ? kCus : 2 * kCus;
     const bool whole = n_seqs > kShareSeqs || c.kv_heads > resident ||
-                       groups >= (p.few() ? kManyFew : kManyTiles) ||
+                       groups >= (p.few() ? kManyFew : kManyTiles) || p.tile_log2 == 8 ||
                        p.tiles * (max_len / kStep + 2) >= kMostSteps ||
                        keys * c.head_dim * 4 <= kWholeBytes;
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
@@ -1326,7 +1358,7 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 // nothing to wait for between them.
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
-    constexpr uint32_t kAtOnce = kWave / LANES;
+    constexpr uint32_t kAtOnce = kWave / LANES, kBatch = 4;
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t pieces = (1u << p.tile_log2) / kWaves;
@@ -1345,6 +1377,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     const Row w = find_row(a, p, t, r);
     const uint32_t dim = a.cache.head_dim;
     const uint32_t e = 4 * (lane % LANES);
+    const uint64_t stride = (uint64_t)dim << p.tile_log2;
     float top = kNoKey, total = 0;
     f32x4 x = {0, 0, 0, 0};
     for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
@@ -1355,32 +1388,28 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
             m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
             l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
         }
-        float most = fmaxf(m, top);
-#pragma unroll
-        for (int d = 1; d < (int)kWave; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-        const float weight = __builtin_amdgcn_exp2f(m - most);
-        const float keep = __builtin_amdgcn_exp2f(top - most);
-        top = most;
-        l *= weight;
-#pragma unroll
-        for (int d = 1; d < (int)kWave; d *= 2) l += __shfl_xor(l, d);
-        total = total * keep + l;
-        x *= keep;
         const float* o = u.o + (uint64_t)r * dim + e;
-        const uint64_t stride = (uint64_t)dim << p.tile_log2;
-        for (uint32_t s0 = 0; s0 < parts; s0 += 4 * kAtOnce) {
-            f32x4 v[4];
+        f32x4 v[kBatch];
+        const auto read = [&](uint32_t s0) {
 #pragma unroll
-            for (uint32_t k = 0; k < 4; k++) {
+            for (uint32_t k = 0; k < kBatch; k++) {
                 const uint32_t s = s0 + k * kAtOnce + lane / LANES;
                 v[k] = f32x4{0, 0, 0, 0};
                 if (s < parts && e < dim) v[k] = *(const SZ_GLOBAL f32x4*)(o + s * stride);
             }
+        };
+        read(0);  // (under way while the weights are made)
+        const float most = wave_max(fmaxf(m, top));
+        const float weight = __builtin_amdgcn_exp2f(m - most);
+        const float keep = __builtin_amdgcn_exp2f(top - most);
+        top = most;
+        total = total * keep + wave_sum(l * weight);
+        x *= keep;
+        for (uint32_t s0 = 0; s0 < parts; s0 += kBatch * kAtOnce) {
+            if (s0 > 0) read(s0);
 #pragma unroll
-            for (uint32_t k = 0; k < 4; k++) {
-                const float by = __shfl(weight, (s0 + k * kAtOnce + lane / LANES) % kWave);
-                x += v[k] * by;
-            }
+            for (uint32_t k = 0; k < kBatch; k++)
+                x += v[k] * __shfl(weight, (s0 + k * kAtOnce + lane / LANES) % kWave);
         }
     }
 #pragma unroll
@@ -1411,6 +1440,12 @@ hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t str
         else
             k_attend_few<DP, 4, false><<<grid, block, 0, stream>>>(a, p, score, ws);
         return hipGetLastError();
+    }
+    if constexpr (DP <= 128) {
+        if (p.tile_log2 == 8) {
+            k_attend_chunk<DP, 2, CAP, false><<<grid, block, 0, stream>>>(a, p, score, ws);
+            return hipGetLastError();
+        }
     }
     if (p.shares != 0)
         k_attend_chunk<DP, 1, CAP, true><<<grid, block, 0, stream>>>(a, p, score, ws);
