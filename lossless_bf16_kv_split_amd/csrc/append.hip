@@ -10,8 +10,7 @@
 //
 // The angle is exact: p * phase_i modulo 2^64 is the fraction of a turn in
 // fixed point, whatever p, and its top 32 bits carry an error below 2^-32
-// turns.  cos and sin are Taylor polynomials on an eighth of a turn (the
-// first terms left out are below 2^-25 there), so no table is read.
+// turns.  No table is read.
 //
 // Bound by the bytes of the rows, and for few tokens by latency.  A row
 // lies across 8 to 64 lanes of a wave, each with 8 (or 4) consecutive
@@ -24,9 +23,14 @@ namespace {
 
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kWavesPerGroup = kThreads / kWave;
-// Waves that fill the chip (256 CUs, 16 each): with fewer tokens than
-// this, a token's rows are shared among several waves.
-constexpr uint64_t kFillWaves = 4096;
+// A token's rows are shared among several waves until there are this many
+// of them, twice what 256 CUs hold at once: fewer leave rows in a queue
+// behind their wave's loads, more work out the token's angles too often
+// (8192 tokens' 72 rows from 32 bits, normed: 94 us with 4096, 87 with
+// 16384, 84 with 32768, 89 with 65536; their 48 rows of BF16 into the cache:
+// 42, 42, 44, 58).  Stores stay cached: attention reads the rows next
+// (non-temporal ones save 3 to 5% of this kernel).
+constexpr uint64_t kFillWaves = 16384;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -37,20 +41,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// cos and sin of a / 2^32 turns
+// cos and sin of a / 2^32 turns: the hardware's own, which take turns (off
+// by at most 1.3e-7 over the whole circle, measured against 64 bits)
 __device__ __forceinline__ void turn_of(uint32_t a, float& c, float& s) {
-    const uint32_t quarter = (a + 0x20000000u) >> 30;
-    const float x = (float)(int32_t)(a - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
-    const float z = x * x;
-    const float sn =
-        fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f),
-                         -1.6666667e-1f), x);
-    const float cs =
-        fmaf(z, fmaf(z, fmaf(z, fmaf(z, 2.4801587e-5f, -1.3888889e-3f), 4.1666667e-2f), -0.5f),
-             1.0f);
-    const float u = (quarter & 1) ? sn : cs, v = (quarter & 1) ? cs : sn;
-    c = __uint_as_float(__float_as_uint(u) ^ (((quarter + 1) & 2) << 30));
-    s = __uint_as_float(__float_as_uint(v) ^ ((quarter & 2) << 30));
+    const float turns = (float)(int32_t)a * 0x1p-32f;
+    c = __builtin_amdgcn_cosf(turns);
+    s = __builtin_amdgcn_sinf(turns);
 }
 
 // VEC elements of a row from element e of it, as floats
@@ -158,15 +154,27 @@ __global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batc
         }
     }
 
+    // the rows of queries and keys, the next one's load under way
     const uint32_t turned = a.q.heads + a.k.heads;
-    for (uint32_t r0 = slice * kRows; r0 < turned; r0 += slices * kRows) {
+    const uint32_t stride = slices * kRows;
+    const auto load = [&](uint32_t r, float (&x)[VEC]) {
+        const bool is_k = r >= a.q.heads;
+        const Rows& src = is_k ? a.k : a.q;
+        const uint32_t h = is_k ? r - a.q.heads : r;
+        if (live && r < turned)
+            load_row<VEC>(src, token * src.token_stride + h * src.head_stride + e, x);
+    };
+    float next[VEC] = {};
+    load(slice * kRows + lane / LANES, next);
+    for (uint32_t r0 = slice * kRows; r0 < turned; r0 += stride) {
         const uint32_t r = r0 + lane / LANES;
         const bool is_k = r >= a.q.heads;
         const uint32_t h = is_k ? r - a.q.heads : r;
-        const Rows& src = is_k ? a.k : a.q;
         const bool on = live && r < turned;
-        float x[VEC] = {};
-        if (on) load_row<VEC>(src, token * src.token_stride + h * src.head_stride + e, x);
+        float x[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; i++) x[i] = next[i];
+        load(r + stride, next);
         const float* weight = is_k ? a.k_weight : a.q_weight;
         float sum = 0;
 #pragma unroll
