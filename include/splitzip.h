@@ -566,7 +566,8 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  *             0, or anything past it, means what the pages hold,
  *             pages_per_seq * page_tokens (2^30 at most).  Work is split for
  *             this bound, so it should not be far above the lengths.
- *   scale     > 0, finite; softcap >= 0, finite (0: none)
+ *   scale     > 0, softcap >= 0 (0: none); both, and scale / softcap, finite
+ *             and below 1e38
  *   d_workspace, workspace_bytes   256-byte aligned, at least
  *             sz_attend_workspace_size(q->heads, cache, batch, max_len); any
  *             content; NULL where that is 0.  Calls (or replays of graphs)

@@ -96,7 +96,7 @@ struct AttendPlan {
     uint32_t shares;     // workgroups that share it out for a KV head; 0: whole tiles
     uint32_t least;      // the fewest steps of a share
     bool wide;           // few rows, whole tiles, a CU each: eight waves
-    bool few() const { return tile_log2 == 4; }
+    __host__ __device__ bool few() const { return tile_log2 == 4; }
 };
 
 constexpr uint32_t kStep = 128;  // keys
@@ -110,8 +110,8 @@ constexpr uint64_t kManyFew = 4096, kManyTiles = 512;
 constexpr uint64_t kWholeBytes = 288 * 1024;
 // Sharing out looks at every sequence in every workgroup, 64 at a time.
 constexpr uint64_t kShareSeqs = 1024;
-// and counts steps in 32 bits, times workgroups
-constexpr uint64_t kMostSteps = uint64_t{1} << 22;
+// and counts steps in 32 bits.
+constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 constexpr uint32_t kLeastFew = 1, kLeastTiles = 4;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
@@ -540,10 +540,14 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 
 // ---- few rows: a decode step, drafted tokens ------------------------------
 //
-// One workgroup takes a tile of 16 rows and a split of its keys; each wave
+// One workgroup takes a tile of 16 rows and a part of its keys; each wave
 // streams every fourth (or eighth) block of 32 keys straight from the pages
 // into registers, with the next block's loads in flight, and the waves'
-// results are joined in LDS at the end.  Bound by the bytes of the cache.
+// results are joined in LDS at the end.  Bound by the bytes of the cache: 48
+// sequences of 130 to 8192 keys, 908 MB, take 166 us (5.5 TB/s; a large copy
+// moves 4.8), two of 32768, 264 MB, 54 us with the join.  A short cache is
+// bound by the chain of loads (lengths, page addresses, keys): about 6 us,
+// and 3 for the join.
 //
 // Matrix operands of 16x16x32: lane (n = lane % 16, h = lane / 16) holds
 // eight of 32 contraction terms of row n.
@@ -559,26 +563,27 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 //    elements 8 n + i as its rows.
 //  - O^T's result: lane (query n, h) then has, for r < 4, elements
 //    32 h + 8 r + i: 32 consecutive ones.
+template <int DP, int WAVES>
+struct FewLds {
+    float o[WAVES][16][DP + 4];
+    float m[WAVES][16], l[WAVES][16];
+};
+
 template <int DP, int WAVES, bool SHARED>
-__global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void k_attend_few(
-    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+__device__ __forceinline__ void few_part(const Attend& a, const AttendPlan& p, const Score& score,
+                                         uint8_t* ws, const Part& part, uint32_t kv,
+                                         FewLds<DP, WAVES>& join) {
     constexpr int kStride = 32 * WAVES;    // keys that the workgroup takes at a time
-    constexpr int kAux = SHARED ? 2 : 0;   // the loads' nt bit
+    // the loads' nt bit: shared out work is more than the caches hold (2 x
+    // 32768 keys: 58 us without; but 12.1 us with, 10.6 without, for tiles of
+    // 1024 keys that stay in them)
+    constexpr int kAux = SHARED ? 2 : 0;
     constexpr int kSlices = DP / 32;       // of K, 32 elements each
     constexpr int kVec = DP < 128 ? 4 : 8; // elements of a V row per load
     constexpr int kVLoads = DP / (16 * kVec);
     constexpr int kProducts = DP / 16;     // of 16 elements of the output
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t kv = blockIdx.x % a.cache.kv_heads;
-    constexpr int kPitch = DP + 4;
-    __shared__ float join_o[WAVES][16][kPitch];
-    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
-    const uint32_t index = blockIdx.x / a.cache.kv_heads;
-    Walk<SHARED> walk(a, p);
-    Part part;
-    if (!walk.first(a, p, index, part)) return;
-    do {
     const Tile& t = part.t;
     const int32_t first = part.first, last = part.last;
 
@@ -736,7 +741,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
                 for (int i = 0; i < 4; i++) {
                     const int32_t key = j + 16 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
                     seen[i] = (key >= low && key < high ? 0x3F80u : 0u) |
-                                 (key + 1 >= low && key + 1 < high ? 0x3F800000u : 0u);
+                              (key + 1 >= low && key + 1 < high ? 0x3F800000u : 0u);
                 }
             }
         }
@@ -756,13 +761,12 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
                     }
 #pragma unroll
             for (int d = 0; d < kProducts; d++) {
-                    f32x4 z = {0, 0, 0, 0};
-                    z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        values(y, d), words8(seen[0], seen[1], seen[2], seen[3]), z, 0,
-                        0, 0);
+                f32x4 z = {0, 0, 0, 0};
+                z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    values(y, d), words8(seen[0], seen[1], seen[2], seen[3]), z, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) o[d][i] += unmark(z[i]);
-                }
+                for (int i = 0; i < 4; i++) o[d][i] += unmark(z[i]);
+            }
         }
 #pragma unroll
         for (int d = 0; d < kProducts; d++) {
@@ -789,8 +793,8 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (h == 0) {
-            join_m[wave][n] = m;
-            join_l[wave][n] = sum;
+            join.m[wave][n] = m;
+            join.l[wave][n] = sum;
         }
 #pragma unroll
         for (int u = 0; u < kVLoads; u++)
@@ -798,23 +802,23 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
             for (int r = 0; r < 4; r++)
 #pragma unroll
                 for (int i = 0; i < kVec; i++)
-                    join_o[wave][n][16 * kVec * u + kRun * h + kVec * r + i] =
+                    join.o[wave][n][16 * kVec * u + kRun * h + kVec * r + i] =
                         o[kVec * u + i][r];
         __syncthreads();
         constexpr int kPer = DP / 16;  // elements of a thread, of the first 256
         const uint32_t r = threadIdx.x / 16 % 16, e = threadIdx.x % 16 * kPer;
         const Row w = find_row(a, p, t, (int32_t)r);
         if (w.on && threadIdx.x < kThreads) {
-            float top = join_m[0][r];
+            float top = join.m[0][r];
 #pragma unroll
-            for (int i = 1; i < WAVES; i++) top = fmaxf(top, join_m[i][r]);
+            for (int i = 1; i < WAVES; i++) top = fmaxf(top, join.m[i][r]);
             float total = 0, x[kPer] = {};
 #pragma unroll
             for (int i = 0; i < WAVES; i++) {
-                const float keep = __builtin_amdgcn_exp2f(join_m[i][r] - top);
-                total += join_l[i][r] * keep;
+                const float keep = __builtin_amdgcn_exp2f(join.m[i][r] - top);
+                total += join.l[i][r] * keep;
 #pragma unroll
-                for (int k = 0; k < kPer; k++) x[k] = fmaf(join_o[i][r][e + k], keep, x[k]);
+                for (int k = 0; k < kPer; k++) x[k] = fmaf(join.o[i][r][e + k], keep, x[k]);
             }
             const uint32_t head = kv * p.group + w.head;
             if (!SHARED || part.alone) {
@@ -850,22 +854,42 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
             }
         }
     }
+}
+
+template <int DP, int WAVES, bool SHARED>
+__global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void k_attend_few(
+    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
+    __shared__ FewLds<DP, WAVES> join;
+    Walk<SHARED> walk(a, p);
+    Part part;
+    if (!walk.first(a, p, index, part)) return;
+    do {
+        few_part<DP, WAVES, SHARED>(a, p, score, ws, part, kv, join);
     } while (walk.next(a, p, index, part));
 }
 
 // ---- chunks: a part of a prompt, or all of it -----------------------------
 //
-// One workgroup of four waves takes a tile of 128 or 256 rows, each wave 32
-// or 64 of them, and walks the tile's keys 64 at a time.  The keys and values
+// One workgroup of four waves takes a tile of 128 (or 256) rows, each wave 32
+// (or 64) of them, and walks the tile's keys 64 at a time.  The keys and values
 // of a step go from the pages straight to LDS (each wave fetches a block of
-// 16 keys) while the step before is worked on: two buffers, one barrier a
-// step.  Bound by the matrix cores and by the softmax's arithmetic beside
-// them.
+// 16 keys) while the step before is worked on, with one barrier a step.
+//
+// Bound by power: with the matrix cores busy 55% of the cycles the clock falls
+// to 1.73 GHz (2.13 with a kernel that kept them busy 42%), so what counts is
+// fewer instructions and fewer reads for the same products.  Measured: 1.0 to
+// 1.05 PFLOP/s on prompts (a library product of 8192^3: 1.40).  The tile of
+// 128 rows leaves room for two workgroups a CU (at most 128 KB of LDS and 256
+// registers a lane for both), which hide each other's barriers and latencies;
+// the one of 256 reads LDS and L2 half as often for the same products and is 3%
+// faster where there are many of them (2048 rows of 64 heads over 32768 keys:
+// 1.95 against 2.01 ms).
 //
 // Matrix operands of 32x32x16: lane (n = lane % 32, h = lane / 32) holds eight
 // of 16 contraction terms of row n.
-//  - K: key 32 b + n, elements 16 s + 8 h .. + 7: 16 bytes of LDS.
-//  - S^T's result i: query n, key 32 b + 8 (i / 4) + 4 h + i % 4.
+//  - K: key n of 32, elements 16 s + 8 h .. + 7: 16 bytes of LDS.
+//  - S^T's result i: query n, key 8 (i / 4) + 4 h + i % 4 of the 32.
 //  - V: keys 16 t + 4 h + .. and 16 t + 8 + 4 h + .. (four each) for element
 //    32 d + n: LDS reads that transpose four rows of 16 words.
 //  - O^T's result i: query n, element 32 d + 8 (i / 4) + 4 h + i % 4.
@@ -873,7 +897,7 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
 // LDS holds rows of DP words in 16-byte pieces, permuted so that both kinds
 // of reads spread over the banks: piece c of key j lies at c ^ k_mix(j) (16
 // keys' same piece: 16 places) and c ^ v_mix(j) (four keys' 64 consecutive
-// bytes: four places).
+// bytes: four places).  No bank conflicts are counted.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define SZ_LDS __attribute__((address_space(3)))
@@ -897,25 +921,21 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                  : "memory");
 }
 
+// Bytes of LDS: K of two steps of 64 keys, V of three
+template <int DP>
+constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP;
+
 template <int DP, int QB, bool CAP, bool SHARED>
-__global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
-    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+__device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
+                                           const Score& score, uint8_t* ws, const Part& part,
+                                           uint32_t kv, uint8_t* lds) {
     constexpr int kKeys = 64;
     constexpr uint32_t kRow = 2 * DP;             // bytes of a row in LDS
     constexpr uint32_t kBuffer = kKeys * kRow;    // K or V of a step
     constexpr int kLoads = DP / 32;               // per wave, of K or V
     constexpr int kSlices = DP / 16, kParts = DP / 32;
-    // K of two steps, V of three
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kBuffer];
-
     const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
-    // whole tiles: the last ones of a prompt see the most keys and go first
-    Walk<SHARED> walk(a, p);
-    Part part;
-    if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
-    do {
     const Tile& t = part.t;
     const int32_t first = part.first, last = part.last;
 
@@ -1349,11 +1369,29 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
             }
         }
     }
+}
+
+template <int DP, int QB, bool CAP, bool SHARED>
+__global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
+    Attend a, AttendPlan p, Score score, uint8_t* ws) {
+    const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<DP>];
+    Walk<SHARED> walk(a, p);
+    Part part;
+    // whole tiles: the last ones of a prompt see the most keys and go first
+    if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
+    do {
+        chunk_part<DP, QB, CAP, SHARED>(a, p, score, ws, part, kv, lds);
     } while (walk.next(a, p, index, part));
 }
 
-// Joins the parts of the tiles that were cut: one wave per row.  64 parts at
-// a time, a lane holds one's maximum and sum; LANES lanes take four elements
+__host__ __device__ inline uint32_t join_pieces(const AttendPlan& p) {
+    return (1u << p.tile_log2) / (p.few() ? kWaves : 4 * kWaves);
+}
+
+// Joins the parts of the tiles that were cut, a row to a wave at a time (of a
+// 128-row tile four, one after the other: a workgroup's way to its tile takes
+// longer than a row).  64 parts at a time, a lane holds one's maximum and sum; LANES lanes take four elements
 // each of one's sums, so that a wave reads 64 / LANES of them at a time, with
 // nothing to wait for between them.
 template <int LANES>
@@ -1361,10 +1399,9 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     constexpr uint32_t kAtOnce = kWave / LANES, kBatch = 4;
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t pieces = (1u << p.tile_log2) / kWaves;
+    const uint32_t pieces = join_pieces(p);
     const uint32_t kv = blockIdx.x % a.cache.kv_heads;
     const uint32_t rest = blockIdx.x / a.cache.kv_heads;
-    const int32_t r = (int32_t)(rest % pieces * kWaves + wave);
     const uint32_t number = rest / pieces;
     const Shares shares(a, p);
     if (number >= Shares::from_lane(shares.tiles1, kWave - 1)) return;
@@ -1373,57 +1410,61 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     const uint32_t step = f.steps0 + at * f.x.steps;
     const uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
-    if (from == upto || r >= t.rows) return;
-    const Row w = find_row(a, p, t, r);
+    if (from == upto) return;
     const uint32_t dim = a.cache.head_dim;
     const uint32_t e = 4 * (lane % LANES);
     const uint64_t stride = (uint64_t)dim << p.tile_log2;
-    float top = kNoKey, total = 0;
-    f32x4 x = {0, 0, 0, 0};
-    for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
-        const uint32_t parts = upto - i0 + 1 < kWave ? upto - i0 + 1 : kWave;
-        const Partial u = partial_of(ws, a, p, kv, i0 + number);
-        float m = kNoKey, l = 0;
-        if (lane < parts) {
-            m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
-            l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
-        }
-        const float* o = u.o + (uint64_t)r * dim + e;
-        f32x4 v[kBatch];
-        const auto read = [&](uint32_t s0) {
-#pragma unroll
-            for (uint32_t k = 0; k < kBatch; k++) {
-                const uint32_t s = s0 + k * kAtOnce + lane / LANES;
-                v[k] = f32x4{0, 0, 0, 0};
-                if (s < parts && e < dim) v[k] = *(const SZ_GLOBAL f32x4*)(o + s * stride);
+    const int32_t rows = 1 << p.tile_log2;
+    for (int32_t r = (int32_t)(rest % pieces * kWaves + wave); r < t.rows && r < rows;
+         r += (int32_t)(pieces * kWaves)) {
+        const Row w = find_row(a, p, t, r);
+        float top = kNoKey, total = 0;
+        f32x4 x = {0, 0, 0, 0};
+        for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
+            const uint32_t parts = upto - i0 + 1 < kWave ? upto - i0 + 1 : kWave;
+            const Partial u = partial_of(ws, a, p, kv, i0 + number);
+            float m = kNoKey, l = 0;
+            if (lane < parts) {
+                m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
+                l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
             }
-        };
-        read(0);  // (under way while the weights are made)
-        const float most = wave_max(fmaxf(m, top));
-        const float weight = __builtin_amdgcn_exp2f(m - most);
-        const float keep = __builtin_amdgcn_exp2f(top - most);
-        top = most;
-        total = total * keep + wave_sum(l * weight);
-        x *= keep;
-        for (uint32_t s0 = 0; s0 < parts; s0 += kBatch * kAtOnce) {
-            if (s0 > 0) read(s0);
+            const float* o = u.o + (uint64_t)r * dim + e;
+            f32x4 v[kBatch];
+            const auto read = [&](uint32_t s0) {
 #pragma unroll
-            for (uint32_t k = 0; k < kBatch; k++)
-                x += v[k] * __shfl(weight, (s0 + k * kAtOnce + lane / LANES) % kWave);
+                for (uint32_t k = 0; k < kBatch; k++) {
+                    const uint32_t s = s0 + k * kAtOnce + lane / LANES;
+                    v[k] = f32x4{0, 0, 0, 0};
+                    if (s < parts && e < dim) v[k] = *(const SZ_GLOBAL f32x4*)(o + s * stride);
+                }
+            };
+            read(0);  // (under way while the weights are made)
+            const float most = wave_max(fmaxf(m, top));
+            const float weight = __builtin_amdgcn_exp2f(m - most);
+            const float keep = __builtin_amdgcn_exp2f(top - most);
+            top = most;
+            total = total * keep + wave_sum(l * weight);
+            x *= keep;
+            for (uint32_t s0 = 0; s0 < parts; s0 += kBatch * kAtOnce) {
+                if (s0 > 0) read(s0);
+#pragma unroll
+                for (uint32_t k = 0; k < kBatch; k++)
+                    x += v[k] * __shfl(weight, (s0 + k * kAtOnce + lane / LANES) % kWave);
+            }
         }
+#pragma unroll
+        for (int d = LANES; d < (int)kWave; d *= 2)
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[i] += __shfl_xor(x[i], d);
+        const float inv = inverse(total);
+        const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+        const uint32_t head = kv * p.group + w.head;
+        if (lane < LANES && e < dim)
+            store_out<4>(a.out, (uint64_t)w.token * a.out.token_stride +
+                                    (uint64_t)head * a.out.head_stride + e, y);
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
     }
-#pragma unroll
-    for (int d = LANES; d < (int)kWave; d *= 2)
-#pragma unroll
-        for (int i = 0; i < 4; i++) x[i] += __shfl_xor(x[i], d);
-    const float inv = inverse(total);
-    const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
-    const uint32_t head = kv * p.group + w.head;
-    if (lane < LANES && e < dim)
-        store_out<4>(a.out, (uint64_t)w.token * a.out.token_stride +
-                                (uint64_t)head * a.out.head_stride + e, y);
-    if (lane == 0 && a.lse != nullptr)
-        a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
 }
 
 template <int DP, bool CAP>
@@ -1481,7 +1522,7 @@ hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
                     a.window);
     const hipError_t e = a.softcap > 0 ? go<true>(a, p, ws, stream) : go<false>(a, p, ws, stream);
     if (e != hipSuccess || p.shares == 0) return e;
-    const dim3 grid(p.tiles * a.cache.kv_heads * ((1u << p.tile_log2) / kWaves)), block(kThreads);
+    const dim3 grid(p.tiles * a.cache.kv_heads * join_pieces(p)), block(kThreads);
     if (a.cache.head_dim <= 64) k_attend_join<16><<<grid, block, 0, stream>>>(a, p, ws);
     else if (a.cache.head_dim <= 128) k_attend_join<32><<<grid, block, 0, stream>>>(a, p, ws);
     else k_attend_join<64><<<grid, block, 0, stream>>>(a, p, ws);

@@ -25,7 +25,7 @@ sz_status check_stream(hipStream_t stream) {
     int current = 0;
     hipDevice_t of = 0;
     if (hipGetDevice(&current) != hipSuccess) return SZ_ERR_HIP;
-    if (stream == nullptr) return SZ_OK;
+    if (stream == nullptr || stream == hipStreamPerThread) return SZ_OK;
     if (hipStreamGetDevice(stream, &of) != hipSuccess) return SZ_ERR_HIP;
     return (int)of == current ? SZ_OK : SZ_ERR_INVALID_ARGUMENT;
 }
@@ -314,7 +314,9 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
         !attend_fits(batch->n_seqs, n, q->heads, cache->kv_heads) ||
         !apart(*q, *out, n, dim, false))
         return SZ_ERR_INVALID_ARGUMENT;
-    if (!(scale > 0) || !std::isfinite(scale) || !(softcap >= 0) || !std::isfinite(softcap) ||
+    // (the kernels multiply by scale log2 e, or 2 scale log2 e / softcap)
+    if (!(scale > 0 && scale < 1e38f) || !(softcap >= 0 && softcap < 1e38f) ||
+        (softcap > 0 && !(scale / softcap < 0.99e38f)) ||
         (window != 0 && !causal) || !aligned(d_lse, 4) || !aligned(d_status, 4))
         return SZ_ERR_INVALID_ARGUMENT;
     const uint64_t most = most_len(*cache);

@@ -41,9 +41,10 @@ struct Turn {
 constexpr uint32_t kWave = 64;
 
 // A page address that may be read or written: the tables hold what the
-// caller put there, and a NULL or misaligned entry is never followed.
+// caller put there, and a NULL, misaligned or impossible entry (addresses
+// have 48 bits, as has the base of a buffer) is never followed.
 __device__ __forceinline__ bool good_page(uint64_t address) {
-    return address != 0 && (address & 15) == 0;
+    return address != 0 && (address & 15) == 0 && address >> 48 == 0;
 }
 
 // The last s in [0, n_seqs) with first(s) <= x, for ascending `first` with
@@ -108,6 +109,7 @@ struct Attend {
     uint32_t causal;
     uint64_t window;
 };
+// Bytes of workspace that launch_attend may use, whatever the window.
 uint64_t attend_workspace(uint32_t q_heads, const Cache& cache, uint64_t n_seqs,
                           uint64_t n_tokens, uint64_t max_len);
 hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream);

@@ -396,6 +396,80 @@ def test_attend_bad_sequences(torch, sz):
     assert st[0] == 1 and st[3] == 0
 
 
+def test_attend_page_addresses_are_checked(torch, sz):
+    """Misaligned addresses and ones of more than 48 bits are never followed."""
+    S = Setup(torch, sz, [(1, 100), (20, 64), (1, 3000)], 8, 2, 128, 16, seed=18)
+    want, _ = sz.attend_pages(S.q.cuda(), S.cache, S.batch)
+    for bad in (lambda x: x + 8, lambda x: x + (1 << 50), lambda x: x | (-1 << 48)):
+        for which in (0, 1):
+            tables = [t.clone() for t in S.cache._keep[:2]]
+            tables[which][2, 100] = bad(tables[which][2, 100])
+            cache = sz.KVCache(*tables, 2, 128, 16, keep=S.cache)
+            out = torch.zeros_like(want)
+            size = sz.sz_attend_workspace_size(8, cache, S.batch)
+            ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+            status = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+            sz.sz_attend_pages(S.q.cuda(), out, None, cache, S.batch, 0, 128 ** -0.5,
+                               workspace=ws, workspace_bytes=size, d_status=status)
+            assert status.tolist() == [0, 0, 1]
+            assert torch.equal(out[:21], want[:21])
+
+
+def test_attend_twice_in_one_workspace(torch, sz):
+    """Two captured graphs with one workspace, replayed one after the other in
+    either order, and eager calls between them."""
+    sets = []
+    for pairs, seed in (([(1, 3000), (1, 17)], 34), ([(5, 900), (1, 4000), (30, 30)], 35)):
+        S = Setup(torch, sz, pairs, 8, 2, 128, 16, seed=seed)
+        sets.append((S, S.q.cuda(), torch.zeros(S.q.shape, dtype=torch.bfloat16, device="cuda"),
+                     sz.attend_pages(S.q.cuda(), S.cache, S.batch)[0]))
+    size = max(sz.sz_attend_workspace_size(8, S.cache, S.batch) for S, *_ in sets)
+    assert size > 0
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def call(S, q, out):
+        sz.sz_attend_pages(q, out, None, S.cache, S.batch, 0, 128 ** -0.5, workspace=ws,
+                           workspace_bytes=size)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for S, q, out, _ in sets:
+            call(S, q, out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for S, q, out, _ in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(S, q, out)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1), (0, 1)):
+        for i in order:
+            sets[i][2].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(sets[i][2], sets[i][3]), order
+        sets[0][2].zero_()
+        call(*sets[0][:3])
+        assert torch.equal(sets[0][2], sets[0][3]), order
+
+
+def test_nothing_to_do(torch, sz):
+    """No tokens, no sequences, and sequences without new tokens."""
+    S = Setup(torch, sz, [(0, 40), (0, 0)], 8, 2, 128, 16, seed=19)
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    out, lse = sz.attend_pages(q, S.cache, S.batch)
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+    k = torch.zeros(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    assert sz.kv_append(k, k, S.cache, S.batch) is None
+    none = sz.Batch(torch.zeros(1, dtype=torch.int32, device="cuda"),
+                    torch.zeros(0, dtype=torch.int32, device="cuda"), 0)
+    sz.attend_pages(q, S.cache, none)
+    sz.kv_append(k, k, S.cache, none)
+    x, _ = sz.qk_norm_rope(q, None, torch.zeros(0, dtype=torch.int32, device="cuda"), sz.rope(128))
+    assert x.shape == q.shape
+    torch.cuda.synchronize()
+
+
 # ---- append, norm and rotation ---------------------------------------------
 
 TURNS = [  # dim, rotary, interleaved, normed

@@ -107,7 +107,8 @@ def test_attend_refuses(sz):
         dict(b=batch(seqs=65536)), dict(b=batch(tokens=1 << 31)),
         dict(b=batch(starts=None)), dict(b=batch(lens=A + 2)),
         dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
-        dict(cap=-1.0), dict(cap=math.nan), dict(cap=math.inf),
+        dict(cap=-1.0), dict(cap=math.nan), dict(cap=math.inf), dict(cap=1e-38, scale=1.0),
+        dict(scale=3e38),
         dict(causal=0, window=5), dict(status=A + 2),
     ]
     for kw in bad:
