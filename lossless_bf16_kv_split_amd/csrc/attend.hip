@@ -112,7 +112,7 @@ constexpr uint64_t kWholeBytes = 288 * 1024;
 constexpr uint64_t kShareSeqs = 1024;
 // and counts steps in 32 bits.
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
-constexpr uint32_t kLeastFew = 1, kLeastTiles = 4;
+constexpr uint32_t kLeastFew = 1, kLeastTiles = 2;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                        uint64_t max_len, uint64_t window) {
@@ -434,10 +434,23 @@ __device__ __forceinline__ float capped(const Score& s, float x) {
     return s.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
 }
 
-// One BF16 word pair with an infinity or a NaN in it
-__device__ __forceinline__ bool odd_pair(uint32_t w) {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+// Infinities and NaN among BF16 word pairs: bits 15 and 31 of the result are
+// set where a half's exponent is all ones (results may be or-ed together)
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    return (w & 0x7F807F80u) + 0x00800080u;
 }
+__device__ __forceinline__ bool any_odd(uint32_t halves) { return (halves & 0x80008000u) != 0; }
+
+// Whether a row sees a key, by the key's offset: the row's keys are low ..
+// high - 1, offsets are from `base`
+struct Sees {
+    uint32_t first, count;
+    __device__ __forceinline__ Sees(int32_t low, int32_t high, int32_t base)
+        : first((uint32_t)(low - base)), count(high > low ? (uint32_t)(high - low) : 0u) {}
+    __device__ __forceinline__ bool operator()(uint32_t offset) const {
+        return offset - first < count;
+    }
+};
 // Such words taken out (0 in their place)
 __device__ __forceinline__ uint32_t plain_pair(uint32_t w) {
     if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
@@ -684,7 +697,7 @@ __device__ __forceinline__ void few_part(const Attend& a, const AttendPlan& p, c
 #pragma unroll
                     for (int i = 0; i < kVec / 2; i++) {
                         if (key < t.lo) x.v[k][u][i] = 0;
-                        odd = odd || odd_pair(x.v[k][u][i]);
+                        odd = odd || any_odd(odd_halves(x.v[k][u][i]));
                     }
             }
             odd = __ballot(odd) != 0;
@@ -710,11 +723,10 @@ __device__ __forceinline__ void few_part(const Attend& a, const AttendPlan& p, c
                 for (int i = 0; i < 8; i++) s[i] *= score.by;
             }
             if (edge) {
+                const Sees sees(low, high, j + 4 * (int32_t)h);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int32_t key = j + 16 * (i / 4) + 4 * (int32_t)h + i % 4;
-                    if (key < low || key >= high) s[i] = -INFINITY;
-                }
+                for (int i = 0; i < 8; i++)
+                    if (!sees(16 * (i / 4) + i % 4)) s[i] = -INFINITY;
             }
             float top = s[0];
 #pragma unroll
@@ -737,11 +749,11 @@ __device__ __forceinline__ void few_part(const Attend& a, const AttendPlan& p, c
 #pragma unroll
             for (int i = 0; i < 4; i++) weights[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
             if (odd) {
+                const Sees sees(low, high, j + 4 * (int32_t)h);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int32_t key = j + 16 * (i / 2) + 4 * (int32_t)h + 2 * (i % 2);
-                    seen[i] = (key >= low && key < high ? 0x3F80u : 0u) |
-                              (key + 1 >= low && key + 1 < high ? 0x3F800000u : 0u);
+                    const uint32_t key = 16 * (i / 2) + 2 * (i % 2);
+                    seen[i] = (sees(key) ? 0x3F80u : 0u) | (sees(key + 1) ? 0x3F800000u : 0u);
                 }
             }
         }
@@ -1072,13 +1084,13 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     const auto rim = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer, uint32_t spare) {
         const uint32_t ka = k_lane + k_buffer * kBuffer;
         const uint32_t values = lds0 + (2 + v_buffer) * kBuffer;
-        bool odd = false;
-#pragma unroll 4
+        uint32_t halves = 0;
+#pragma unroll 8
         for (int i = 0; i < (int)(kBuffer / 1024); i++) {
             const u32x4 x = *(const SZ_LDS u32x4*)(uintptr_t)(values + 1024 * i + 16 * lane);
-            odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
+            halves |= odd_halves(x.x) | odd_halves(x.y) | odd_halves(x.z) | odd_halves(x.w);
         }
-        odd = __ballot(odd) != 0;
+        const bool odd = __ballot(any_odd(halves)) != 0;
         if (odd) {
 #pragma unroll 1
             for (int i = 0; i < (int)(kBuffer / 1024); i++) {
@@ -1102,16 +1114,16 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                         keys_at(ka + 32 * k * kRow, c), q[b][c], s[k], 0, 0, 0);
                     // (or all the operands are read at once, into registers
                     // that the other loop misses)
-                    if (c % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    if (c % 8 == 7) __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            const Sees sees(low[b], high[b], j + 4 * (int32_t)h);
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
-                    const int32_t key = j + 32 * k + 8 * (i / 4) + 4 * (int32_t)h + i % 4;
-                    s[k][i] = key < low[b] || key >= high[b] ? -INFINITY : scored(s[k][i]);
+                    s[k][i] = sees(32 * k + 8 * (i / 4) + i % 4) ? scored(s[k][i]) : -INFINITY;
                     top = fmaxf(top, s[k][i]);
                 }
             follow(b, top * by);
@@ -1139,19 +1151,20 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
             if (odd) {
 #pragma unroll 1
                 for (int k = 0; k < kKeys; k++) {
-                    const bool sees = j + k >= low[b] && j + k < high[b];
+                    const bool seen = j + k >= low[b] && j + k < high[b];
 #pragma unroll
                     for (int d = 0; d < kParts; d++)
 #pragma unroll
                         for (int g = 0; g < 4; g++) {
                             const u32x2 w = *(const SZ_LDS u32x2*)(uintptr_t)(
                                 values + k * kRow + ((4 * d + g) ^ v_mix<DP>(k)) * 16 + 8 * h);
-                            if (__ballot(sees && (odd_pair(w.x) || odd_pair(w.y))) == 0) continue;
+                            if (__ballot(seen && any_odd(odd_halves(w.x) | odd_halves(w.y))) == 0)
+                                continue;
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const float x = __uint_as_float(
                                     e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-                                if (sees && !(fabsf(x) <= FLT_MAX)) o[b][d][4 * g + e] += x;
+                                if (seen && !(fabsf(x) <= FLT_MAX)) o[b][d][4 * g + e] += x;
                             }
                         }
                 }
