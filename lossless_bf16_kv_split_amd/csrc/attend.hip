@@ -103,15 +103,22 @@ constexpr uint32_t kStep = 128;  // keys
 constexpr uint64_t kCus = 256;
 // The work is shared out among as many workgroups as the chip holds at once:
 // two a CU, one with 256-element heads.  Whole tiles where there are enough
-// of them to even out, or where a tile's keys and values are few bytes: one
-// workgroup reads them (at about 50 GB/s, what one CU gets) in the time that
-// the second launch would take.
+// of them to even out (kManyFew, kManyTiles), or where a tile has so few keys
+// that one workgroup is done with them in the time that the second launch
+// would take.  Few rows: by the bytes, which one CU gets at about 50 GB/s (9
+// sequences of 5 tokens under a window of 1024, 64 elements, 264 KB a tile:
+// 10.6 us whole, 14.4 shared out; 777 keys of 128, 398 KB: 12.1 and 11.2).
+// Tiles of 128 rows: 128 elements, 896 keys: 23.7 us whole, 30.1 shared out;
+// 1500: 35.5 and 22.5; 256 elements, 319 keys: 22.7 and 30.4; 565: 32.1 and
+// 29.5; 64 elements (whose steps cost nearly what 128 do), 1100: 20.9, 19.4.
 constexpr uint64_t kManyFew = 4096, kManyTiles = 512;
-constexpr uint64_t kWholeBytes = 288 * 1024;
+constexpr uint64_t kWholeFew = 288 * 1024, kWholeTiles = 480 * 1024;
 // Sharing out looks at every sequence in every workgroup, 64 at a time.
 constexpr uint64_t kShareSeqs = 1024;
 // and counts steps in 32 bits.
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
+// The fewest steps of a share (a share of few rows costs about 5 us before
+// its first step and 1 us a step; one of a tile 8 and 2.5)
 constexpr uint32_t kLeastFew = 1, kLeastTiles = 2;
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
@@ -134,10 +141,11 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     const uint64_t full = rows >> p.tile_log2;
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
     const uint64_t resident = c.head_dim > 128 ? kCus : 2 * kCus;
+    const uint64_t width = p.few() || c.head_dim > 128 ? c.head_dim : 128;
     const bool whole = n_seqs > kShareSeqs || c.kv_heads > resident ||
                        groups >= (p.few() ? kManyFew : kManyTiles) || p.tile_log2 == 8 ||
                        p.tiles * (max_len / kStep + 2) >= kMostSteps ||
-                       keys * c.head_dim * 4 <= kWholeBytes;
+                       keys * width * 4 <= (p.few() ? kWholeFew : kWholeTiles);
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
     p.least = p.few() ? kLeastFew : kLeastTiles;
     p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
