@@ -94,7 +94,7 @@ struct AttendPlan {
     uint32_t tile_log2;
     uint32_t tiles;      // a bound of the tiles' numbers
     uint32_t shares;     // workgroups that share it out for a KV head; 0: whole tiles
-    uint32_t least;      // the fewest steps of a share
+    uint32_t alone;      // up to so many steps in all, shares of one step
     bool wide;           // few rows, whole tiles, a CU each: eight waves
     __host__ __device__ bool few() const { return tile_log2 == 4; }
 };
@@ -117,9 +117,10 @@ constexpr uint64_t kWholeFew = 288 * 1024, kWholeTiles = 480 * 1024;
 constexpr uint64_t kShareSeqs = 1024;
 // and counts steps in 32 bits.
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
-// The fewest steps of a share (a share of few rows costs about 5 us before
-// its first step and 1 us a step; one of a tile 8 and 2.5)
-constexpr uint32_t kLeastFew = 1, kLeastTiles = 2;
+// Shares of one step only where all of them find a CU for themselves, of a
+// 128-row tile never: twice the parts to join and to write cost more (32 / 8
+// heads of 128 elements, one token: 4096 keys 13.6 us in shares of one step,
+// 14.4 of two; 8192 keys 18.1 and 15.8; 64 tokens on 4096: 32.0 and 26.3).
 
 AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t n_tokens,
                        uint64_t max_len, uint64_t window) {
@@ -147,7 +148,7 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
                        p.tiles * (max_len / kStep + 2) >= kMostSteps ||
                        keys * width * 4 <= (p.few() ? kWholeFew : kWholeTiles);
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
-    p.least = p.few() ? kLeastFew : kLeastTiles;
+    p.alone = p.few() ? (uint32_t)(kCus / c.kv_heads) : 0;
     p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
     return p;
 }
@@ -287,7 +288,7 @@ struct Shares {
         tiles0 = tiles1 - tiles;
         total = from_lane(steps1, kWave - 1);
         quota = (total + p.shares - 1) / p.shares;
-        quota = quota < p.least ? p.least : quota;
+        if (quota == 1 && total > p.alone) quota = 2;
     }
 
     // A sequence: by one of its steps, or one of its tiles
