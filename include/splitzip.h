@@ -535,7 +535,8 @@ sz_status sz_qk_norm_rope(const sz_heads *q, const sz_heads *q_out, const float 
  * have cache->kv_heads heads; every other argument as in sz_qk_norm_rope.
  *   d_status  optional device i32[n_seqs]: SZ_OK, or
  *             SZ_ERR_INVALID_ARGUMENT for a sequence whose starts are out
- *             of order or range, whose length is below its new tokens' count
+ *             of range or order (an earlier start lies above its first row,
+ *             a later one below its end), whose length is below its new tokens' count
  *             or past its pages, or one of whose written pages is NULL or
  *             misaligned.  Of such a sequence the tokens that have no place
  *             are not written and the others may be; nothing outside valid
@@ -574,7 +575,8 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  *             that may overlap need workspaces of their own.
  *   d_status  optional device i32[n_seqs]: SZ_OK, or
  *             SZ_ERR_INVALID_ARGUMENT for a sequence whose starts are out
- *             of order or range, whose length is negative or above max_len,
+ *             of range or order (an earlier start lies above its first row,
+ *             a later one below its end), whose length is negative or above max_len,
  *             or one of whose pages with a visible token is NULL or
  *             misaligned.  The outputs of such a sequence are unspecified;
  *             nothing outside valid pages is read.

@@ -18,6 +18,8 @@
 // and walks rows of it.
 #include "kv_internal.h"
 
+#include <cstdint>
+
 namespace sz {
 namespace {
 
@@ -275,30 +277,46 @@ hipError_t launch(const TurnRows& a, const Cache& cache, const Batch& batch, hip
     return pick<kHalves, APPEND>(a, cache, batch, stream);
 }
 
-__global__ __launch_bounds__(kWave) void k_check_seqs(SeqCheck c) {
-    const uint32_t s = blockIdx.x, lane = threadIdx.x;
-    const Seq q = load_seq(c.batch, s, c.max_len);
-    bool good = q.good;
-    if (good) {
-        const int64_t first_new = (int64_t)q.len - (q.end - q.begin);
-        int64_t from = 0;
-        if (c.append) {
-            if (first_new < 0) good = false;
-            from = first_new;
-        } else if (c.causal && c.window != 0 && (uint64_t)first_new + 1 > c.window &&
-                   first_new >= 0) {
-            from = first_new + 1 - (int64_t)c.window;
-        }
-        if (good && q.begin < q.end && from < q.len) {
-            const uint64_t row = (uint64_t)s * c.cache.table_pitch;
-            const uint64_t last = (uint64_t)(q.len - 1) >> c.cache.page_log2;
-            for (uint64_t p = ((uint64_t)from >> c.cache.page_log2) + lane; p <= last; p += kWave)
-                good = good && good_page(c.cache.k_pages[row + p]) &&
-                       good_page(c.cache.v_pages[row + p]);
-        }
+// Sequences are found by a search over their starts, which finds one's rows
+// for certain where no start before its own lies above it and none after
+// lies below its end.  A wave takes `each` (at most 32) sequences: it reads
+// all starts once, 64 at a time, and compares its own among themselves.
+__global__ __launch_bounds__(kWave) void k_check_seqs(SeqCheck c, uint32_t each) {
+    const uint32_t lane = threadIdx.x, s0 = blockIdx.x * each, n = c.batch.n_seqs;
+    const uint32_t s1 = n - s0 < each ? n : s0 + each;
+    int32_t top = INT32_MIN, low = INT32_MAX;
+    for (uint32_t i = lane; i <= n; i += kWave) {
+        const int32_t x = c.batch.starts[i];
+        if (i < s0) top = x > top ? x : top;
+        if (i > s1) low = x < low ? x : low;
     }
-    const bool all = __ballot(!good) == 0;
-    if (lane == 0) c.status[s] = all ? kSeqGood : kBlockInvalid;
+    const int32_t own = s0 + lane <= s1 ? c.batch.starts[s0 + lane] : 0;
+    for (uint32_t s = s0; s < s1; s++) {
+        const Seq q = load_seq(c.batch, s, c.max_len);
+        bool good = q.good && top <= q.begin && low >= q.end;
+        if (s0 + lane <= s1) good = good && (s0 + lane <= s ? own <= q.begin : own >= q.end);
+        if (good) {
+            const int64_t first_new = (int64_t)q.len - (q.end - q.begin);
+            int64_t from = 0;
+            if (c.append) {
+                if (first_new < 0) good = false;
+                from = first_new;
+            } else if (c.causal && c.window != 0 && (uint64_t)first_new + 1 > c.window &&
+                       first_new >= 0) {
+                from = first_new + 1 - (int64_t)c.window;
+            }
+            if (good && q.begin < q.end && from < q.len) {
+                const uint64_t row = (uint64_t)s * c.cache.table_pitch;
+                const uint64_t last = (uint64_t)(q.len - 1) >> c.cache.page_log2;
+                for (uint64_t p = ((uint64_t)from >> c.cache.page_log2) + lane; p <= last;
+                     p += kWave)
+                    good = good && good_page(c.cache.k_pages[row + p]) &&
+                           good_page(c.cache.v_pages[row + p]);
+            }
+        }
+        const bool all = __ballot(!good) == 0;
+        if (lane == 0) c.status[s] = all ? kSeqGood : kBlockInvalid;
+    }
 }
 
 }  // namespace
@@ -315,7 +333,8 @@ hipError_t launch_append(const TurnRows& a, const Cache& cache, const Batch& bat
 
 hipError_t launch_check_seqs(const SeqCheck& c, hipStream_t stream) {
     if (c.batch.n_seqs == 0) return hipSuccess;
-    k_check_seqs<<<dim3(c.batch.n_seqs), dim3(kWave), 0, stream>>>(c);
+    const uint32_t each = (c.batch.n_seqs + 2047) / 2048;
+    k_check_seqs<<<dim3((c.batch.n_seqs + each - 1) / each), dim3(kWave), 0, stream>>>(c, each);
     return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@
 #include "kv_internal.h"
 
 #include <cfloat>
+#include <cstdint>
 
 namespace sz {
 namespace {
@@ -227,15 +228,23 @@ struct Shares {
     uint32_t quota;
     // this lane's sequences: steps and tiles before them, and with them
     uint32_t steps0, steps1, tiles0, tiles1;
+    int32_t before;       // the largest start before them
     Load own;             // each == 1: the lane's sequence
 
-    static __device__ __forceinline__ Load load(const Attend& a, const AttendPlan& p, uint32_t s) {
+    // (no sequence begins before an earlier one's start: those that remain
+    // lie apart from each other, whatever the starts, so that their tiles and
+    // steps stay within what the host counted on)
+    static __device__ __forceinline__ int32_t start(const Attend& a, uint32_t s) {
+        return s < a.batch.n_seqs ? a.batch.starts[s] : INT32_MIN;
+    }
+    static __device__ __forceinline__ Load load(const Attend& a, const AttendPlan& p, uint32_t s,
+                                                int32_t begin, int32_t before) {
         Load x{};
         if (s >= a.batch.n_seqs) return x;
-        x.q.begin = a.batch.starts[s];
+        x.q.begin = begin;
         x.q.end = a.batch.starts[s + 1];
         x.q.len = a.batch.lens[s];
-        x.q.good = x.q.begin >= 0 && x.q.begin < x.q.end &&
+        x.q.good = x.q.begin >= 0 && x.q.begin >= before && x.q.begin < x.q.end &&
                    x.q.end <= (int64_t)a.batch.n_tokens && x.q.len >= 0 && x.q.len <= a.max_len;
         if (!x.q.good) return x;
         const int64_t rows = (int64_t)(x.q.end - x.q.begin) * p.group;
@@ -263,6 +272,22 @@ struct Shares {
         return x;
     }
 
+    // the largest value up to a lane
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ int32_t most(int32_t x) {
+        const int32_t y = __builtin_amdgcn_update_dpp(INT32_MIN, x, CTRL, ROWS, 0xF, false);
+        return x > y ? x : y;
+    }
+    static __device__ __forceinline__ int32_t scan_most(int32_t x) {
+        x = most<0x111, 0xF>(x);
+        x = most<0x112, 0xF>(x);
+        x = most<0x114, 0xF>(x);
+        x = most<0x118, 0xF>(x);
+        x = most<0x142, 0xA>(x);
+        x = most<0x143, 0xC>(x);
+        return x;
+    }
+
     static __device__ __forceinline__ uint32_t from_lane(uint32_t x, uint32_t lane) {
         return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
     }
@@ -271,13 +296,26 @@ struct Shares {
         const uint32_t lane = threadIdx.x % kWave;
         each = (a.batch.n_seqs + kWave - 1) / kWave;
         uint32_t steps = 0, tiles = 0;
+        before = INT32_MIN;
         if (each == 1) {
-            own = load(a, p, lane);
+            const int32_t begin = start(a, lane);
+            own = load(a, p, lane, begin, scan_most(begin));
             steps = own.tiles * own.steps;
             tiles = own.tiles;
         } else {
+            int32_t top = INT32_MIN;
             for (uint32_t i = 0; i < each; i++) {
-                const Load x = load(a, p, lane * each + i);
+                const int32_t begin = start(a, lane * each + i);
+                top = begin > top ? begin : top;
+            }
+            top = scan_most(top);
+            before = __shfl_up(top, 1);
+            if (lane == 0) before = INT32_MIN;
+            top = before;
+            for (uint32_t i = 0; i < each; i++) {
+                const int32_t begin = start(a, lane * each + i);
+                const Load x = load(a, p, lane * each + i, begin, top);
+                top = begin > top ? begin : top;
                 steps += x.tiles * x.steps;
                 tiles += x.tiles;
             }
@@ -311,7 +349,10 @@ struct Shares {
         Load x = own;
         if (each > 1) {
             const uint32_t mine = threadIdx.x % kWave, first = lane * each;
-            x = load(a, p, mine < each ? first + mine : a.batch.n_seqs);
+            const uint32_t s = mine < each ? first + mine : a.batch.n_seqs;
+            const int32_t begin = start(a, s), top = scan_most(begin);
+            const int32_t base = (int32_t)from_lane((uint32_t)before, lane);
+            x = load(a, p, s, begin, top > base ? top : base);
             const uint32_t steps = x.tiles * x.steps;
             const uint32_t s1 = scan(steps) + f.steps0, t1 = scan(x.tiles) + f.tiles0;
             lane = first_past(s1, t1);

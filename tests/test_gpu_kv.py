@@ -785,3 +785,65 @@ def test_other_streams(torch, sz):
     torch.cuda.synchronize()
     for a, w in zip(args, want):
         assert torch.equal(a[1], w[0]) and torch.equal(a[2], w[1])
+
+
+@pytest.mark.parametrize("n", [40, 64, 65, 300])
+@pytest.mark.parametrize("new", [4, 900])
+def test_attend_starts_out_of_order(torch, sz, n, new):
+    """Ranges of rows that lie over one another, as wrong starts can make
+    them: reported, nothing written past the workspace, and a sequence whose
+    rows lie apart from the rest is answered."""
+    page, width = 16, 160
+    S = Setup(torch, sz, [(new, 2400)], 8, 2, 128, page, seed=31, before=n)
+    S.ids = S.ids[:, :1].new_full((1, width), -1).index_put(
+        (torch.tensor(0), torch.arange(S.ids.shape[1])), S.ids[0])
+    for spread in ("over all rows", "apart"):
+        hi = S.n if spread == "over all rows" else n
+        starts = [0 if s % 2 == 0 else hi for s in range(n)] + [n, S.n]
+        if n % 2 == 1 and spread == "over all rows":
+            starts[n] = 0
+        view = [ref.page_view(p, S.shape, True) for p in (S.kd, S.vd)]
+        cache = sz.paged_cache(view[0], view[1], S.ids.expand(n + 1, width).cuda())
+        i32 = dict(dtype=torch.int32, device="cuda")
+        batch = sz.Batch(torch.tensor(starts, **i32), torch.full((n + 1,), 2400, **i32), S.n)
+        out = torch.full(S.q.shape, SENTINEL, dtype=torch.bfloat16, device="cuda")
+        size = sz.sz_attend_workspace_size(8, cache, batch, 2400)
+        assert size > 0
+        ws = torch.full((size + (1 << 22),), 0xFF, dtype=torch.uint8, device="cuda")
+        status = torch.full((n + 1,), -1, dtype=torch.int32, device="cuda")
+        say("out of order", n, new, spread, "workspace", size)
+        sz.sz_attend_pages(S.q.cuda(), out, None, cache, batch, 2400, 128 ** -0.5, workspace=ws,
+                           workspace_bytes=size, d_status=status)
+        torch.cuda.synchronize()
+        assert bool((ws[size:] == 0xFF).all())
+        st = status.tolist()
+        assert sum(st[:n]) >= n - 2
+        if spread == "apart":
+            assert st[n] == 0
+            want, _, tol, _ = ref.attend(S.q[n:], S.rows(S.k, 0), S.rows(S.v, 0), 2400,
+                                         128 ** -0.5)
+            assert bool(((out[n:].cpu().double() - want).abs() <= tol).all())
+        elif n % 2 == 0:
+            assert st[n] == 1
+
+
+def test_append_starts_out_of_order(torch, sz):
+    """Every sequence that is reported good is written whole."""
+    S = Setup(torch, sz, [(n, 40) for n in (3, 2, 4, 5, 1)], 8, 2, 128, 16, seed=32)
+    k = S.rand(S.n, 2, 128).bfloat16().cuda()
+    for starts in ([0, 3, 5, 9, 14, 15], [0, 3, 2, 9, 14, 15], [0, 12, 5, 9, 14, 15],
+                   [0, 3, 5, 1, 14, 15], [0, 3, 5, 9, 14, -1], [15, 0, 3, 5, 9, 14]):
+        S.upload()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        batch = sz.Batch(torch.tensor(starts, **i32), torch.full((5,), 40, **i32), S.n)
+        status = torch.full((5,), -1, dtype=torch.int32, device="cuda")
+        sz.sz_kv_append(k, k, None, None, None, None, 0.0, None, None, S.cache, batch, status)
+        torch.cuda.synchronize()
+        for s, st in enumerate(status.tolist()):
+            a, b = starts[s], starts[s + 1]
+            apart = a <= b and all(x <= a for x in starts[:s]) and \
+                all(x >= b for x in starts[s + 1:]) and 0 <= a and b <= S.n
+            assert st == (0 if apart else 1), (starts, s)
+            if apart:
+                for pool in (S.kd, S.vd):
+                    assert torch.equal(S.rows(pool.cpu(), s)[40 - (b - a):], k[a:b].cpu())
