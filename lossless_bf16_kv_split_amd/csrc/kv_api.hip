@@ -321,6 +321,7 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
         return SZ_ERR_INVALID_ARGUMENT;
     const uint64_t most = most_len(*cache);
     if (max_len == 0 || max_len > most) max_len = most;
+    if (window > kMaxLen) window = 0;  // (it hides nothing; the kernels count in 32 bits)
     if (overlap(d_lse, d_lse == nullptr ? 0 : 4 * n * q->heads, span(*q, n, dim)) ||
         overlap(d_lse, d_lse == nullptr ? 0 : 4 * n * q->heads, span(*out, n, dim)))
         return SZ_ERR_INVALID_ARGUMENT;

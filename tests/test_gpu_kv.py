@@ -847,3 +847,11 @@ def test_append_starts_out_of_order(torch, sz):
             if apart:
                 for pool in (S.kd, S.vd):
                     assert torch.equal(S.rows(pool.cpu(), s)[40 - (b - a):], k[a:b].cpu())
+
+
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 + 5, 2 ** 32, 2 ** 63, 2 ** 64 - 1])
+def test_attend_windows_past_any_length(torch, sz, window):
+    S = Setup(torch, sz, [(1, 300), (70, 500)], 8, 2, 128, 16, seed=33)
+    want, want_lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch)
+    out, lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch, window=window)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
