@@ -558,8 +558,8 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  * Scores, the softmax's maximum and sum, and the accumulated output are
  * FP32; the weights are rounded to BF16 before they multiply the values.
  *   q         BF16, batch->n_tokens tokens, heads a multiple of kv_heads;
- *             n_tokens * heads < 2^31, and n_tokens * heads / 16 + n_seqs *
- *             kv_heads < 2^31
+ *             n_tokens * heads < 2^31, and n_tokens * heads / 128 + 2 *
+ *             n_seqs * kv_heads < 2^24
  *   out       BF16 or F32, as many heads
  *   d_lse     optional device float[n_tokens][q heads]: ln of the sum of
  *             exp(score) over the visible keys

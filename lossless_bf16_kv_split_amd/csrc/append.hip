@@ -33,6 +33,8 @@ constexpr uint32_t kWavesPerGroup = kThreads / kWave;
 // 42, 42, 44, 58).  Stores stay cached: attention reads the rows next
 // (non-temporal ones save 3 to 5% of this kernel).
 constexpr uint64_t kFillWaves = 16384;
+// Tokens of a launch, a wave each where there are so many
+constexpr uint64_t kMostTokens = uint64_t{1} << 25;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -105,12 +107,12 @@ enum { kNoTurn = 0, kHalves = 1, kInterleaved = 2 };
 // LANES lanes hold a row, VEC elements each; slices waves share a token.
 template <int LANES, int VEC, int MODE, bool APPEND>
 __global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batch batch,
-                                                   uint32_t slices) {
+                                                   uint32_t slices, uint32_t first) {
     constexpr uint32_t kRows = kWave / LANES;  // rows a wave holds at once
     const uint32_t lane = threadIdx.x % kWave;
     const uint64_t wave =
         (uint64_t)blockIdx.x * kWavesPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint64_t token = wave / slices;
+    const uint64_t token = first + wave / slices;
     const uint32_t slice = (uint32_t)(wave % slices);
     if (token >= a.n_tokens) return;
 
@@ -245,10 +247,15 @@ hipError_t go(const TurnRows& a, const Cache& cache, const Batch& batch, hipStre
     const uint64_t most = (rows + kWave / LANES - 1) / (kWave / LANES);
     uint64_t slices = (kFillWaves + a.n_tokens - 1) / a.n_tokens;
     slices = slices < 1 ? 1 : slices > most ? most : slices;
-    const uint64_t groups = (a.n_tokens * slices + kWavesPerGroup - 1) / kWavesPerGroup;
-    k_turn<LANES, VEC, MODE, APPEND>
-        <<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a, cache, batch, (uint32_t)slices);
-    return hipGetLastError();
+    // (a launch holds fewer than 2^32 threads)
+    for (uint64_t first = 0; first < a.n_tokens; first += kMostTokens) {
+        const uint64_t tokens = a.n_tokens - first < kMostTokens ? a.n_tokens - first : kMostTokens;
+        const uint64_t groups = (tokens * slices + kWavesPerGroup - 1) / kWavesPerGroup;
+        k_turn<LANES, VEC, MODE, APPEND><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(
+            a, cache, batch, (uint32_t)slices, (uint32_t)first);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
 }
 
 // Lanes per row: the least power of two that holds it.  A lane's elements

@@ -157,9 +157,12 @@ uint64_t most_len(const sz_kv_cache& c) {
     return n > kMaxLen ? kMaxLen : n;
 }
 
-// Attention counts a call's rows, and its tiles for every KV head, in 31 bits
+// Attention counts a call's rows in 31 bits, and a launch has fewer than 2^32
+// threads: 256 for a tile of a KV head, rows / 16 + n_seqs of them where rows
+// <= 16 n_seqs, rows / 128 + n_seqs otherwise.
 bool attend_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t q_heads, uint64_t kv_heads) {
-    return n_tokens * q_heads <= kMaxTokens && n_tokens * q_heads / 16 + n_seqs * kv_heads <= kMaxTokens;
+    return n_tokens * q_heads <= kMaxTokens &&
+           n_tokens * q_heads / 128 + 2 * n_seqs * kv_heads < uint64_t{1} << 24;
 }
 
 }  // namespace

@@ -855,3 +855,27 @@ def test_attend_windows_past_any_length(torch, sz, window):
     want, want_lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch)
     out, lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch, window=window)
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_more_tokens_than_one_launch_takes(torch, sz):
+    """2^26 and some rows, against the same rows in calls of their own."""
+    n, page, R = (1 << 26) + 5, 65536, sz.rope(8)
+    x = (torch.arange(n, dtype=torch.int32, device="cuda") * 40503).to(torch.int16)
+    x = (x & 0x3FFF).view(torch.bfloat16).view(n, 1, 1).expand(n, 1, 8).contiguous()
+    positions = torch.arange(n, dtype=torch.int32, device="cuda")
+    say("rotation of", n)
+    out, _ = sz.qk_norm_rope(x, None, positions, R)
+    spots = [(0, 3), ((1 << 25) - 3, (1 << 25) + 3), ((1 << 26) - 3, n)]
+    for a, b in spots:
+        want, _ = sz.qk_norm_rope(x[a:b], None, positions[a:b], R)
+        assert torch.equal(out[a:b].view(torch.int16), want.view(torch.int16)), a
+    pool = torch.zeros(1025, page, 1, 8, dtype=torch.bfloat16, device="cuda")
+    cache = sz.paged_cache(pool, pool, torch.arange(1025, device="cuda").view(1, -1))
+    batch = sz.Batch(torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                     torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    say("append of", n)
+    sz.kv_append(out, out, cache, batch)    # (keys and values to the same pages)
+    got = pool.view(-1, 1, 8)
+    for a, b in spots:
+        assert torch.equal(got[a:b].view(torch.int16), out[a:b].view(torch.int16)), a
+    assert bool((got[n:] == 0).all())

@@ -258,3 +258,14 @@ def test_rope_frequencies(sz):
                 (64, 1e4, 3, 2.0, 0.0), (64, 1e4, 3, 2.0, 4096.0, 0.0), (64, 1e4, 4, 2.0, 4096.0, 4.0, 1.0)):
         with pytest.raises(sz.SplitZipError):
             sz.sz_rope_frequencies(*bad)
+
+
+def test_attend_refuses_more_than_a_launch(sz):
+    def call(seqs, kv_heads, tokens):
+        c = cache(kv_heads=kv_heads, dim=8, head_stride=8, token_stride=8 * kv_heads)
+        b = batch(seqs=seqs, tokens=tokens)
+        h = dict(n=kv_heads, head_stride=8, token_stride=8 * kv_heads)
+        assert sz._lib.sz_attend_workspace_size(kv_heads, at(c), at(b), 0) == 0
+        return attend(sz, c=c, b=b, q=heads(A + (1 << 42), **h), out=heads(A + (1 << 45), **h))
+    assert call(65535, 128, 65535) == 1
+    assert call(1, 128, 1 << 24) == 1
