@@ -534,6 +534,8 @@ def sz_rope_frequencies(rotary_dim: int, base: float, stretch: int = SZ_ROPE_PLA
                         factor: float = 1.0, original_len: float = 0.0, slow: float = 1.0,
                         fast: float = 32.0):
     """Angles per position (a list of rotary_dim / 2 floats) and magnitude."""
+    if not 0 <= rotary_dim < 1 << 32:  # (ctypes would cut it to 32 bits)
+        raise SplitZipError(SZ_ERR_INVALID_ARGUMENT, "sz_rope_frequencies")
     out = (ctypes.c_double * max(1, rotary_dim // 2))()
     magnitude = ctypes.c_float()
     _check(_lib.sz_rope_frequencies(rotary_dim, base, stretch, factor, original_len, slow, fast,

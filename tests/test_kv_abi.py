@@ -269,3 +269,11 @@ def test_attend_refuses_more_than_a_launch(sz):
         return attend(sz, c=c, b=b, q=heads(A + (1 << 42), **h), out=heads(A + (1 << 45), **h))
     assert call(65535, 128, 65535) == 1
     assert call(1, 128, 1 << 24) == 1
+
+
+@pytest.mark.parametrize("dims", [0, -2, -128, 2 ** 32 + 2])
+def test_rope_frequencies_of_impossible_sizes(sz, dims):
+    with pytest.raises(sz.SplitZipError):
+        sz.sz_rope_frequencies(dims, 10000.0)
+    with pytest.raises(sz.SplitZipError):
+        sz.rope(dims)
