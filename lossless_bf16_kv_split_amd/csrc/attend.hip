@@ -938,15 +938,19 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
 // of a step go from the pages straight to LDS (each wave fetches a block of
 // 16 keys) while the step before is worked on, with one barrier a step.
 //
-// Bound by power: with the matrix cores busy 55% of the cycles the clock falls
-// to 1.73 GHz (2.13 with a kernel that kept them busy 42%), so what counts is
-// fewer instructions and fewer reads for the same products.  Measured: 1.0 to
-// 1.05 PFLOP/s on prompts (a library product of 8192^3: 1.40).  The tile of
-// 128 rows leaves room for two workgroups a CU (at most 128 KB of LDS and 256
-// registers a lane for both), which hide each other's barriers and latencies;
-// the one of 256 reads LDS and L2 half as often for the same products and is 3%
-// faster where there are many of them (2048 rows of 64 heads over 32768 keys:
-// 1.95 against 2.01 ms).
+// Bound by power: at 0.95 PFLOP/s under the counters the matrix cores are busy
+// 48% of the cycles, the vector units 41%, and the clock falls from 2.4 to
+// 2.0 GHz (1.73 with a kernel that kept the former busy 55%), so what counts
+// is fewer instructions and fewer reads for the same products.  Measured:
+// 2048 tokens of 64 heads on 32768 keys 1.92 to 1.98 ms (1.08 to 1.11 PFLOP/s),
+// a prompt of 8192 tokens of 32 heads 0.53 to 0.55 ms (1.00 to 1.04); a library
+// product of 8192^3: 1.40.  With a cap on the scores, two more transcendental
+// instructions each, a fifth slower.  The tile of 128 rows leaves room for two
+// workgroups a CU (at most 128 KB of LDS and 256 registers a lane for both),
+// which hide each other's barriers and latencies; the one of 256 reads LDS and
+// L2 half as often for the same products and is 3% faster where there are many
+// of them.  Heads of 256 elements have one workgroup of 128 rows a CU: 0.86
+// PFLOP/s on 2048 tokens of 16 heads over 8192 keys.
 //
 // Matrix operands of 32x32x16: lane (n = lane % 32, h = lane / 32) holds eight
 // of 16 contraction terms of row n.
@@ -1352,6 +1356,10 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     if (in0 >= in1) in0 = in1 = steps;
     if (SHARED) arrived();  // (every wave is done with the part before)
     if (steps > 0) fetch_step(first, 0, 0);
+    // (waves without rows, of a token among chunks, leave LDS to the others:
+    // 24 tokens and two chunks of 833, 256 elements, capped, 137 -> 132 us;
+    // whole tiles run 2% slower with the test)
+    const bool works = !SHARED || 32 * QB * (int32_t)wave < t.rows;
     int32_t x = 0;
     uint32_t vb = 0;  // x % 3
     const auto begin_step = [&] {
@@ -1374,18 +1382,22 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         Half even, uneven;
         uint32_t va = v_lane + vb * kBuffer;
         begin_step();
-        ahead(even, k_lane + (x & 1) * kBuffer);
-        inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
+        if (works) {
+            ahead(even, k_lane + (x & 1) * kBuffer);
+            inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
+        }
         end_step();
         while (x < in1) {
             const uint32_t ka = k_lane + (x & 1) * kBuffer;
             begin_step();
-            inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
-            va = v_lane + vb * kBuffer;
-            inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
+            if (works) {
+                inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
+                va = v_lane + vb * kBuffer;
+                inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
+            }
             end_step();
         }
-        inner(uneven, even, 0, va + 32 * kRow, std::false_type{});
+        if (works) inner(uneven, even, 0, va + 32 * kRow, std::false_type{});
     }
     // nothing may still be on its way to this workgroup's LDS when it ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1454,9 +1466,12 @@ __host__ __device__ inline uint32_t join_pieces(const AttendPlan& p) {
 
 // Joins the parts of the tiles that were cut, a row to a wave at a time (of a
 // 128-row tile four, one after the other: a workgroup's way to its tile takes
-// longer than a row).  64 parts at a time, a lane holds one's maximum and sum; LANES lanes take four elements
-// each of one's sums, so that a wave reads 64 / LANES of them at a time, with
-// nothing to wait for between them.
+// longer than a row).  64 parts at a time, a lane holds one's maximum and sum;
+// LANES lanes take four elements each of one's sums, so that a wave reads
+// 64 / LANES of them at a time, and four times as many with nothing to wait
+// for between them (16 times: no faster with 64 parts, 1 us slower with
+// few).  Latency bound: 3 us of a short call, 6 where 48 sequences' tiles
+// were cut.
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p, uint8_t* ws) {
     constexpr uint32_t kAtOnce = kWave / LANES, kBatch = 4;
