@@ -607,9 +607,9 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // streams every fourth (or eighth) block of 32 keys straight from the pages
 // into registers, with the next block's loads in flight, and the waves'
 // results are joined in LDS at the end.  Bound by the bytes of the cache: 48
-// sequences of 130 to 8192 keys, 908 MB, take 166 us (5.5 TB/s; a large copy
-// moves 4.8), two of 32768, 264 MB, 54 us with the join.  A short cache is
-// bound by the chain of loads (lengths, page addresses, keys): about 6 us,
+// sequences of 130 to 8192 keys, 908 MB, take 168 us (5.4 TB/s; a large copy
+// moves 4.8), two of 32768, 264 MB, 55 us with the join.  A short cache is
+// bound by the chain of loads (lengths, page addresses, keys): about 7 us,
 // and 3 for the join.
 //
 // Matrix operands of 16x16x32: lane (n = lane % 16, h = lane / 16) holds
@@ -938,14 +938,14 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
 // of a step go from the pages straight to LDS (each wave fetches a block of
 // 16 keys) while the step before is worked on, with one barrier a step.
 //
-// Bound by power: at 0.95 PFLOP/s under the counters the matrix cores are busy
+// Bound by power: at 1.0 PFLOP/s under the counters the matrix cores are busy
 // 48% of the cycles, the vector units 41%, and the clock falls from 2.4 to
 // 2.0 GHz (1.73 with a kernel that kept the former busy 55%), so what counts
 // is fewer instructions and fewer reads for the same products.  Measured:
 // 2048 tokens of 64 heads on 32768 keys 1.92 to 1.98 ms (1.08 to 1.11 PFLOP/s),
 // a prompt of 8192 tokens of 32 heads 0.53 to 0.55 ms (1.00 to 1.04); a library
 // product of 8192^3: 1.40.  With a cap on the scores, two more transcendental
-// instructions each, a fifth slower.  The tile of 128 rows leaves room for two
+// instructions each, 15 to 26% slower.  The tile of 128 rows leaves room for two
 // workgroups a CU (at most 128 KB of LDS and 256 registers a lane for both),
 // which hide each other's barriers and latencies; the one of 256 reads LDS and
 // L2 half as often for the same products and is 3% faster where there are many
