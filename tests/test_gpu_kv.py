@@ -879,3 +879,34 @@ def test_more_tokens_than_one_launch_takes(torch, sz):
     for a, b in spots:
         assert torch.equal(got[a:b].view(torch.int16), out[a:b].view(torch.int16)), a
     assert bool((got[n:] == 0).all())
+
+
+def test_as_many_sequences_as_there_can_be(torch, sz):
+    """One key each: the output is its value. Then one start out of order."""
+    n = 65535
+    g = torch.Generator().manual_seed(34)
+    pool = torch.zeros(2, n, 16, 1, 8, dtype=torch.bfloat16, device="cuda")
+    cache = sz.paged_cache(pool[0], pool[1], torch.randperm(n, generator=g).view(n, 1).cuda())
+    x = torch.randn(3, n, 1, 8, generator=g).bfloat16().cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts, lens = torch.arange(n + 1, **i32), torch.ones(n, **i32)
+    batch = sz.Batch(starts, lens, n)
+    say("append and attention", n)
+    q = sz.kv_append(x[0], x[1], cache, batch, sz.rope(8), q=x[2])
+    out, _ = sz.attend_pages(q, cache, batch)
+    assert torch.equal(out, x[1])
+    at = 40000
+    starts[at] = 7
+    want = torch.zeros(n, **i32)
+    want[7:at + 1] = 1                 # what ends past row 7 before it, and the one it begins
+    for call in ("append", "attend"):
+        status = torch.full((n,), -1, **i32)
+        if call == "append":
+            sz.sz_kv_append(x[0], x[1], None, None, None, None, 0.0, None, None, cache, batch,
+                            status)
+        else:
+            sz.sz_attend_pages(q, out.zero_(), None, cache, batch, 0, 1.0, d_status=status)
+        torch.cuda.synchronize()
+        got = status.cpu()
+        assert torch.equal(got, want.cpu()), (call, (got != want.cpu()).nonzero()[:4].tolist())
+    assert torch.equal(out[:7], x[1][:7]) and torch.equal(out[at + 1:], x[1][at + 1:])
