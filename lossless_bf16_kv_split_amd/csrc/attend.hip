@@ -109,10 +109,12 @@ constexpr uint64_t kCus = 256;
 // would take.  Few rows: by the bytes, which one CU gets at about 50 GB/s (9
 // sequences of 5 tokens under a window of 1024, 64 elements, 264 KB a tile:
 // 10.6 us whole, 14.4 shared out; 777 keys of 128, 398 KB: 12.1 and 11.2).
+// Where they are many: 256 sequences of 1024 keys, 8 KV heads: 199 us whole,
+// 237 shared out; 128 of 2048: 210 and 198.
 // Tiles of 128 rows: 128 elements, 896 keys: 23.7 us whole, 30.1 shared out;
 // 1500: 35.5 and 22.5; 256 elements, 319 keys: 22.7 and 30.4; 565: 32.1 and
 // 29.5; 64 elements (whose steps cost nearly what 128 do), 1100: 20.9, 19.4.
-constexpr uint64_t kManyFew = 4096, kManyTiles = 512;
+constexpr uint64_t kManyFew = 2048, kManyTiles = 512;
 constexpr uint64_t kWholeFew = 288 * 1024, kWholeTiles = 480 * 1024;
 // Sharing out looks at every sequence in every workgroup, 64 at a time.
 constexpr uint64_t kShareSeqs = 1024;
