@@ -114,8 +114,14 @@ constexpr uint64_t kCus = 256;
 // Tiles of 128 rows: 128 elements, 896 keys: 23.7 us whole, 30.1 shared out;
 // 1500: 35.5 and 22.5; 256 elements, 319 keys: 22.7 and 30.4; 565: 32.1 and
 // 29.5; 64 elements (whose steps cost nearly what 128 do), 1100: 20.9, 19.4.
+// Long chunks, four tiles a sequence and more, fill the CUs evenly with whole
+// tiles from one a CU on, and every cut of theirs costs 128 KB of sums written
+// and read: 32 / 8 heads of 128, 256 tiles, 1024 keys 27 us whole, 42 shared
+// out; 4096: 84 and 92; 16384: 323 and 298; 128 tiles, 1024 keys: 26 and 34;
+// 2048: 45 and 43.
 constexpr uint64_t kManyFew = 2048, kManyTiles = 512;
 constexpr uint64_t kWholeFew = 288 * 1024, kWholeTiles = 480 * 1024;
+constexpr uint64_t kWholeHalf = 700 * 1024, kWholeOneEach = 4096 * 1024;
 // Sharing out looks at every sequence in every workgroup, 64 at a time.
 constexpr uint64_t kShareSeqs = 1024;
 // and counts steps in 32 bits.
@@ -146,10 +152,13 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * c.kv_heads;
     const uint64_t resident = c.head_dim > 128 ? kCus : 2 * kCus;
     const uint64_t width = p.few() || c.head_dim > 128 ? c.head_dim : 128;
+    uint64_t most_bytes = p.few() ? kWholeFew : kWholeTiles;
+    if (!p.few() && full >= 4 * n_seqs && groups >= kCus / 2)
+        most_bytes = groups >= kCus ? kWholeOneEach : kWholeHalf;
     const bool whole = n_seqs > kShareSeqs || c.kv_heads > resident ||
                        groups >= (p.few() ? kManyFew : kManyTiles) || p.tile_log2 == 8 ||
                        p.tiles * (max_len / kStep + 2) >= kMostSteps ||
-                       keys * width * 4 <= (p.few() ? kWholeFew : kWholeTiles);
+                       keys * width * 4 <= most_bytes;
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
     p.alone = p.few() ? (uint32_t)(kCus / c.kv_heads) : 0;
     p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
