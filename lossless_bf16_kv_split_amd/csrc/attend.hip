@@ -479,18 +479,36 @@ __device__ __forceinline__ Row find_row(const Attend& a, const AttendPlan& p, co
 }
 
 // t of a raw score: score * (scale log2 e), or the capped form, whose tanh
-// is 1 - 2 / (1 + e^2x)
+// is 1 - 2 / (1 + e^2x), and for |x| < 1/2, where that difference leaves few
+// bits, x (1 + c1 x^2 + c2 x^4 + c3 x^6 + c4 x^8), off by less than 3e-8 of it
+// (least squares on Chebyshev nodes, reweighted until the error was even).
 struct Score {
     float by;    // scale log2 e; capped: 2 scale log2 e / softcap
     float cap;   // softcap log2 e, 0 for none
+    float odd[5];  // capped: the polynomial in the score times `by`
 };
 Score score_of(const Attend& a) {
-    Score s;
+    static const double kTanh[5] = {1.0, -0.33333143895419826, 0.1332587893917483,
+                                    -0.05304549308250774, 0.01724148911923954};
+    Score s{};
     s.cap = a.softcap * kLog2e;
     s.by = a.softcap > 0 ? 2 * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e;
+    const double half = 0.5 * 0.69314718055994531;  // x = half * (score * by)
+    double power = half * a.softcap * 1.4426950408889634;
+    for (int i = 0; i < 5; i++, power *= half * half) s.odd[i] = (float)(kTanh[i] * power);
     return s;
 }
 __device__ __forceinline__ float capped(const Score& s, float x) {
+    const float y = x * s.by, e = __builtin_amdgcn_exp2f(y), z = y * y;
+    const float far = s.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+    const float near =
+        y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, s.odd[4], s.odd[3]), s.odd[2]), s.odd[1]), s.odd[0]);
+    return fabsf(y) < kLog2e ? near : far;
+}
+// Off by up to 1.5e-7 of the cap instead, for rows that see 64 keys and more,
+// over which that averages out (2048 tokens of 32 heads of 128 on 8192 keys:
+// 309 us, 404 with the other).
+__device__ __forceinline__ float capped_quickly(const Score& s, float x) {
     const float e = __builtin_amdgcn_exp2f(x * s.by);
     return s.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
 }
@@ -1123,7 +1141,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     }
 
     const float by = CAP ? 1.0f : score.by;
-    const auto scored = [&](float x) { return CAP ? capped(score, x) : x; };
+    const auto scored = [&](float x) { return CAP ? capped_quickly(score, x) : x; };
     // The running maximum of block b of 32 rows, and what hangs on it, where
     // a score of it (its largest in this lane: top, in powers of two) is too
     // far above it
@@ -1188,7 +1206,9 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
-                    s[k][i] = sees(32 * k + 8 * (i / 4) + i % 4) ? scored(s[k][i]) : -INFINITY;
+                    s[k][i] = sees(32 * k + 8 * (i / 4) + i % 4)
+                                  ? (CAP ? capped(score, s[k][i]) : s[k][i])
+                                  : -INFINITY;
                     top = fmaxf(top, s[k][i]);
                 }
             follow(b, top * by);

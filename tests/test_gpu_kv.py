@@ -910,3 +910,26 @@ def test_as_many_sequences_as_there_can_be(torch, sz):
         got = status.cpu()
         assert torch.equal(got, want.cpu()), (call, (got != want.cpu()).nonzero()[:4].tolist())
     assert torch.equal(out[:7], x[1][:7]) and torch.equal(out[at + 1:], x[1][at + 1:])
+
+
+@pytest.mark.parametrize("cap", [2.0, 50.0])
+@pytest.mark.parametrize("pairs", [[(1, 1), (1, 3), (1, 40)], [(30, 30), (5, 40), (100, 100)]],
+                         ids=["tokens", "chunks"])
+def test_attend_caps_keep_small_scores(torch, sz, cap, pairs):
+    """Scores far below the cap are as exact as without one: each within
+    (head_dim / 2 + 8) rounding steps of its terms' size, and so the log-sum,
+    an average of them, with as many steps of its own for the sum."""
+    S = Setup(torch, sz, pairs, 8, 2, 128, 16, seed=35, scale=0.25)
+    _, lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch, softcap=cap)
+    for s, (new, length) in enumerate(pairs):
+        a, b = S.starts[s], S.starts[s + 1]
+        q, k = S.q[a:b].double(), S.rows(S.k, s).double().repeat_interleave(4, 1)
+        raw = torch.einsum("ihd,jhd->ihj", q, k) * 128 ** -0.5
+        size = torch.einsum("ihd,jhd->ihj", q.abs(), k.abs()) * 128 ** -0.5
+        hidden = torch.arange(length)[None, :] > torch.arange(length - new, length)[:, None]
+        t = (cap * torch.tanh(raw / cap)).masked_fill(hidden[:, None], -math.inf)
+        want = torch.logsumexp(t, -1)
+        most = size.masked_fill(hidden[:, None], 0).amax(-1)
+        tol = 2.0 ** -24 * ((64 + 8) * most + 16 * (1 + want.abs()))
+        got = lse[a:b].cpu().double()
+        assert bool(((got - want).abs() <= tol).all()), (s, float(((got - want).abs() / tol).max()))
