@@ -1006,14 +1006,40 @@ __device__ __forceinline__ constexpr uint32_t v_mix(uint32_t j) {
     return DP == 64 ? (j >> 1 & 1) << 2 : (j & 3) << 2;
 }
 
-// 64 lanes' 16 bytes each, from offsets of a buffer to consecutive LDS bytes;
-// offsets past the buffer's end store zeros.  Completion is counted by vmcnt.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset,
+// N times 64 lanes' 16 bytes each, from offsets of a buffer to consecutive LDS
+// bytes, 1024 a time; offsets past the buffer's end store zeros.  Completion is
+// counted by vmcnt.  A load reads m0 and the resource's scalar registers, and
+// the hardware waits for neither: one state must lie between a scalar write of
+// m0 and the load, five between a vector instruction's write of a scalar
+// register (a lane read back, a reload of a spilled one) and it.  The compiler
+// keeps to that only around instructions that it knows, so the block itself
+// waits: the move and four states after it, once for up to four loads.
+// (m0 is the compiler's to write just before an instruction that reads it and
+// never holds a value across others: it refuses it as a clobber.)
+template <int N>
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, const uint32_t* at,
                                             uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(offset), "s"(from)
-                 : "memory");
+#define SZ_NEXT_LOAD(at) \
+    "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 " at ", %1, 0 offen lds\n\t"
+    static_assert(N == 2 || N % 4 == 0, "");
+    if constexpr (N == 2) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
+                     "buffer_load_dwordx4 %2, %1, 0 offen lds\n\t" SZ_NEXT_LOAD("%3")
+                     :
+                     : "s"(lds), "s"(from), "v"(at[0]), "v"(at[1])
+                     : "memory", "scc");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
+                         "buffer_load_dwordx4 %2, %1, 0 offen lds\n\t" SZ_NEXT_LOAD("%3")
+                             SZ_NEXT_LOAD("%4") SZ_NEXT_LOAD("%5")
+                         :
+                         : "s"(lds + 1024 * i), "s"(from), "v"(at[i]), "v"(at[i + 1]),
+                           "v"(at[i + 2]), "v"(at[i + 3])
+                         : "memory", "scc");
+    }
+#undef SZ_NEXT_LOAD
 }
 
 // Bytes of LDS: K of two steps of 64 keys, V of three
@@ -1094,8 +1120,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                                 << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)page);
         const auto rows = block_rows(a.cache, at, slot, kv, last - jb);
         const uint32_t to = lds0 + buffer * kBuffer + wave * 16 * kRow;
-#pragma unroll
-        for (int i = 0; i < kLoads; i++) load_to_lds(rows, off[i], to + 1024 * i);
+        load_to_lds<kLoads>(rows, off, to);
     };
     uint64_t next_k = page_at(a.cache.k_pages, first), next_v = page_at(a.cache.v_pages, first);
     const auto fetch_step = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer) {
