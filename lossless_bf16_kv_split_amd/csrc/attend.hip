@@ -505,9 +505,14 @@ __device__ __forceinline__ float capped(const Score& s, float x) {
         y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, s.odd[4], s.odd[3]), s.odd[2]), s.odd[1]), s.odd[0]);
     return fabsf(y) < kLog2e ? near : far;
 }
-// Off by up to 1.5e-7 of the cap instead, for rows that see 64 keys and more,
-// over which that averages out (2048 tokens of 32 heads of 128 on 8192 keys:
-// 309 us, 404 with the other).
+// Off by up to 1.5e-7 of the cap instead, whatever the score: in steps that
+// every row sees all of, for caps up to kQuickCap, where that is at most 1e-5 of
+// a score, a 400th of a weight's rounding to BF16 (2048 tokens of 32 heads of
+// 128 on 8192 keys: 308 us, 399 with the other).  It rounds small scores
+// all the same way, so no number of keys evens it out: with a cap of 1e5
+// weights would be a hundredth off, with 1e8 the scores would be gone.
+constexpr float kQuickCap = 64.0f;
+enum { kUncapped = 0, kQuick = 1, kExact = 2 };  // what such steps compute
 __device__ __forceinline__ float capped_quickly(const Score& s, float x) {
     const float e = __builtin_amdgcn_exp2f(x * s.by);
     return s.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
@@ -1046,7 +1051,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, const u
 template <int DP>
 constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP;
 
-template <int DP, int QB, bool CAP, bool SHARED>
+template <int DP, int QB, int CAP, bool SHARED>
 __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                                            const Score& score, uint8_t* ws, const Part& part,
                                            uint32_t kv, uint8_t* lds) {
@@ -1165,8 +1170,10 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
             for (int i = 0; i < 16; i++) o[b][d][i] = 0;
     }
 
-    const float by = CAP ? 1.0f : score.by;
-    const auto scored = [&](float x) { return CAP ? capped_quickly(score, x) : x; };
+    const float by = CAP != kUncapped ? 1.0f : score.by;
+    const auto scored = [&](float x) {
+        return CAP == kQuick ? capped_quickly(score, x) : CAP == kExact ? capped(score, x) : x;
+    };
     // The running maximum of block b of 32 rows, and what hangs on it, where
     // a score of it (its largest in this lane: top, in powers of two) is too
     // far above it
@@ -1232,7 +1239,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     s[k][i] = sees(32 * k + 8 * (i / 4) + i % 4)
-                                  ? (CAP ? capped(score, s[k][i]) : s[k][i])
+                                  ? (CAP != kUncapped ? capped(score, s[k][i]) : s[k][i])
                                   : -INFINITY;
                     top = fmaxf(top, s[k][i]);
                 }
@@ -1502,7 +1509,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     }
 }
 
-template <int DP, int QB, bool CAP, bool SHARED>
+template <int DP, int QB, int CAP, bool SHARED>
 __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
@@ -1601,7 +1608,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     }
 }
 
-template <int DP, bool CAP>
+template <int DP, int CAP>
 hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
     const dim3 grid((p.shares != 0 ? p.shares : p.tiles) * a.cache.kv_heads);
     constexpr uint32_t block = kThreads;
@@ -1629,7 +1636,7 @@ hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t str
     return hipGetLastError();
 }
 
-template <bool CAP>
+template <int CAP>
 hipError_t go(const Attend& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
     const uint32_t dim = a.cache.head_dim;
     return dim <= 64    ? go<64, CAP>(a, p, ws, stream)
@@ -1654,7 +1661,9 @@ hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {
     const AttendPlan p =
         plan_attend(a.q.heads, a.cache, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len,
                     a.window);
-    const hipError_t e = a.softcap > 0 ? go<true>(a, p, ws, stream) : go<false>(a, p, ws, stream);
+    const hipError_t e = !(a.softcap > 0)         ? go<kUncapped>(a, p, ws, stream)
+                         : a.softcap <= kQuickCap ? go<kQuick>(a, p, ws, stream)
+                                                  : go<kExact>(a, p, ws, stream);
     if (e != hipSuccess || p.shares == 0) return e;
     const dim3 grid(p.tiles * a.cache.kv_heads * join_pieces(p)), block(kThreads);
     if (a.cache.head_dim <= 64) k_attend_join<16><<<grid, block, 0, stream>>>(a, p, ws);

@@ -96,3 +96,51 @@ def page_view(pool, cache_shape, tokens_first):
     if tokens_first:
         return pool.view(-1, page, KH, D)
     return pool.view(-1, KH, page, D).transpose(1, 2)
+
+
+def attend_rows(q, positions, keys, values, length, scale, causal=True, window=0, softcap=0.0,
+                f32_out=False):
+    """attend() for some rows of a sequence only: q [rows, H, D], at cache
+    positions [rows]; keys and values of the whole sequence, used a KV head
+    at a time.  The same bounds, but for a cap: its score is off by at most
+    16 U32 of its own size (below |x| = 1/2 a polynomial off by 3e-8, of an
+    argument off by 4 roundings, with 3 more; above, where |tanh x| > 0.46,
+    an exponent's argument off by 4 U32 of x sech^2 x <= 0.45, two units each
+    for the exponential and the reciprocal and one for the difference: less
+    than 6 U32, 13 relative; and two roundings of the cap), and for caps of
+    64 and less, where steps that every row sees may leave out the
+    polynomial, by 8 U32 of the cap."""
+    n, H, D = q.shape
+    KH = keys.shape[1]
+    G = H // KH
+    out, tol = (torch.zeros(n, H, D, dtype=torch.float64) for _ in range(2))
+    lse, tol_lse = (torch.zeros(n, H, dtype=torch.float64) for _ in range(2))
+    j = torch.arange(length)[None]
+    c = positions[:, None]
+    seen = (j <= c) if causal else (j < length).expand(n, length)
+    if window:
+        seen = seen & (j > c - window)
+    count = seen.sum(1)[:, None, None]
+    seen = seen[:, None]
+    for kv in range(KH):
+        at = slice(kv * G, (kv + 1) * G)
+        x, K, V = q[:, at].double(), keys[:, kv].double(), values[:, kv].double()
+        s = (x @ K.t()) * scale
+        size = ((x.abs() @ K.abs().t()) * scale).masked_fill(~seen, 0).amax(-1, keepdim=True)
+        bound = size
+        if softcap:
+            s = softcap * torch.tanh(s / softcap)
+            bound = size.clamp(max=softcap)
+        top = s.abs().masked_fill(~seen, 0).amax(-1, keepdim=True)
+        ds = D * U32 * size + 8 * U32 * torch.maximum(bound, top)
+        if softcap:
+            ds = ds + 16 * U32 * top + (8 * U32 * softcap if softcap <= 64 else 0)
+        s = s.masked_fill(~seen, -math.inf)
+        z = torch.logsumexp(s, -1, keepdim=True)
+        p = torch.exp(s - z.clamp(min=-1e300))
+        o = p @ V
+        rel = 4 * ds + (2 * count + 64) * U32 + 2.0 ** -19
+        out[:, at], lse[:, at] = o, z[..., 0]
+        tol[:, at] = (U16 + rel) * (p @ V.abs()) * (1 + U16) + (0 if f32_out else U16) * o.abs()
+        tol_lse[:, at] = (rel + 8 * U32 * z.abs() + 8 * U32 * top)[..., 0]
+    return out, lse, tol, tol_lse
