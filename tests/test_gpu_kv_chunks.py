@@ -1,7 +1,9 @@
 """Attention of chunks over a paged cache (sz_attend_pages) where tiles have
 128 and 256 rows: sampled rows of long calls against the plain 64-bit form,
 with the bounds of kv_reference.py."""
+import ctypes
 import math
+import re
 
 import pytest
 
@@ -17,7 +19,7 @@ def some_rows(n, count, seed, torch):  # noqa: F811
     g = torch.Generator().manual_seed(seed)
     borders = [0, 1, 15, 16, 31, 32, 33, 63, 64, 127, 128, 129, 255, 256, 257, 511, 512, n - 2, n - 1]
     picked = {x for x in borders if 0 <= x < n}
-    picked |= set(torch.randint(0, n, (count,), generator=g).tolist()) if n else set()
+    picked |= set(torch.randint(0, n, (count,), generator=g).tolist())
     return torch.tensor(sorted(picked), dtype=torch.int64)
 
 
@@ -43,6 +45,8 @@ def check(torch, sz, S, label, count=24, out_type=None, max_len=0, **kw):  # noq
     for s, (new, length) in enumerate(S.pairs):
         a, b = S.starts[s], S.starts[s + 1]
         covered[a:b] = True
+        if new == 0:
+            continue
         rows = some_rows(new, count, s, torch)
         want, want_lse, tol, tol_lse = ref.attend_rows(
             S.q[a + rows], length - new + rows, S.rows(S.k, s), S.rows(S.v, s), length,
@@ -75,3 +79,114 @@ def test_caps_of_any_size(torch, sz, shape, cap, max_len):  # noqa: F811
         S.upload()
     check(torch, sz, S, f"cap {cap} {shape} {max_len}", max_len=max_len, softcap=cap,
           out_type=torch.float32)
+
+
+# ---- tiles of 256 rows: calls of many rows -----------------------------------
+
+class NodeParams(ctypes.Structure):
+    _fields_ = [("block", ctypes.c_uint32 * 3), ("extra", ctypes.c_void_p),
+                ("func", ctypes.c_void_p), ("grid", ctypes.c_uint32 * 3),
+                ("params", ctypes.c_void_p), ("shared", ctypes.c_uint32)]
+
+
+def kernels(torch, sz, S, **kw):  # noqa: F811
+    """What an attention call launches, from a graph that it is captured into:
+    ("few" or "chunk", head size compiled for, waves or blocks of 32 rows a
+    wave), or ("join",)."""
+    q, out = S.q.cuda(), torch.zeros(S.q.shape, dtype=torch.bfloat16, device="cuda")
+    size = sz.sz_attend_workspace_size(S.q.shape[1], S.cache, S.batch)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        sz.sz_attend_pages(q, out, None, S.cache, S.batch, 0, S.dim ** -0.5, workspace=ws,
+                           workspace_bytes=size, **kw)
+    hip = ctypes.CDLL(next(x.split()[-1] for x in open("/proc/self/maps") if "libamdhip64" in x))
+    hip.hipKernelNameRefByPtr.restype = ctypes.c_char_p
+    hip.hipKernelNameRefByPtr.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    raw, count = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert hip.hipGraphGetNodes(raw, None, ctypes.byref(count)) == 0
+    nodes = (ctypes.c_void_p * count.value)()
+    assert hip.hipGraphGetNodes(raw, nodes, ctypes.byref(count)) == 0
+    found = []
+    for node in nodes:
+        p = NodeParams()
+        assert hip.hipGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        name = hip.hipKernelNameRefByPtr(p.func, None).decode()
+        kind = re.search(r"k_attend_(few|chunk|join)(?:I|<)(?:Li)?(\d+)(?:E(?:Li)?|, )?(\d*)", name)
+        assert kind, name
+        found.append(("join",) if kind[1] == "join" else (kind[1], int(kind[2]), int(kind[3])))
+    return found
+
+
+# (new tokens, cached length): two chunks whose rows end inside a tile, and
+# short sequences between them, one without tokens
+RAGGED = [(3, 50), (1501, 1501), (1, 900), (0, 0), (1280, 1777), (37, 20), (2, 2)]
+LARGE = [  # heads, kv_heads, dim, page
+    (64, 16, 64, 16), (64, 16, 128, 64), (64, 16, 72, 32), (64, 16, 96, 16), (48, 16, 128, 16),
+]
+MASKS = [dict(), dict(window=1), dict(window=100), dict(window=1000), dict(causal=False),
+         dict(softcap=30.0), dict(softcap=200.0, window=300)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+@pytest.mark.parametrize("kw", MASKS, ids=str)
+def test_large_tiles(torch, sz, shape, kw):  # noqa: F811
+    S = Setup(torch, sz, RAGGED, *shape, tokens_first=shape[3] != 32, seed=51, before=1, behind=2)
+    check(torch, sz, S, f"large tiles {shape} {kw}", **kw)
+    assert kernels(torch, sz, S, **kw) == [("chunk", 64 if shape[2] <= 64 else 128, 2)]
+
+
+def test_large_tiles_f32_output_and_growing_scores(torch, sz):  # noqa: F811
+    """Keys that grow along the sequence: the running maximum of both blocks
+    of 32 rows moves in every step."""
+    S = Setup(torch, sz, [(2700, 3000)], 64, 16, 128, 64, seed=52)
+    S.q = S.q.abs()
+    page = ref.page_view(S.k, S.shape, True)
+    for j in range(3000):
+        page[S.ids[0, j // 64], j % 64] = 0.01 * j / 128 ** 0.5
+    S.upload()
+    check(torch, sz, S, "growing, large tiles", out_type=torch.float32)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_large_tiles_and_unseen_content(torch, sz, dim):  # noqa: F811
+    """NaN and infinities ahead of a row in its own tile, before its window,
+    past the length: no effect, bit for bit; on the rows that see them, their
+    own."""
+    window = 700
+    pairs = [(2200, 2300), (64, 64)]
+    at = 1333                                  # a position inside a tile
+    first = pairs[0][1] - pairs[0][0]
+
+    def setup():
+        return Setup(torch, sz, pairs, 64, 16, dim, 16, seed=53)
+    S = setup()
+    want, want_lse = run(torch, sz, S, window=window)
+    assert kernels(torch, sz, S, window=window) == [("chunk", 64 if dim == 64 else 128, 2)]
+    blind = torch.ones(S.n, dtype=torch.bool)  # rows that do not see the position
+    blind[at - first:at - first + window] = False
+    for value in (math.nan, math.inf, -math.inf):
+        say("large tiles, unseen", dim, value)
+        T = setup()
+        for pool in (T.k, T.v):
+            ref.page_view(pool, T.shape, True)[T.ids[0, at // 16], at % 16] = value
+            # past the lengths, and in pages of no sequence
+            page = ref.page_view(pool, T.shape, True)
+            page[T.ids[0, 2300 // 16], 2300 % 16:] = value
+            used = torch.zeros(pool.shape[0], dtype=torch.bool)
+            used[T.ids[T.ids >= 0]] = True
+            page[~used] = value
+        T.upload()
+        got, got_lse = run(torch, sz, T, window=window)
+        assert torch.equal(got[blind], want[blind]) and torch.equal(got_lse[blind], want_lse[blind])
+        # one element of a value alone: that element of the rows that see it
+        T = setup()
+        ref.page_view(T.v, T.shape, True)[T.ids[0, at // 16], at % 16, :, 5] = value
+        T.upload()
+        got, got_lse = run(torch, sz, T, window=window)
+        assert torch.equal(got_lse, want_lse)
+        assert torch.equal(got[blind], want[blind])
+        rest = [d for d in range(dim) if d != 5]
+        assert torch.equal(got[:, :, rest], want[:, :, rest])
+        hit = got[~blind][:, :, 5].float()
+        assert bool(torch.isnan(hit).all() if math.isnan(value) else (hit == value).all())
