@@ -137,9 +137,17 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group;
     p.tile_log2 = rows <= 16 * n_seqs ? 4 : 7;
-    // (256 rows where even they are many: half the reads of LDS and L2 for
-    // the same products)
-    if (c.head_dim <= 128 && (rows >> 8) * c.kv_heads >= kManyTiles) p.tile_log2 = 8;
+    // 256 rows where even they are many and sequences fill 16 of them on average
+    // (8 with 64 elements): half the reads of LDS and L2 for the same products,
+    // but one workgroup a CU, not two, and more rows that a sequence's last tile
+    // lacks (32 / 8 heads of 128, tiles of 128 and of 256 rows: 2 chunks of 2048
+    // tokens 198 us and 192, 4 of 1000 206 and 205, 8 of 512 116 and 130, 32 of
+    // 128 120 and 149; 4096 tokens beside 200 single ones 484 and 700; of 64: 8
+    // of 512 81 and 73, 16 of 256 79 and 78, 32 of 128 73 and 82, but 8 of 1024
+    // beside 8 single ones 199 and 249)
+    if (p.tile_log2 == 7 && c.head_dim <= 128 &&
+        rows >> (c.head_dim <= 64 ? 11 : 12) >= n_seqs && (rows >> 8) * c.kv_heads >= kManyTiles)
+        p.tile_log2 = 8;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     // keys of a tile: a window shows its rows' tokens' own keys and those of
     // a window before

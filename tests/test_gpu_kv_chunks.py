@@ -38,14 +38,14 @@ def run(torch, sz, S, out_type=None, max_len=0, scale=None, **kw):  # noqa: F811
     return out.cpu(), lse.cpu()
 
 
-def check(torch, sz, S, label, count=24, out_type=None, max_len=0, **kw):  # noqa: F811
+def check(torch, sz, S, label, count=24, out_type=None, max_len=0, every=1, **kw):  # noqa: F811
     say(label)
     out, lse = run(torch, sz, S, out_type, max_len, **kw)
     covered = torch.zeros(S.n, dtype=torch.bool)
     for s, (new, length) in enumerate(S.pairs):
         a, b = S.starts[s], S.starts[s + 1]
         covered[a:b] = True
-        if new == 0:
+        if new == 0 or (s % every and new < 16):
             continue
         rows = some_rows(new, count, s, torch)
         want, want_lse, tol, tol_lse = ref.attend_rows(
@@ -118,9 +118,9 @@ def kernels(torch, sz, S, **kw):  # noqa: F811
     return found
 
 
-# (new tokens, cached length): two chunks whose rows end inside a tile, and
-# short sequences between them, one without tokens
-RAGGED = [(3, 50), (1501, 1501), (1, 900), (0, 0), (1280, 1777), (37, 20), (2, 2)]
+# (new tokens, cached length): two chunks whose rows end inside a tile, a short
+# sequence whose first rows see nothing, one without tokens
+RAGGED = [(37, 20), (2101, 2101), (0, 0), (3377, 3877)]
 LARGE = [  # heads, kv_heads, dim, page
     (64, 16, 64, 16), (64, 16, 128, 64), (64, 16, 72, 32), (64, 16, 96, 16), (48, 16, 128, 16),
 ]
@@ -190,3 +190,19 @@ def test_large_tiles_and_unseen_content(torch, sz, dim):  # noqa: F811
         assert torch.equal(got[:, :, rest], want[:, :, rest])
         hit = got[~blind][:, :, 5].float()
         assert bool(torch.isnan(hit).all() if math.isnan(value) else (hit == value).all())
+
+
+@pytest.mark.parametrize("case", [
+    ("few", 64, [(1, 20 + i * 7 % 50) for i in range(2048)]),            # a large decode batch
+    ("few", 32, [(4, 20 + i * 7 % 50) for i in range(1024)]),            # drafts
+    ("chunk", 32, [(8, 20 + i * 7 % 50) for i in range(512)]),
+    ("chunk", 32, [(1, 40)] * 60 + [(4090, 4090)] + [(1, 70)] * 40),     # decodes and a prompt
+], ids=["tokens", "drafts", "more rows", "mixed"])
+def test_short_sequences_keep_small_tiles(torch, sz, case):  # noqa: F811
+    """Tiles of 256 rows are for sequences that fill them, not for calls that
+    have many rows in all."""
+    kind, heads, pairs = case
+    # (no spare rows: they count among a call's, and drafts have just 16 a tile)
+    S = Setup(torch, sz, pairs, heads, 8, 128, 16, seed=54)
+    check(torch, sz, S, f"{kind} {len(pairs)}", every=29)
+    assert kernels(torch, sz, S) == [(kind, 128, 4 if kind == "few" else 1)]
