@@ -418,9 +418,10 @@ sz_status sz_decode_blocks(const void *d_src, uint64_t src_pitch, const uint64_t
  * 8 .. 256.  Tensors of rows are described by sz_heads.  A tensor that a
  * call writes must not overlap itself (rows lie inside one another's
  * strides: tokens of heads, or heads of tokens) nor any other tensor of the
- * call; two tensors may interleave with the same token stride (slices of
- * one fused projection).  sz_qk_norm_rope and sz_kv_append may write a
- * BF16 tensor in place: same data, strides and type as its source. */
+ * call; two tensors may interleave with the same token stride, or with the
+ * same token and head strides (slices of one fused projection).
+ * sz_qk_norm_rope and sz_kv_append may write a BF16 tensor in place: same
+ * data, strides and type as its source. */
 typedef enum {
     SZ_TYPE_BF16 = 1,
     SZ_TYPE_F32 = 2

@@ -70,7 +70,7 @@ Span span(const sz_heads& t, uint64_t tokens, uint64_t dim) {
 }
 
 // Whether a call that writes b may have a beside it: apart, in place (the
-// caller says whether that is allowed), or slices of the same tokens.
+// caller says whether that is allowed), or slices of the same tokens or heads.
 bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, bool in_place) {
     const Span x = span(a, tokens, dim), y = span(b, tokens, dim);
     if (x.end <= y.begin || y.end <= x.begin) return true;
@@ -85,7 +85,15 @@ bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, 
     const uint64_t b_bytes = ((b.heads - 1) * b.head_stride + dim) * size_of(b.type);
     const uint64_t ahead = x.begin <= y.begin ? (y.begin - x.begin) % step
                                               : (step - (x.begin - y.begin) % step) % step;
-    return ahead >= a_bytes && ahead + b_bytes <= step;
+    if (ahead >= a_bytes && ahead + b_bytes <= step) return true;
+    // or the same step from head to head too, within which the one is before
+    // the other (slices of every head of a fused tensor), where a token's
+    // heads line up with the next one's or do not reach it
+    const uint64_t head = a.head_stride * size_of(a.type);
+    if (head == 0 || head != b.head_stride * size_of(b.type)) return false;
+    const uint64_t in_head = ahead % head;
+    return in_head >= dim * size_of(a.type) && in_head + dim * size_of(b.type) <= head &&
+           (step % head == 0 || (a_bytes <= step && ahead + b_bytes <= step));
 }
 
 bool overlap(const void* p, uint64_t bytes, Span s) {

@@ -206,3 +206,28 @@ def test_short_sequences_keep_small_tiles(torch, sz, case):  # noqa: F811
     S = Setup(torch, sz, pairs, heads, 8, 128, 16, seed=54)
     check(torch, sz, S, f"{kind} {len(pairs)}", every=29)
     assert kernels(torch, sz, S) == [(kind, 128, 4 if kind == "few" else 1)]
+
+
+def test_slices_of_every_head(torch, sz):  # noqa: F811
+    """Queries, keys and outputs side by side in every head of one tensor."""
+    g = torch.Generator().manual_seed(55)
+    n, H, D = 150, 4, 64
+    x = torch.randn(n, H, 3, D, generator=g).bfloat16().cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    rope, w = sz.rope(D), 1 + 0.2 * torch.randn(D, generator=g).cuda()
+    want = sz.qk_norm_rope(x[:, :, 0].contiguous(), x[:, :, 1].contiguous(), pos, rope, w, w)
+    y = x.clone()
+    q, k = y[:, :, 0], y[:, :, 1]
+    sz.sz_qk_norm_rope(q, q, w, k, k, w, D, n, pos, 1e-6, rope)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(y[:, :, 2], x[:, :, 2])
+    pool = torch.randn(2, 10, 16, H, D, generator=g).bfloat16().cuda()
+    cache = sz.paged_cache(pool[0], pool[1], torch.arange(10, device="cuda").view(1, -1))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = sz.Batch(torch.tensor([0, n], **i32), torch.tensor([n], **i32), n)
+    want, _ = sz.attend_pages(q.contiguous(), cache, batch, max_len=n)
+    size = sz.sz_attend_workspace_size(H, cache, batch, n)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+    sz.sz_attend_pages(q, y[:, :, 2], None, cache, batch, n, D ** -0.5, workspace=ws,
+                       workspace_bytes=size)
+    assert torch.equal(y[:, :, 2], want)

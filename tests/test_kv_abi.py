@@ -277,3 +277,22 @@ def test_rope_frequencies_of_impossible_sizes(sz, dims):
         sz.sz_rope_frequencies(dims, 10000.0)
     with pytest.raises(sz.SplitZipError):
         sz.rope(dims)
+
+
+def test_slices_that_interleave_head_by_head(sz):
+    """Queries and keys (and more) side by side in every head of one tensor
+    lie apart, as slices of its tokens do; rows that reach into the next
+    slice do not."""
+    def call(q, k):  # (no sequences: checked, and nothing launched)
+        return append(sz, k=k, v=heads(A + GB), q=q, q_out=q,
+                      b=batch(seqs=0, starts=None, lens=None))
+    step = dict(n=8, head_stride=3 * 128, token_stride=24 * 128)
+    assert call(heads(A + 256, **step), heads(A, **step)) == 0
+    assert call(heads(A, **step), heads(A + 512, **step)) == 0
+    assert call(heads(A + 256 + 768 * 3, **step), heads(A, **step)) == 0    # some heads further on
+    assert call(heads(A + 128, **step), heads(A, **step)) == 1              # reaches into it
+    assert call(heads(A + 640, **step), heads(A, **step)) == 1              # into the next head's
+    odd = dict(n=8, head_stride=3 * 128, token_stride=25 * 128)             # spare room in a token
+    assert call(heads(A + 256, **odd), heads(A, **odd)) == 0
+    assert call(heads(A + 256 + 768 * 3, **odd), heads(A, **odd)) == 1      # into the next token's
+    assert call(heads(A + 256, n=8, head_stride=256, token_stride=24 * 128), heads(A, **step)) == 1
