@@ -772,6 +772,8 @@ def qk_norm_rope(q, k, positions, rope=None, q_weight=None, k_weight=None, eps: 
     be None); returns new bfloat16 tensors (sz_qk_norm_rope)."""
     import torch
     some = q if q is not None else k
+    if some is None:
+        raise ValueError("neither queries nor keys")
     out = [None if x is None else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
            for x in (q, k)]
     sz_qk_norm_rope(q, out[0], q_weight, k, out[1], k_weight, some.shape[2], some.shape[0],

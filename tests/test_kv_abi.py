@@ -296,3 +296,8 @@ def test_slices_that_interleave_head_by_head(sz):
     assert call(heads(A + 256, **odd), heads(A, **odd)) == 0
     assert call(heads(A + 256 + 768 * 3, **odd), heads(A, **odd)) == 1      # into the next token's
     assert call(heads(A + 256, n=8, head_stride=256, token_stride=24 * 128), heads(A, **step)) == 1
+
+
+def test_neither_queries_nor_keys(sz):
+    with pytest.raises(ValueError):
+        sz.qk_norm_rope(None, None, None)
