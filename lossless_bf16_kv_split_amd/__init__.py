@@ -390,6 +390,16 @@ def _on_device(t, dtype, what: str, dim: int | None = None):
     return t
 
 
+_U32, _U64 = 1 << 32, 1 << 64
+
+
+def _fits(limit: int, *sizes) -> None:
+    """Sizes as their C type holds them (ctypes would cut them to it)."""
+    for x in sizes:
+        if not 0 <= x < limit:
+            raise ValueError(f"a size of {x}")
+
+
 class _Descriptor(ctypes.Structure):
     def _set(self, device, *keep):
         self._keep, self._at = keep, ctypes.addressof(self)
@@ -437,10 +447,12 @@ class KVCache(_Descriptor):
         if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device or \
                 pitch[0] != pitch[1]:
             raise ValueError("the page tables must have the same shape, strides and device")
+        token_stride = kv_heads * head_dim if token_stride is None else token_stride
+        head_stride = head_dim if head_stride is None else head_stride
+        _fits(_U32, kv_heads, head_dim, page_tokens)
+        _fits(_U64, token_stride, head_stride)
         super().__init__(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[1], pitch[0],
-                         kv_heads * head_dim if token_stride is None else token_stride,
-                         head_dim if head_stride is None else head_stride,
-                         kv_heads, head_dim, page_tokens)
+                         token_stride, head_stride, kv_heads, head_dim, page_tokens)
         self.rows = k_pages.shape[0]
         self._set(k_pages.device, k_pages, v_pages, keep)
 
@@ -457,6 +469,7 @@ class Batch(_Descriptor):
             _on_device(t, torch.int32, "starts and lens", 1)
         if starts.numel() != lens.numel() + 1 or starts.device != lens.device:
             raise ValueError("starts must have one entry more than lens, on the same device")
+        _fits(_U64, n_tokens)
         super().__init__(starts.data_ptr(), lens.data_ptr(), lens.numel(), n_tokens)
         self._set(starts.device, starts, lens)
 
@@ -593,6 +606,7 @@ def sz_kv_append(k, v, k_weight, q, q_out, q_weight, eps: float, rope, positions
 
 
 def sz_attend_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
+    _fits(_U64, q_heads, max_len)
     return int(_lib.sz_attend_workspace_size(q_heads, _at(cache), _at(batch), max_len))
 
 
@@ -602,6 +616,8 @@ def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softc
     """q, out: Heads, or tensors [tokens, heads, head_dim]; lse: a float32
     tensor [tokens, heads] or None; cache: a KVCache; batch: a Batch."""
     q, out = _heads(q), _heads(out)
+    if not (0 <= max_len < _U64 and 0 <= window < _U64 and 0 <= workspace_bytes < _U64):
+        _fits(_U64, max_len, window, workspace_bytes)
     stream = _call_stream(stream, cache, batch, q, out)
     index, n = cache._index, batch.n_tokens
     _tokens(n, q, out)

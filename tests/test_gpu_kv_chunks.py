@@ -231,3 +231,32 @@ def test_slices_of_every_head(torch, sz):  # noqa: F811
     sz.sz_attend_pages(q, y[:, :, 2], None, cache, batch, n, D ** -0.5, workspace=ws,
                        workspace_bytes=size)
     assert torch.equal(y[:, :, 2], want)
+
+
+def test_sizes_that_would_be_cut(torch, sz):  # noqa: F811
+    """Sizes outside their C type are refused, not taken modulo 2^32 or 2^64."""
+    S = Setup(torch, sz, [(1, 100), (20, 300)], 8, 2, 64, 16, seed=56)
+    tables = S.cache._keep[:2]
+    for kw in (dict(kv_heads=2 ** 32 + 2), dict(head_dim=2 ** 32 + 64), dict(page_tokens=2 ** 32 + 16),
+               dict(page_tokens=-16), dict(token_stride=2 ** 64 + 128), dict(head_stride=-64)):
+        args = dict(kv_heads=2, head_dim=64, page_tokens=16)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            sz.KVCache(*tables, **args)
+    starts = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for n in (-1, 2 ** 64 + 1):
+        with pytest.raises(ValueError):
+            sz.Batch(starts, starts[:1], n)
+    q = S.q.cuda()
+    for kw in (dict(window=-1), dict(window=2 ** 64 + 5), dict(max_len=-1), dict(max_len=2 ** 64 + 300)):
+        with pytest.raises(ValueError):
+            sz.attend_pages(q, S.cache, S.batch, **kw)
+    out = torch.zeros_like(q)
+    for size in (-1, 2 ** 64):
+        with pytest.raises(ValueError):
+            sz.sz_attend_pages(q, out, None, S.cache, S.batch, 0, 0.1, workspace=None,
+                               workspace_bytes=size)
+    with pytest.raises(ValueError):
+        sz.sz_attend_workspace_size(2 ** 64 + 8, S.cache, S.batch)
+    with pytest.raises(ValueError):
+        sz.sz_attend_workspace_size(8, S.cache, S.batch, -1)
