@@ -515,7 +515,9 @@ sz_status sz_rope_phases(const double *inv_freq, uint64_t n, uint64_t *phases);
 /* Norm and rotation of queries and keys in one pass: for every token and
  * head, y = x / sqrt(mean(x^2) + eps) * weight over the head's elements
  * (weight NULL: y = x), then the rotation of the token's position, in FP32,
- * rounded once to BF16.
+ * rounded once to BF16.  (With a weight the squares are FP32 too: elements
+ * of 2^60 and more in size, or with eps 0 heads all below 2^-60, give 0 or
+ * infinities.)
  *   q, q_out / k, k_out  source (BF16 or F32) and BF16 destination, each
  *                        with n_tokens tokens; q or k (with its destination)
  *                        may be NULL
@@ -557,7 +559,12 @@ sz_status sz_kv_append(const sz_heads *k, const sz_heads *v, const float *d_k_we
  * zeros and a log-sum of -infinity.  A key or value that a query does not
  * see has no effect on it, whatever its bits.
  * Scores, the softmax's maximum and sum, and the accumulated output are
- * FP32; the weights are rounded to BF16 before they multiply the values.
+ * FP32; the weights are rounded to BF16 before they multiply the values,
+ * whatever the output's type.  Weights are at most 2^8 and the sums are
+ * divided at the end, so a row's scores must stay below 2^29 and the size of
+ * its values times 2^8 times its keys below 2^127; beyond that its outputs
+ * may be infinite, NaN or zero.  Scores that are all -infinity give what no
+ * key gives.
  *   q         BF16, batch->n_tokens tokens, heads a multiple of kv_heads;
  *             n_tokens * heads < 2^31, and n_tokens * heads / 128 + 2 *
  *             n_seqs * kv_heads < 2^24

@@ -754,7 +754,9 @@ def paged_cache(k_pool, v_pool, table) -> KVCache:
     bfloat16 (any strides that keep head_dim contiguous, so that a permuted
     [pages, kv_heads, page_tokens, head_dim] pool does too) and an integer
     table [sequences, pages] of page numbers, negative for none.  The address
-    tables are made here; make the cache again when the table changes."""
+    tables are made here (the largest page number is read back, which waits
+    for the device); make the cache again when the table changes, or keep
+    address tables of your own up to date and make a KVCache of them once."""
     import torch
     for t in (k_pool, v_pool):
         _on_device(t, torch.bfloat16, "a pool", 4)

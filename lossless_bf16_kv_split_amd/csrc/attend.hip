@@ -988,10 +988,10 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
 // a prompt of 8192 tokens of 32 heads 0.53 to 0.55 ms (1.00 to 1.04); a library
 // product of 8192^3: 1.40.  With a cap on the scores, two more transcendental
 // instructions each, 15 to 26% slower.  The tile of 128 rows leaves room for two
-// workgroups a CU (at most 128 KB of LDS and 256 registers a lane for both),
-// which hide each other's barriers and latencies; the one of 256 reads LDS and
-// L2 half as often for the same products and is 3% faster where there are many
-// of them.  Heads of 256 elements have one workgroup of 128 rows a CU: 0.86
+// workgroups a CU (which take all of its 160 KB of LDS, with 128 elements, and
+// up to 256 registers a lane each), which hide each other's barriers and
+// latencies; the one of 256 reads LDS and L2 half as often for the same products
+// and is 3% faster where sequences fill many of them.  Heads of 256 elements have one workgroup of 128 rows a CU: 0.86
 // PFLOP/s on 2048 tokens of 16 heads over 8192 keys.
 //
 // Matrix operands of 32x32x16: lane (n = lane % 32, h = lane / 32) holds eight
@@ -1058,6 +1058,8 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, const u
 // Bytes of LDS: K of two steps of 64 keys, V of three
 template <int DP>
 constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP;
+static_assert(2 * kChunkLds<128> <= 160 * 1024, "two workgroups a CU");
+static_assert(kChunkLds<256> <= 160 * 1024, "");
 
 template <int DP, int QB, int CAP, bool SHARED>
 __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,

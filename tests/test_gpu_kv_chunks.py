@@ -260,3 +260,27 @@ def test_sizes_that_would_be_cut(torch, sz):  # noqa: F811
         sz.sz_attend_workspace_size(2 ** 64 + 8, S.cache, S.batch)
     with pytest.raises(ValueError):
         sz.sz_attend_workspace_size(8, S.cache, S.batch, -1)
+
+
+@pytest.mark.parametrize("new,length", [(1, 300), (1, 5000), (200, 300), (200, 5000)])
+def test_ends_of_the_range(torch, sz, new, length):  # noqa: F811
+    """Values of 2^127 / 2^8 / keys, scores of 2^28 and scores that are all
+    -infinity (rows that see equal keys: the output is the value, to the
+    weights' rounding and the output's, the log-sum the score plus ln keys to
+    FP32's steps at that size)."""
+    S = Setup(torch, sz, [(new, length)], 8, 2, 64, 16, seed=57)
+    S.q.fill_(1.0)
+    for key, value in ((0.0, 2.0 ** 127 / 2 ** 8 / 8192), (2.0 ** 28 / 8, 3.0), (-math.inf, 3.0)):
+        S.k.fill_(key)
+        S.v.fill_(value)
+        S.upload()
+        out, lse = run(torch, sz, S)
+        out, lse = out.double(), lse.double()
+        say("ends", new, length, key, value)
+        if key == -math.inf:
+            assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+            continue
+        assert bool(((out - value).abs() <= value * (2 * ref.U16 + ref.U16 ** 2 + 2.0 ** -12)).all())
+        n = torch.arange(length - new, length)[:, None] + 1.0
+        want = key * 8 + n.double().log()
+        assert bool(((lse - want).abs() <= 8 * ref.U32 * want.abs() + 2.0 ** -16).all())
