@@ -1026,32 +1026,37 @@ __device__ __forceinline__ constexpr uint32_t v_mix(uint32_t j) {
 // m0 and the load, five between a vector instruction's write of a scalar
 // register (a lane read back, a reload of a spilled one) and it.  The compiler
 // keeps to that only around instructions that it knows, so the block itself
-// waits: the move and four states after it, once for up to four loads.
+// waits: the move and four states after it, once for all loads (a block for
+// every two or four of them: 2048 tokens of 64 heads of 128 on 32768 keys 2108
+// us, not 1908; of 16 heads of 256 on 8192 296, not 267).
 // (m0 is the compiler's to write just before an instruction that reads it and
 // never holds a value across others: it refuses it as a clobber.)
 template <int N>
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, const uint32_t* at,
                                             uint32_t lds) {
+#define SZ_FIRST_LOAD "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
 #define SZ_NEXT_LOAD(at) \
     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 " at ", %1, 0 offen lds\n\t"
-    static_assert(N == 2 || N % 4 == 0, "");
+    static_assert(N == 2 || N == 4 || N == 8, "");
     if constexpr (N == 2) {
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
-                     "buffer_load_dwordx4 %2, %1, 0 offen lds\n\t" SZ_NEXT_LOAD("%3")
+        asm volatile(SZ_FIRST_LOAD SZ_NEXT_LOAD("%3")
                      :
                      : "s"(lds), "s"(from), "v"(at[0]), "v"(at[1])
                      : "memory", "scc");
+    } else if constexpr (N == 4) {
+        asm volatile(SZ_FIRST_LOAD SZ_NEXT_LOAD("%3") SZ_NEXT_LOAD("%4") SZ_NEXT_LOAD("%5")
+                     :
+                     : "s"(lds), "s"(from), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+                     : "memory", "scc");
     } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
-                         "buffer_load_dwordx4 %2, %1, 0 offen lds\n\t" SZ_NEXT_LOAD("%3")
-                             SZ_NEXT_LOAD("%4") SZ_NEXT_LOAD("%5")
-                         :
-                         : "s"(lds + 1024 * i), "s"(from), "v"(at[i]), "v"(at[i + 1]),
-                           "v"(at[i + 2]), "v"(at[i + 3])
-                         : "memory", "scc");
+        asm volatile(SZ_FIRST_LOAD SZ_NEXT_LOAD("%3") SZ_NEXT_LOAD("%4") SZ_NEXT_LOAD("%5")
+                         SZ_NEXT_LOAD("%6") SZ_NEXT_LOAD("%7") SZ_NEXT_LOAD("%8") SZ_NEXT_LOAD("%9")
+                     :
+                     : "s"(lds), "s"(from), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]),
+                       "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
+                     : "memory", "scc");
     }
+#undef SZ_FIRST_LOAD
 #undef SZ_NEXT_LOAD
 }
 
