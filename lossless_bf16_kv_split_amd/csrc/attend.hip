@@ -106,9 +106,12 @@ constexpr uint64_t kCus = 256;
 // two a CU, one with 256-element heads.  Whole tiles where there are enough
 // of them to even out (kManyFew, kManyTiles), or where a tile has so few keys
 // that one workgroup is done with them in the time that the second launch
-// would take.  Few rows: by the bytes, which one CU gets at about 50 GB/s (9
-// sequences of 5 tokens under a window of 1024, 64 elements, 264 KB a tile:
-// 10.6 us whole, 14.4 shared out; 777 keys of 128, 398 KB: 12.1 and 11.2).
+// would take.  Few rows: by the bytes, which one CU gets at about 50 GB/s (one
+// token of 32 / 8 heads of 128, whole and shared out: 512 keys, 256 KB, 11.9 and
+// 12.7 us; 640, 12.4 and 13.1; 704, 13.6 and 13.4; 896, 14.8 and 13.0; of 64
+// elements: 1152 keys, 288 KB, 11.8 and 12.7; 1280, 13.5 and 12.3.  More
+// sequences stay better whole for longer: 32 of 768 keys 21 and 29; 9 of 5
+// tokens, 64 elements, 1536 keys 14.7 and 16.7).
 // Where they are many: 256 sequences of 1024 keys, 8 KV heads: 199 us whole,
 // 237 shared out; 128 of 2048: 210 and 198.
 // Tiles of 128 rows: 128 elements, 896 keys: 23.7 us whole, 30.1 shared out;
@@ -981,17 +984,17 @@ __global__ __launch_bounds__(WAVES * kWave, DP > 128 || WAVES > 4 ? 1 : 2) void 
 // 16 keys) while the step before is worked on, with one barrier a step.
 //
 // Bound by power: at 1.0 PFLOP/s under the counters the matrix cores are busy
-// 48% of the cycles, the vector units 41%, and the clock falls from 2.4 to
+// 50% of the cycles, the vector units 42%, and the clock falls from 2.4 to
 // 2.0 GHz (1.73 with a kernel that kept the former busy 55%), so what counts
 // is fewer instructions and fewer reads for the same products.  Measured:
-// 2048 tokens of 64 heads on 32768 keys 1.92 to 1.98 ms (1.08 to 1.11 PFLOP/s),
-// a prompt of 8192 tokens of 32 heads 0.53 to 0.55 ms (1.00 to 1.04); a library
-// product of 8192^3: 1.40.  With a cap on the scores, two more transcendental
-// instructions each, 15 to 26% slower.  The tile of 128 rows leaves room for two
+// 2048 tokens of 64 heads on 32768 keys 1.89 to 1.93 ms (1.11 to 1.13 PFLOP/s),
+// a prompt of 8192 tokens of 32 heads 0.53 ms (1.04); a library product of
+// 8192^3: 1.40.  With a cap on the scores, two more transcendental instructions
+// each, 15 to 30% slower.  The tile of 128 rows leaves room for two
 // workgroups a CU (which take all of its 160 KB of LDS, with 128 elements, and
 // up to 256 registers a lane each), which hide each other's barriers and
 // latencies; the one of 256 reads LDS and L2 half as often for the same products
-// and is 3% faster where sequences fill many of them.  Heads of 256 elements have one workgroup of 128 rows a CU: 0.86
+// and is 3% faster where sequences fill many of them.  Heads of 256 elements have one workgroup of 128 rows a CU: 0.89
 // PFLOP/s on 2048 tokens of 16 heads over 8192 keys.
 //
 // Matrix operands of 32x32x16: lane (n = lane % 32, h = lane / 32) holds eight
