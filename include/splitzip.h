@@ -598,6 +598,63 @@ sz_status sz_attend_pages(const sz_heads *q, const sz_heads *out, float *d_lse,
                           void *d_workspace, uint64_t workspace_bytes, int32_t *d_status,
                           hipStream_t stream);
 
+/* ---- a paged cache of latents ------------------------------------------
+ * Latent attention keeps one row per token, whatever the heads: a latent of
+ * latent_dim elements, from which every head's key and value are made, and
+ * rotary_dim elements of the key that are rotated and shared by the heads.
+ * The calls below append such rows and attend over them: in the absorbed
+ * form, where the projection of a head's keys has been multiplied into its
+ * query and the values' one is left to be applied to the output, so that a
+ * row is key and value at once (single tokens, drafts), and in the expanded
+ * form, where every head's keys and values have been made from the latents
+ * (prompts).  Rules of the calls above apply: streams, graphs, overlaps,
+ * row order, ragged batches, statuses. */
+typedef struct {
+    const void *const *d_pages; /* page c / page_tokens of sequence s: d_pages[s * table_pitch + ..] */
+    uint64_t pages_per_seq;     /* as in sz_kv_cache */
+    uint64_t table_pitch;
+    uint64_t token_stride;      /* elements from a token's row to the next's in a page, at least */
+                                /* latent_dim + rotary_dim; a multiple of 8, below 2^26 */
+    uint32_t latent_dim;        /* a multiple of 8, 8 .. 512 */
+    uint32_t rotary_dim;        /* a multiple of 8, 0 .. 64; its elements follow the latent's */
+    uint32_t page_tokens;       /* a power of two, 16 .. 65536 */
+} sz_latent_cache;
+
+/* Appends new tokens' rows: latents normed over their latent_dim elements
+ * (with a weight, as in sz_qk_norm_rope), rotary parts rotated, in FP32 and
+ * rounded once to BF16; with q given, the rotary parts of the queries'
+ * heads are rotated to q_out in the same launch.  Positions as in
+ * sz_kv_append.
+ *   latent    one head of latent_dim elements, BF16 or F32
+ *   k_rotary  one head of rotary_dim elements; NULL where that is 0
+ *   q, q_out  NULL, or rotary_dim > 0 and heads of as many elements: the
+ *             queries' rotary parts and their BF16 destination (in place
+ *             where q is BF16; usually the last elements of the rows that
+ *             sz_attend_latent takes)
+ *   d_weight  optional device float[latent_dim], 16-byte aligned
+ *   rope      NULL or rotary_dim 0: no rotation; else of cache->rotary_dim
+ *   d_status  as in sz_kv_append */
+sz_status sz_latent_append(const sz_heads *latent, const float *d_weight, float eps,
+                           const sz_heads *k_rotary, const sz_heads *q, const sz_heads *q_out,
+                           const sz_rope *rope, const int32_t *d_positions,
+                           const sz_latent_cache *cache, const sz_batch *batch,
+                           int32_t *d_status, hipStream_t stream);
+
+/* Attention of every new token over its sequence's latents, the absorbed
+ * form: scores are scale * (query head . row), over latent_dim + rotary_dim
+ * elements, the values a row's first latent_dim.  Positions, what a query
+ * sees, empty queries, accuracy, max_len, workspace and statuses as in
+ * sz_attend_pages, with one KV head, no window and no cap.
+ *   q    BF16, heads of latent_dim + rotary_dim elements
+ *   out  BF16 or F32, as many heads of latent_dim elements
+ *   n_tokens * heads < 2^31, n_tokens * heads / 128 + 2 * n_seqs < 2^24 */
+uint64_t sz_attend_latent_workspace_size(uint64_t heads, const sz_latent_cache *cache,
+                                         const sz_batch *batch, uint64_t max_len);
+sz_status sz_attend_latent(const sz_heads *q, const sz_heads *out, float *d_lse,
+                           const sz_latent_cache *cache, const sz_batch *batch, uint64_t max_len,
+                           float scale, int causal, void *d_workspace, uint64_t workspace_bytes,
+                           int32_t *d_status, hipStream_t stream);
+
 /* ---- compressed transfer to and from host memory ----------------------
  * The explainers present the codec as a way to shrink the KV transfer
  * between prefill and decode servers (introduction and "Les Resultats").

@@ -33,6 +33,8 @@ __all__ = [
     "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
     "sz_attend_workspace_size", "sz_attend_pages", "Heads", "KVCache", "Batch", "Rope",
     "rope_phases", "rope", "paged_cache", "qk_norm_rope", "kv_append", "attend_pages",
+    "sz_latent_append", "sz_attend_latent_workspace_size", "sz_attend_latent", "LatentCache",
+    "latent_cache", "latent_append", "attend_latent",
     "sz_status_string", "encode",
     "decode", "encode_blocks", "decode_blocks", "BlockContainers",
     "PREFIX_BYTES", "MAX_ELEMENTS", "NOALLOC_WORKSPACE_BYTES",
@@ -124,7 +126,12 @@ def _load() -> ctypes.CDLL:
     L.sz_attend_workspace_size.argtypes = [u64, p, p, u64]
     L.sz_attend_workspace_size.restype = u64
     L.sz_attend_pages.argtypes = [p, p, p, p, p, u64, f32, f32, i32, u64, p, u64, p, p]
-    for name in ("sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
+    L.sz_latent_append.argtypes = [p, p, f32, p, p, p, p, p, p, p, p, p]
+    L.sz_attend_latent_workspace_size.argtypes = [u64, p, p, u64]
+    L.sz_attend_latent_workspace_size.restype = u64
+    L.sz_attend_latent.argtypes = [p, p, p, p, p, u64, f32, i32, p, u64, p, p]
+    for name in ("sz_latent_append", "sz_attend_latent",
+                 "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
                  "sz_attend_pages", "sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
                  "sz_encode_pack", "sz_encode_pack_ranked", "sz_encode_sample",
                  "sz_encode_first_pass", "sz_encode_finish",
@@ -457,6 +464,29 @@ class KVCache(_Descriptor):
         self._set(k_pages.device, k_pages, v_pages, keep)
 
 
+class LatentCache(_Descriptor):
+    """sz_latent_cache: pages is an int64 CUDA tensor [sequences, pages] of
+    page addresses; token_stride in elements of a page (default: rows side
+    by side)."""
+    _fields_ = [("d_pages", ctypes.c_void_p), ("pages_per_seq", ctypes.c_uint64),
+                ("table_pitch", ctypes.c_uint64), ("token_stride", ctypes.c_uint64),
+                ("latent_dim", ctypes.c_uint32), ("rotary_dim", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32)]
+
+    def __init__(self, pages, latent_dim: int, rotary_dim: int, page_tokens: int,
+                 token_stride: int | None = None, keep=None):
+        import torch
+        _on_device(pages, torch.int64, "a page table", 2)
+        token_stride = latent_dim + rotary_dim if token_stride is None else token_stride
+        _fits(_U32, latent_dim, rotary_dim, page_tokens)
+        _fits(_U64, token_stride)
+        super().__init__(pages.data_ptr(), pages.shape[1],
+                         pages.stride(0) if pages.shape[0] > 1 else pages.shape[1], token_stride,
+                         latent_dim, rotary_dim, page_tokens)
+        self.rows = pages.shape[0]
+        self._set(pages.device, pages, keep)
+
+
 class Batch(_Descriptor):
     """sz_batch: starts and lens are int32 CUDA tensors of n_seqs + 1 and
     n_seqs entries; n_tokens is the row count of the token-major tensors."""
@@ -630,6 +660,51 @@ def sz_attend_pages(q, out, lse, cache, batch, max_len: int, scale: float, softc
         _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_attend_pages")
 
 
+def sz_latent_append(latent, weight, eps: float, k_rotary, q, q_out, rope, positions, cache,
+                     batch, d_status=None, stream=None) -> None:
+    """latent, k_rotary, q, q_out: Heads, or tensors [tokens, heads, elements]
+    (one head in the first two); cache: a LatentCache; batch: a Batch; rope: a
+    Rope or None."""
+    latent, k_rotary, q, q_out = _heads(latent), _heads(k_rotary), _heads(q), _heads(q_out)
+    stream = _call_stream(stream, cache, batch, latent, k_rotary, q, q_out, rope)
+    index, n = cache._index, batch.n_tokens
+    _tokens(n, latent, k_rotary, q, q_out)
+    _dims(cache.latent_dim, latent)
+    _dims(cache.rotary_dim, k_rotary, q, q_out)
+    _check_rows(cache, batch)
+    _check(_lib.sz_latent_append(
+        _at(latent), _array(weight, "float32", cache.latent_dim, index, "weight"), eps,
+        _at(k_rotary), _at(q), _at(q_out), _at(rope),
+        _array(positions, "int32", n, index, "positions"), cache._at, batch._at,
+        _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_latent_append")
+
+
+def sz_attend_latent_workspace_size(heads: int, cache, batch, max_len: int = 0) -> int:
+    _fits(_U64, heads, max_len)
+    return int(_lib.sz_attend_latent_workspace_size(heads, _at(cache), _at(batch), max_len))
+
+
+def sz_attend_latent(q, out, lse, cache, batch, max_len: int, scale: float, causal: bool = True,
+                     workspace=None, workspace_bytes: int = 0, d_status=None,
+                     stream=None) -> None:
+    """q, out: Heads, or tensors [tokens, heads, elements]; lse: a float32
+    tensor [tokens, heads] or None; cache: a LatentCache; batch: a Batch."""
+    q, out = _heads(q), _heads(out)
+    if not (0 <= max_len < _U64 and 0 <= workspace_bytes < _U64):
+        _fits(_U64, max_len, workspace_bytes)
+    stream = _call_stream(stream, cache, batch, q, out)
+    index, n = cache._index, batch.n_tokens
+    _tokens(n, q, out)
+    _dims(cache.latent_dim + cache.rotary_dim, q)
+    _dims(cache.latent_dim, out)
+    _check_rows(cache, batch)
+    _check(_lib.sz_attend_latent(
+        q._at, out._at, _array(lse, "float32", n * q.heads, index, "lse"), cache._at, batch._at,
+        max_len, scale, int(causal), _array(workspace, "uint8", workspace_bytes, index, "workspace"),
+        workspace_bytes, _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream),
+        "sz_attend_latent")
+
+
 # ---- conveniences (torch allocates; the library computes) -----------------
 
 def encode(x, stream=None):
@@ -749,6 +824,24 @@ def rope(rotary_dim: int, base: float = 10000.0, stretch: int = SZ_ROPE_PLAIN,
     return Rope(rope_phases(freq).to(device), interleaved, magnitude)
 
 
+def _bf16_pool(pool, dim: int) -> None:
+    import torch
+    _on_device(pool, torch.bfloat16, "a pool", dim)
+
+
+def _page_addresses(pool, table):
+    """The address table of a table of page numbers."""
+    import torch
+    if table.dim() != 2 or table.dtype not in (torch.int32, torch.int64) or \
+            table.device != pool.device:
+        raise ValueError("the table must be a 2-D integer tensor on the pools' device")
+    ids = table.to(torch.int64)
+    if ids.numel() > 0 and int(ids.max()) >= pool.shape[0]:
+        raise ValueError("a page number past the pool")
+    return torch.where(ids >= 0, pool.data_ptr() + ids * (pool.stride(0) * 2),
+                       torch.zeros_like(ids))
+
+
 def paged_cache(k_pool, v_pool, table) -> KVCache:
     """The cache of two pools [pages, page_tokens, kv_heads, head_dim] of
     bfloat16 (any strides that keep head_dim contiguous, so that a permuted
@@ -757,24 +850,22 @@ def paged_cache(k_pool, v_pool, table) -> KVCache:
     tables are made here (the largest page number is read back, which waits
     for the device); make the cache again when the table changes, or keep
     address tables of your own up to date and make a KVCache of them once."""
-    import torch
     for t in (k_pool, v_pool):
-        _on_device(t, torch.bfloat16, "a pool", 4)
+        _bf16_pool(t, 4)
     if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride():
         raise ValueError("the pools must have the same shape and strides")
-    if table.dim() != 2 or table.dtype not in (torch.int32, torch.int64) or \
-            not (table.device == k_pool.device == v_pool.device):
-        raise ValueError("the table must be a 2-D integer tensor on the pools' device")
-    ids = table.to(torch.int64)
-    if ids.numel() > 0 and int(ids.max()) >= k_pool.shape[0]:
-        raise ValueError("a page number past the pool")
-    step = k_pool.stride(0) * 2
+    return KVCache(_page_addresses(k_pool, table), _page_addresses(v_pool, table),
+                   k_pool.shape[2], k_pool.shape[3], k_pool.shape[1], k_pool.stride(1),
+                   k_pool.stride(2), keep=(k_pool, v_pool))
 
-    def addresses(pool):
-        return torch.where(ids >= 0, pool.data_ptr() + ids * step, torch.zeros_like(ids))
 
-    return KVCache(addresses(k_pool), addresses(v_pool), k_pool.shape[2], k_pool.shape[3],
-                   k_pool.shape[1], k_pool.stride(1), k_pool.stride(2), keep=(k_pool, v_pool))
+def latent_cache(pool, table, latent_dim: int) -> LatentCache:
+    """The latent cache of a pool [pages, page_tokens, latent_dim + rotary_dim]
+    of bfloat16 and an integer table [sequences, pages] of page numbers,
+    negative for none; as paged_cache."""
+    _bf16_pool(pool, 3)
+    return LatentCache(_page_addresses(pool, table), latent_dim, pool.shape[2] - latent_dim,
+                       pool.shape[1], pool.stride(1), keep=pool)
 
 
 def _raise_on(status, call: str) -> None:
@@ -832,4 +923,39 @@ def attend_pages(q, cache, batch, max_len: int = 0, scale: float | None = None,
                     size, status)
     if check:
         _raise_on(status, "sz_attend_pages")
+    return out, lse
+
+
+def latent_append(latent, cache, batch, k_rotary=None, rope=None, q=None, weight=None,
+                  eps: float = 1e-6, positions=None, check: bool = True):
+    """Append new tokens' latents [tokens, 1, latent_dim] and rotary parts
+    [tokens, 1, rotary_dim] to a cache of latents (sz_latent_append); returns
+    the turned rotary parts of the queries as a new bfloat16 tensor where q
+    is given (rows of no sequence are zero).  ``check`` as in kv_append."""
+    import torch
+    out = None if q is None else torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=latent.device) if check else None
+    sz_latent_append(latent, weight, eps, k_rotary, q, out, rope, positions, cache, batch, status)
+    if check:
+        _raise_on(status, "sz_latent_append")
+    return out
+
+
+def attend_latent(q, cache, batch, scale: float, max_len: int = 0, causal: bool = True,
+                  out_dtype=None, check: bool = True):
+    """Attention of absorbed queries [tokens, heads, latent_dim + rotary_dim]
+    over a cache of latents (sz_attend_latent); returns the output [tokens,
+    heads, latent_dim] (bfloat16 unless ``out_dtype`` is float32) and the
+    log-sums [tokens, heads], zero for rows of no sequence.  scale is that of
+    the heads before they were absorbed; ``check`` as in kv_append."""
+    import torch
+    out = torch.zeros((*q.shape[:2], cache.latent_dim), dtype=out_dtype or torch.bfloat16,
+                      device=q.device)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+    size = sz_attend_latent_workspace_size(q.shape[1], cache, batch, max_len)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=q.device) if check else None
+    sz_attend_latent(q, out, lse, cache, batch, max_len, scale, causal, ws, size, status)
+    if check:
+        _raise_on(status, "sz_attend_latent")
     return out, lse

@@ -104,6 +104,77 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&x)[VEC]) {
 
 enum { kNoTurn = 0, kHalves = 1, kInterleaved = 2 };
 
+// The angles of a lane that holds VEC elements of a row from element e on
+template <int VEC, int MODE>
+struct Angles {
+    static constexpr int kCount = MODE == kInterleaved ? VEC / 2 : VEC;
+    float c[kCount], sn[kCount];
+    uint32_t partner;  // the lane with the pairs' other halves
+    bool turns;
+
+    __device__ __forceinline__ Angles(const Turn& t, uint32_t e, uint32_t lane, int32_t position) {
+        const uint32_t half = t.dims / 2;
+        turns = MODE != kNoTurn && e < t.dims;
+        const bool lower = e < half;
+        partner = lane;
+        if (MODE == kHalves && turns) partner = lower ? lane + half / VEC : lane - half / VEC;
+        if (turns) {
+            const uint32_t first = MODE == kInterleaved ? e / 2 : lower ? e : e - half;
+            const uint32_t far = position < 0 ? 0u - (uint32_t)position : (uint32_t)position;
+#pragma unroll
+            for (int i = 0; i < kCount; i++) {
+                const uint64_t turn = (uint64_t)far * t.phases[first + i];
+                turn_of((uint32_t)(turn >> 32), c[i], sn[i]);
+                c[i] *= t.magnitude;
+                sn[i] *= position < 0 ? -t.magnitude : t.magnitude;
+                if (MODE == kHalves && lower) sn[i] = -sn[i];
+            }
+        }
+    }
+    // (every lane of the wave calls this: halves pass between lanes)
+    __device__ __forceinline__ void turn(float (&x)[VEC]) const {
+        if constexpr (MODE == kHalves) {
+#pragma unroll
+            for (int i = 0; i < VEC; i++) {
+                const float other = __shfl(x[i], partner);
+                if (turns) x[i] = fmaf(x[i], c[i], other * sn[i]);
+            }
+        } else if constexpr (MODE == kInterleaved) {
+            if (turns) {
+#pragma unroll
+                for (int i = 0; i < VEC / 2; i++) {
+                    const float u = x[2 * i], v = x[2 * i + 1];
+                    x[2 * i] = fmaf(u, c[i], -v * sn[i]);
+                    x[2 * i + 1] = fmaf(v, c[i], u * sn[i]);
+                }
+            }
+        }
+    }
+};
+
+// Where a new token goes in the cache; `there`: it has a place.
+struct Place {
+    uint64_t entry;  // of the page tables
+    uint64_t slot;   // elements into the page
+    int32_t position;
+    bool there;
+};
+__device__ __forceinline__ Place find_place(const Cache& cache, const Batch& batch,
+                                            uint64_t token) {
+    Place p{};
+    const uint32_t s = find_seq(batch.n_seqs, (int64_t)token,
+                                [&](uint32_t i) { return (int64_t)batch.starts[i]; });
+    const Seq q = load_seq(batch, s, (int64_t)(cache.pages_per_seq << cache.page_log2));
+    if (!q.good || (int64_t)token < q.begin || (int64_t)token >= q.end) return p;
+    const int64_t c = (int64_t)q.len - q.end + (int64_t)token;
+    if (c < 0) return p;
+    p.entry = (uint64_t)s * cache.table_pitch + ((uint64_t)c >> cache.page_log2);
+    p.slot = ((uint64_t)c & ((1u << cache.page_log2) - 1)) * cache.token_stride;
+    p.position = (int32_t)c;
+    p.there = true;
+    return p;
+}
+
 // LANES lanes hold a row, VEC elements each; slices waves share a token.
 template <int LANES, int VEC, int MODE, bool APPEND>
 __global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batch batch,
@@ -120,43 +191,19 @@ __global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batc
     uint64_t k_page = 0, v_page = 0, slot = 0;
     int32_t position = 0;
     if constexpr (APPEND) {
-        const uint32_t s = find_seq(batch.n_seqs, (int64_t)token,
-                                    [&](uint32_t i) { return (int64_t)batch.starts[i]; });
-        const Seq q = load_seq(batch, s, (int64_t)(cache.pages_per_seq << cache.page_log2));
-        if (!q.good || (int64_t)token < q.begin || (int64_t)token >= q.end) return;
-        const int64_t c = (int64_t)q.len - q.end + (int64_t)token;
-        if (c < 0) return;
-        const uint64_t entry = (uint64_t)s * cache.table_pitch + ((uint64_t)c >> cache.page_log2);
-        k_page = cache.k_pages[entry];
-        v_page = cache.v_pages[entry];
-        slot = ((uint64_t)c & ((1u << cache.page_log2) - 1)) * cache.token_stride;
-        position = (int32_t)c;
+        const Place place = find_place(cache, batch, token);
+        if (!place.there) return;
+        k_page = cache.k_pages[place.entry];
+        v_page = cache.v_pages[place.entry];
+        slot = place.slot;
+        position = place.position;
     }
     if (MODE != kNoTurn && a.positions != nullptr) position = a.positions[token];
 
     const uint32_t l = lane % LANES;
     const uint32_t e = l * VEC;  // this lane's first element
     const bool live = e < a.head_dim;
-    // the lane's angles
-    constexpr int kAngles = MODE == kInterleaved ? VEC / 2 : VEC;
-    float c[kAngles], sn[kAngles];
-    const uint32_t half = a.turn.dims / 2;
-    const bool turns = MODE != kNoTurn && e < a.turn.dims;
-    const bool lower = e < half;
-    uint32_t partner = lane;
-    if (MODE == kHalves && turns) partner = lower ? lane + half / VEC : lane - half / VEC;
-    if (turns) {
-        const uint32_t first = MODE == kInterleaved ? e / 2 : lower ? e : e - half;
-        const uint32_t far = position < 0 ? 0u - (uint32_t)position : (uint32_t)position;
-#pragma unroll
-        for (int i = 0; i < kAngles; i++) {
-            const uint64_t turn = (uint64_t)far * a.turn.phases[first + i];
-            turn_of((uint32_t)(turn >> 32), c[i], sn[i]);
-            c[i] *= a.turn.magnitude;
-            sn[i] *= position < 0 ? -a.turn.magnitude : a.turn.magnitude;
-            if (MODE == kHalves && lower) sn[i] = -sn[i];
-        }
-    }
+    const Angles<VEC, MODE> angles(a.turn, e, lane, position);
 
     // the rows of queries and keys, the next one's load under way
     const uint32_t turned = a.q.heads + a.k.heads;
@@ -190,22 +237,7 @@ __global__ __launch_bounds__(kThreads) void k_turn(TurnRows a, Cache cache, Batc
 #pragma unroll
             for (int i = 0; i < VEC; i++) x[i] = x[i] * inv * weight[e + i];
         }
-        if constexpr (MODE == kHalves) {
-#pragma unroll
-            for (int i = 0; i < VEC; i++) {
-                const float other = __shfl(x[i], partner);
-                if (turns) x[i] = fmaf(x[i], c[i], other * sn[i]);
-            }
-        } else if constexpr (MODE == kInterleaved) {
-            if (turns) {
-#pragma unroll
-                for (int i = 0; i < VEC / 2; i++) {
-                    const float u = x[2 * i], v = x[2 * i + 1];
-                    x[2 * i] = fmaf(u, c[i], -v * sn[i]);
-                    x[2 * i + 1] = fmaf(v, c[i], u * sn[i]);
-                }
-            }
-        }
+        angles.turn(x);
         if (on) {
             if (APPEND && is_k) {
                 if (good_page(k_page))
@@ -284,6 +316,91 @@ hipError_t launch(const TurnRows& a, const Cache& cache, const Batch& batch, hip
     return pick<kHalves, APPEND>(a, cache, batch, stream);
 }
 
+// A new token's latent (normed with a weight) and its key's rotary part go to
+// its row of a latent page, side by side; the rotary parts of its queries are
+// turned beside them.  The latent row lies across a wave, 8 elements a lane; of
+// rotary rows (the key's first, then the queries') a wave holds as many as it
+// has LANES.  Slices as in k_turn; the first one has the latent.
+template <int LANES, int VEC, int MODE>
+__global__ __launch_bounds__(kThreads) void k_latent_append(LatentRows a, Cache cache, Batch batch,
+                                                            uint32_t slices, uint32_t first) {
+    constexpr uint32_t kRows = kWave / LANES;
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint64_t wave =
+        (uint64_t)blockIdx.x * kWavesPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint64_t token = first + wave / slices;
+    const uint32_t slice = (uint32_t)(wave % slices);
+    if (token >= a.n_tokens) return;
+    float x[8] = {};
+    const uint32_t e8 = 8 * lane;
+    const bool latent = slice == 0, on8 = latent && e8 < a.latent_dim;
+    if (on8) load_row<8>(a.latent, token * a.latent.token_stride + e8, x);  // (before the lookups)
+    const Place place = find_place(cache, batch, token);
+    if (!place.there) return;
+    const uint64_t page = cache.k_pages[place.entry];
+    uint16_t* row = reinterpret_cast<uint16_t*>(page) + place.slot;
+    const int32_t position =
+        MODE != kNoTurn && a.positions != nullptr ? a.positions[token] : place.position;
+
+    const uint32_t e = lane % LANES * VEC;
+    const bool live = e < a.rotary_dim;
+    const uint32_t rows = (a.rotary_dim != 0) + a.q.heads, stride = slices * kRows;
+    const auto load = [&](uint32_t r, float (&y)[VEC]) {
+        if (!live || r >= rows) return;
+        if (r == 0) load_row<VEC>(a.k, token * a.k.token_stride + e, y);
+        else load_row<VEC>(a.q, token * a.q.token_stride + (r - 1) * a.q.head_stride + e, y);
+    };
+    float next[VEC] = {};
+    load(slice * kRows + lane / LANES, next);
+
+    if (latent) {
+        if (a.weight != nullptr) {
+            float sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+            for (int d = 1; d < (int)kWave; d *= 2) sum += __shfl_xor(sum, d);
+            const float inv = 1.0f / sqrtf(sum / (float)a.latent_dim + a.eps);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (on8) x[i] = x[i] * inv * a.weight[e8 + i];
+        }
+        if (on8 && good_page(page)) store_row<8>(row + e8, x);
+    }
+
+    const Angles<VEC, MODE> angles(a.turn, e, lane, position);
+    for (uint32_t r0 = slice * kRows; r0 < rows; r0 += stride) {
+        const uint32_t r = r0 + lane / LANES;
+        float y[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; i++) y[i] = next[i];
+        load(r + stride, next);
+        angles.turn(y);
+        if (!live || r >= rows) continue;
+        if (r == 0) {
+            if (good_page(page)) store_row<VEC>(row + a.latent_dim + e, y);
+        } else {
+            store_row<VEC>(static_cast<uint16_t*>(a.q_out.data) + token * a.q_out.token_stride +
+                               (r - 1) * a.q_out.head_stride + e, y);
+        }
+    }
+}
+
+template <int LANES, int VEC, int MODE>
+hipError_t go(const LatentRows& a, const Cache& cache, const Batch& batch, hipStream_t stream) {
+    const uint64_t most = (1 + (uint64_t)a.q.heads + kWave / LANES - 1) / (kWave / LANES);
+    uint64_t slices = (kFillWaves + a.n_tokens - 1) / a.n_tokens;
+    slices = slices < 1 ? 1 : slices > most ? most : slices;
+    for (uint64_t first = 0; first < a.n_tokens; first += kMostTokens) {
+        const uint64_t tokens = a.n_tokens - first < kMostTokens ? a.n_tokens - first : kMostTokens;
+        const uint64_t groups = (tokens * slices + kWavesPerGroup - 1) / kWavesPerGroup;
+        k_latent_append<LANES, VEC, MODE><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(
+            a, cache, batch, (uint32_t)slices, (uint32_t)first);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
+}
+
 // Sequences are found by a search over their starts, which finds one's rows
 // for certain where no start before its own lies above it and none after
 // lies below its end.  A wave takes `each` (at most 32) sequences: it reads
@@ -336,6 +453,16 @@ hipError_t launch_append(const TurnRows& a, const Cache& cache, const Batch& bat
                          hipStream_t stream) {
     if (batch.n_seqs == 0) return hipSuccess;
     return launch<true>(a, cache, batch, stream);
+}
+
+hipError_t launch_latent_append(const LatentRows& a, const Cache& cache, const Batch& batch,
+                                hipStream_t stream) {
+    if (batch.n_seqs == 0 || a.n_tokens == 0) return hipSuccess;
+    if (a.turn.dims == 0) return go<8, 8, kNoTurn>(a, cache, batch, stream);
+    if (a.turn.interleaved) return go<8, 8, kInterleaved>(a, cache, batch, stream);
+    // (a lane's elements must not straddle the halves)
+    if (a.turn.dims % 16 != 0) return go<16, 4, kHalves>(a, cache, batch, stream);
+    return go<8, 8, kHalves>(a, cache, batch, stream);
 }
 
 hipError_t launch_check_seqs(const SeqCheck& c, hipStream_t stream) {

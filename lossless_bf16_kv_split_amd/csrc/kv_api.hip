@@ -71,8 +71,9 @@ Span span(const sz_heads& t, uint64_t tokens, uint64_t dim) {
 
 // Whether a call that writes b may have a beside it: apart, in place (the
 // caller says whether that is allowed), or slices of the same tokens or heads.
-bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, bool in_place) {
-    const Span x = span(a, tokens, dim), y = span(b, tokens, dim);
+bool apart(const sz_heads& a, uint64_t a_dim, const sz_heads& b, uint64_t b_dim, uint64_t tokens,
+           bool in_place) {
+    const Span x = span(a, tokens, a_dim), y = span(b, tokens, b_dim);
     if (x.end <= y.begin || y.end <= x.begin) return true;
     if (in_place && a.data == b.data && a.type == b.type && a.heads == b.heads &&
         a.token_stride == b.token_stride && a.head_stride == b.head_stride)
@@ -81,8 +82,8 @@ bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, 
     // before the other
     const uint64_t step = a.token_stride * size_of(a.type);
     if (step == 0 || step != b.token_stride * size_of(b.type)) return false;
-    const uint64_t a_bytes = ((a.heads - 1) * a.head_stride + dim) * size_of(a.type);
-    const uint64_t b_bytes = ((b.heads - 1) * b.head_stride + dim) * size_of(b.type);
+    const uint64_t a_bytes = ((a.heads - 1) * a.head_stride + a_dim) * size_of(a.type);
+    const uint64_t b_bytes = ((b.heads - 1) * b.head_stride + b_dim) * size_of(b.type);
     const uint64_t ahead = x.begin <= y.begin ? (y.begin - x.begin) % step
                                               : (step - (x.begin - y.begin) % step) % step;
     if (ahead >= a_bytes && ahead + b_bytes <= step) return true;
@@ -92,8 +93,11 @@ bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, 
     const uint64_t head = a.head_stride * size_of(a.type);
     if (head == 0 || head != b.head_stride * size_of(b.type)) return false;
     const uint64_t in_head = ahead % head;
-    return in_head >= dim * size_of(a.type) && in_head + dim * size_of(b.type) <= head &&
+    return in_head >= a_dim * size_of(a.type) && in_head + b_dim * size_of(b.type) <= head &&
            (step % head == 0 || (a_bytes <= step && ahead + b_bytes <= step));
+}
+bool apart(const sz_heads& a, const sz_heads& b, uint64_t tokens, uint64_t dim, bool in_place) {
+    return apart(a, dim, b, dim, tokens, in_place);
 }
 
 bool overlap(const void* p, uint64_t bytes, Span s) {
@@ -107,16 +111,19 @@ sz::Rows rows_of(const sz_heads* t) {
                     t->type == SZ_TYPE_F32};
 }
 
+bool table_ok(uint64_t pages_per_seq, uint64_t table_pitch, uint32_t page_tokens) {
+    if (page_tokens < 16 || page_tokens > 65536 || (page_tokens & (page_tokens - 1)) != 0)
+        return false;
+    return pages_per_seq > 0 && pages_per_seq <= kMaxTokens && table_pitch >= pages_per_seq &&
+           table_pitch <= (uint64_t{1} << 40);
+}
+
 bool cache_ok(const sz_kv_cache* c) {
     if (c == nullptr || c->d_k_pages == nullptr || c->d_v_pages == nullptr ||
         !aligned(c->d_k_pages, 8) || !aligned(c->d_v_pages, 8))
         return false;
-    if (!head_dim_ok(c->head_dim) || c->kv_heads == 0 || c->kv_heads > kMaxHeads) return false;
-    if (c->page_tokens < 16 || c->page_tokens > 65536 ||
-        (c->page_tokens & (c->page_tokens - 1)) != 0)
-        return false;
-    if (c->pages_per_seq == 0 || c->pages_per_seq > kMaxTokens ||
-        c->table_pitch < c->pages_per_seq || c->table_pitch > (uint64_t{1} << 40))
+    if (!head_dim_ok(c->head_dim) || c->kv_heads == 0 || c->kv_heads > kMaxHeads ||
+        !table_ok(c->pages_per_seq, c->table_pitch, c->page_tokens))
         return false;
     return strides_ok(c->token_stride, c->head_stride) && c->token_stride < kMaxPageStride &&
            rows_apart(c->page_tokens, c->kv_heads, c->token_stride, c->head_stride, c->head_dim);
@@ -129,6 +136,25 @@ sz::Cache cache_of(const sz_kv_cache& c) {
                      reinterpret_cast<const uint64_t*>(c.d_v_pages),
                      c.pages_per_seq, c.table_pitch, c.token_stride, c.head_stride,
                      c.kv_heads, c.head_dim, lg};
+}
+
+bool latent_dims_ok(uint64_t latent, uint64_t rotary) {
+    return latent >= 8 && latent <= 512 && latent % 8 == 0 && rotary <= 64 && rotary % 8 == 0;
+}
+
+bool latent_ok(const sz_latent_cache* c) {
+    if (c == nullptr || c->d_pages == nullptr || !aligned(c->d_pages, 8) ||
+        !latent_dims_ok(c->latent_dim, c->rotary_dim) ||
+        !table_ok(c->pages_per_seq, c->table_pitch, c->page_tokens))
+        return false;
+    return c->token_stride % 8 == 0 && c->token_stride < kMaxPageStride &&
+           c->token_stride >= c->latent_dim + c->rotary_dim;
+}
+
+// A cache of one head, whose keys and values are the same rows
+sz_kv_cache rows_of(const sz_latent_cache& c) {
+    return sz_kv_cache{c.d_pages, c.d_pages, c.pages_per_seq, c.table_pitch, c.token_stride, 0, 1,
+                       c.latent_dim + c.rotary_dim, c.page_tokens};
 }
 
 bool batch_ok(const sz_batch* b) {
@@ -344,11 +370,101 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
     if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
     if (sz_status s = check_stream(stream)) return s;
     const sz::Attend a{rows_of(q), rows_of(out), d_lse, cache_of(*cache), batch_of(*batch),
-                       (int64_t)max_len, scale, softcap, causal != 0, window};
+                       (int64_t)max_len, scale, softcap, causal != 0, window, dim};
     sz_status st = hip_status(sz::launch_attend(a, static_cast<uint8_t*>(d_workspace), stream));
     if (st == SZ_OK && d_status != nullptr)
         st = hip_status(sz::launch_check_seqs(
             sz::SeqCheck{a.cache, a.batch, a.max_len, 0, a.causal, window, d_status}, stream));
+    return st;
+}
+
+sz_status sz_latent_append(const sz_heads* latent, const float* d_weight, float eps,
+                           const sz_heads* k_rotary, const sz_heads* q, const sz_heads* q_out,
+                           const sz_rope* rope, const int32_t* d_positions,
+                           const sz_latent_cache* cache, const sz_batch* batch,
+                           int32_t* d_status, hipStream_t stream) {
+    if (!latent_ok(cache) || !batch_ok(batch)) return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t n = batch->n_tokens;
+    const uint32_t dim = cache->latent_dim, rotary = cache->rotary_dim;
+    if (!rope_ok(rope, rotary) ||
+        (rope != nullptr && rope->rotary_dim != 0 && rope->rotary_dim != rotary) ||
+        !heads_ok(latent, n, dim, false) || latent->heads != 1 || !aligned(d_weight, 16))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if ((k_rotary == nullptr) != (rotary == 0) || (q == nullptr) != (q_out == nullptr) ||
+        (q != nullptr && rotary == 0))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (k_rotary != nullptr && (!heads_ok(k_rotary, n, rotary, false) || k_rotary->heads != 1))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (q != nullptr && !(turned_ok(q, q_out, nullptr, n, rotary) &&
+                          apart(*latent, dim, *q_out, rotary, n, false) &&
+                          apart(*k_rotary, *q_out, n, rotary, false)))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0) || !std::isfinite(eps) || !aligned(d_positions, 4) || !aligned(d_status, 4))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
+    if (sz_status s = check_stream(stream)) return s;
+    const sz_kv_cache rows = rows_of(*cache);
+    const sz::Cache c = cache_of(rows);
+    const sz::Batch b = batch_of(*batch);
+    const sz::LatentRows a{rows_of(latent), rows_of(k_rotary), rows_of(q), rows_of(q_out),
+                           d_weight, d_positions, turn_of(rope), eps, dim, rotary, (uint32_t)n};
+    sz_status st = hip_status(sz::launch_latent_append(a, c, b, stream));
+    if (st == SZ_OK && d_status != nullptr)
+        st = hip_status(sz::launch_check_seqs(
+            sz::SeqCheck{c, b, (int64_t)most_len(rows), 1, 1, 0, d_status}, stream));
+    return st;
+}
+
+uint64_t sz_attend_latent_workspace_size(uint64_t heads, const sz_latent_cache* cache,
+                                         const sz_batch* batch, uint64_t max_len) {
+    if (cache == nullptr || batch == nullptr ||
+        !latent_dims_ok(cache->latent_dim, cache->rotary_dim) || heads == 0 || heads > kMaxHeads ||
+        !table_ok(cache->pages_per_seq, cache->table_pitch, cache->page_tokens) ||
+        batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxTokens ||
+        !attend_fits(batch->n_seqs, batch->n_tokens, heads, 1) || batch->n_seqs == 0 ||
+        batch->n_tokens == 0)
+        return 0;
+    const sz_kv_cache rows = rows_of(*cache);
+    const uint64_t most = most_len(rows);
+    return sz::attend_latent_workspace((uint32_t)heads, cache_of(rows), cache->latent_dim,
+                                       batch->n_seqs, batch->n_tokens,
+                                       max_len == 0 || max_len > most ? most : max_len);
+}
+
+sz_status sz_attend_latent(const sz_heads* q, const sz_heads* out, float* d_lse,
+                           const sz_latent_cache* cache, const sz_batch* batch, uint64_t max_len,
+                           float scale, int causal, void* d_workspace, uint64_t workspace_bytes,
+                           int32_t* d_status, hipStream_t stream) {
+    if (!latent_ok(cache) || !batch_ok(batch)) return SZ_ERR_INVALID_ARGUMENT;
+    const sz_kv_cache rows = rows_of(*cache);
+    const uint64_t n = batch->n_tokens;
+    const uint32_t dim = rows.head_dim, value = cache->latent_dim;
+    if (!heads_ok(q, n, dim, false) || !heads_ok(out, n, value, true) ||
+        q->type != SZ_TYPE_BF16 || q->heads != out->heads ||
+        !attend_fits(batch->n_seqs, n, q->heads, 1) || !apart(*q, dim, *out, value, n, false))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (!(scale > 0 && scale < 1e38f) || !aligned(d_lse, 4) || !aligned(d_status, 4))
+        return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t most = most_len(rows);
+    if (max_len == 0 || max_len > most) max_len = most;
+    const uint64_t lse_bytes = d_lse == nullptr ? 0 : 4 * n * q->heads;
+    if (overlap(d_lse, lse_bytes, span(*q, n, dim)) ||
+        overlap(d_lse, lse_bytes, span(*out, n, value)))
+        return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t need = sz_attend_latent_workspace_size(q->heads, cache, batch, max_len);
+    if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 256) ||
+                     workspace_bytes < need || overlap(d_workspace, need, span(*q, n, dim)) ||
+                     overlap(d_workspace, need, span(*out, n, value))))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
+    if (sz_status s = check_stream(stream)) return s;
+    const sz::Attend a{rows_of(q), rows_of(out), d_lse, cache_of(rows), batch_of(*batch),
+                       (int64_t)max_len, scale, 0, causal != 0, 0, value};
+    sz_status st =
+        hip_status(sz::launch_attend_latent(a, static_cast<uint8_t*>(d_workspace), stream));
+    if (st == SZ_OK && d_status != nullptr)
+        st = hip_status(sz::launch_check_seqs(
+            sz::SeqCheck{a.cache, a.batch, a.max_len, 0, a.causal, 0, d_status}, stream));
     return st;
 }
 

@@ -99,6 +99,19 @@ hipError_t launch_turn(const TurnRows& a, hipStream_t stream);
 hipError_t launch_append(const TurnRows& a, const Cache& cache, const Batch& batch,
                          hipStream_t stream);
 
+// New tokens of a latent cache: k_pages and v_pages of its Cache are the same
+// table, its one head's rows latent and rotary part together.
+struct LatentRows {
+    Rows latent, k, q, q_out;  // k without rotary part, q where absent: no heads
+    const float* weight;
+    const int32_t* positions;
+    Turn turn;
+    float eps;
+    uint32_t latent_dim, rotary_dim, n_tokens;
+};
+hipError_t launch_latent_append(const LatentRows& a, const Cache& cache, const Batch& batch,
+                                hipStream_t stream);
+
 struct Attend {
     Rows q, out;
     float* lse;
@@ -108,11 +121,17 @@ struct Attend {
     float scale, softcap;
     uint32_t causal;
     uint64_t window;
+    uint32_t value_dim;  // elements of an output row
 };
 // Bytes of workspace that launch_attend may use, whatever the window.
 uint64_t attend_workspace(uint32_t q_heads, const Cache& cache, uint64_t n_seqs,
                           uint64_t n_tokens, uint64_t max_len);
 hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream);
+
+// The same over a latent cache: value_dim is the latent's
+uint64_t attend_latent_workspace(uint32_t heads, const Cache& cache, uint32_t latent_dim,
+                                 uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len);
+hipError_t launch_attend_latent(const Attend& a, uint8_t* ws, hipStream_t stream);
 
 // Every sequence's status: one wave per sequence checks its range, its
 // length and the pages that the call touches (append: those of the new
