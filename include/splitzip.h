@@ -655,6 +655,80 @@ sz_status sz_attend_latent(const sz_heads *q, const sz_heads *out, float *d_lse,
                            float scale, int causal, void *d_workspace, uint64_t workspace_bytes,
                            int32_t *d_status, hipStream_t stream);
 
+/* ---- eviction from a paged cache ---------------------------------------
+ * A cache over its budget gives up the tokens that attention has looked at
+ * the least: sz_weigh_pages adds up what each cached token has received,
+ * step by step, beside sz_attend_pages; sz_evict_pages picks the tokens that
+ * stay and copies their rows into other pages. */
+
+/* The attention weight that cached tokens receive from a call's new tokens:
+ * for KV head v of sequence s and every cached position j < d_lens[s]
+ *   w[s][v][j] = keep * before[s][v][j] + sum exp(score - lse)
+ * over the rows (new tokens and query heads of v) that see j, with the
+ * scores and visibility of sz_attend_pages and the log-sums that it left in
+ * d_lse.  The new tokens' own positions (the last ones) have no `before`;
+ * entries from d_lens[s] on are left as they were.  A row whose log-sum is
+ * -infinity adds nothing; a row adds nothing to keys that it does not see,
+ * whatever its bits and theirs.  FP32 throughout; the order of additions is
+ * fixed by the call's sizes.  Only keys are read: d_v_pages of the cache may be
+ * the key table.
+ *   q, d_lse   as sz_attend_pages took and left them (d_lse float[n_tokens]
+ *              [q heads]); limits of q's heads and tokens as there
+ *   d_before   optional device float[n_seqs][kv_heads][weights_pitch]; not read
+ *              where it is NULL or keep is 0.  May be d_weights
+ *   d_weights  device float[n_seqs][kv_heads][weights_pitch]
+ *   weights_pitch  >= max_len (or what stands for it), < 2^31
+ *   keep       finite
+ *   max_len, scale, softcap, causal, window   as in sz_attend_pages
+ *   d_workspace, workspace_bytes   256-byte aligned, at least
+ *              sz_weigh_workspace_size of the same sizes; any content; NULL
+ *              where that is 0
+ *   d_status   as in sz_attend_pages; the weights of a sequence at fault are
+ *              unspecified or as they were */
+uint64_t sz_weigh_workspace_size(uint64_t q_heads, const sz_kv_cache *cache,
+                                 const sz_batch *batch, uint64_t max_len);
+sz_status sz_weigh_pages(const sz_heads *q, const float *d_lse, const float *d_before,
+                         float *d_weights, uint64_t weights_pitch, float keep,
+                         const sz_kv_cache *cache, const sz_batch *batch, uint64_t max_len,
+                         float scale, float softcap, int causal, uint64_t window,
+                         void *d_workspace, uint64_t workspace_bytes, int32_t *d_status,
+                         hipStream_t stream);
+
+/* Eviction: of each sequence's d_lens[s] cached tokens at most `budget`
+ * stay: the first `first`, the last `recent`, and of those between them the
+ * ones with the largest weights (of equal weights the earlier; NaN counts as
+ * less than any number).  The rows of those that stay are copied, in
+ * their order, to positions 0, 1, .. of the sequence's pages in `to`, their
+ * weights to d_weights_to, and their old positions are written to d_kept (-1
+ * from the number of those that stay on).  With weight_heads = kv_heads every
+ * KV head keeps tokens of its own; with weight_heads = 1 all keep the same.
+ * Keys stay as they were rotated: new tokens go on at the positions that they
+ * would have had (d_positions of sz_kv_append).  All of a sequence that is
+ * within the budget is copied as it is.
+ *   d_weights     device float[n_seqs][weight_heads][weights_pitch]
+ *   d_weights_to  device float[n_seqs][weight_heads][budget]; entries past
+ *                 those that stay are left as they were
+ *   d_kept        device i32[n_seqs][weight_heads][budget]
+ *   from, to      caches of the same kv_heads and head_dim; pages and strides
+ *                 may differ.  `to` must have room for min(budget, max_len)
+ *                 tokens, and its written pages must not be pages that the
+ *                 call reads: pages shared by other sequences stay as they are
+ *   d_lens, d_lens_to   device i32[n_seqs], apart: tokens before and after
+ *   n_seqs        0 .. 65535; n_seqs * weight_heads and n_seqs * budget / 16
+ *                 below 2^22 and 2^24
+ *   max_len       as in sz_attend_pages, <= weights_pitch
+ *   budget        1 .. 2^30, >= first + recent
+ *   d_status      optional device i32[n_seqs]: SZ_OK, or
+ *                 SZ_ERR_INVALID_ARGUMENT for a sequence whose length is
+ *                 negative or above max_len (none of its tokens stays), or one
+ *                 of whose pages, read or written, is NULL or misaligned (rows
+ *                 there are not copied) */
+sz_status sz_evict_pages(const float *d_weights, uint64_t weight_heads, uint64_t weights_pitch,
+                         const sz_kv_cache *from, const int32_t *d_lens, uint64_t n_seqs,
+                         uint64_t max_len, uint64_t budget, uint64_t first, uint64_t recent,
+                         const sz_kv_cache *to, float *d_weights_to, int32_t *d_kept,
+                         int32_t *d_lens_to, int32_t *d_status, hipStream_t stream);
+
 /* ---- compressed transfer to and from host memory ----------------------
  * The explainers present the codec as a way to shrink the KV transfer
  * between prefill and decode servers (introduction and "Les Resultats").

@@ -35,6 +35,7 @@ __all__ = [
     "rope_phases", "rope", "paged_cache", "qk_norm_rope", "kv_append", "attend_pages",
     "sz_latent_append", "sz_attend_latent_workspace_size", "sz_attend_latent", "LatentCache",
     "latent_cache", "latent_append", "attend_latent",
+    "sz_weigh_workspace_size", "sz_weigh_pages", "sz_evict_pages", "weigh_pages", "evict_pages",
     "sz_status_string", "encode",
     "decode", "encode_blocks", "decode_blocks", "BlockContainers",
     "PREFIX_BYTES", "MAX_ELEMENTS", "NOALLOC_WORKSPACE_BYTES",
@@ -130,7 +131,11 @@ def _load() -> ctypes.CDLL:
     L.sz_attend_latent_workspace_size.argtypes = [u64, p, p, u64]
     L.sz_attend_latent_workspace_size.restype = u64
     L.sz_attend_latent.argtypes = [p, p, p, p, p, u64, f32, i32, p, u64, p, p]
-    for name in ("sz_latent_append", "sz_attend_latent",
+    L.sz_weigh_workspace_size.argtypes = [u64, p, p, u64]
+    L.sz_weigh_workspace_size.restype = u64
+    L.sz_weigh_pages.argtypes = [p, p, p, p, u64, f32, p, p, u64, f32, f32, i32, u64, p, u64, p, p]
+    L.sz_evict_pages.argtypes = [p, u64, u64, p, p, u64, u64, u64, u64, u64, p, p, p, p, p, p]
+    for name in ("sz_latent_append", "sz_attend_latent", "sz_weigh_pages", "sz_evict_pages",
                  "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
                  "sz_attend_pages", "sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
                  "sz_encode_pack", "sz_encode_pack_ranked", "sz_encode_sample",
@@ -705,6 +710,63 @@ def sz_attend_latent(q, out, lse, cache, batch, max_len: int, scale: float, caus
         "sz_attend_latent")
 
 
+def sz_weigh_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
+    _fits(_U64, q_heads, max_len)
+    return int(_lib.sz_weigh_workspace_size(q_heads, _at(cache), _at(batch), max_len))
+
+
+def sz_weigh_pages(q, lse, before, weights, weights_pitch: int, keep: float, cache, batch,
+                   max_len: int, scale: float, softcap: float = 0.0, causal: bool = True,
+                   window: int = 0, workspace=None, workspace_bytes: int = 0, d_status=None,
+                   stream=None) -> None:
+    """q: Heads, or a tensor [tokens, heads, head_dim]; lse: a float32 tensor
+    [tokens, heads]; before (or None) and weights: float32 tensors [sequences,
+    KV heads, weights_pitch]; cache: a KVCache; batch: a Batch."""
+    q = _heads(q)
+    if not (0 <= max_len < _U64 and 0 <= window < _U64 and 0 <= workspace_bytes < _U64 and
+            0 <= weights_pitch < _U64):
+        _fits(_U64, max_len, window, workspace_bytes, weights_pitch)
+    stream = _call_stream(stream, cache, batch, q)
+    index, n = cache._index, batch.n_tokens
+    _tokens(n, q)
+    _dims(cache.head_dim, q)
+    _check_rows(cache, batch)
+    size = batch.n_seqs * cache.kv_heads * weights_pitch
+    _check(_lib.sz_weigh_pages(
+        q._at, _array(lse, "float32", n * q.heads, index, "lse"),
+        _array(before, "float32", size, index, "before"),
+        _array(weights, "float32", size, index, "weights"), weights_pitch, keep, cache._at,
+        batch._at, max_len, scale, softcap, int(causal), window,
+        _array(workspace, "uint8", workspace_bytes, index, "workspace"), workspace_bytes,
+        _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_weigh_pages")
+
+
+def sz_evict_pages(weights, weights_to, from_cache, to_cache, lens, lens_to, max_len: int,
+                   budget: int, first: int, recent: int, kept, d_status=None,
+                   stream=None) -> None:
+    """weights: a float32 tensor [sequences, weight heads, pitch]; weights_to
+    and kept: float32 and int32 tensors [sequences, weight heads, budget]; lens
+    and lens_to: int32 tensors [sequences]; from_cache, to_cache: KVCaches."""
+    if weights.dim() != 3:
+        raise ValueError("weights must have 3 dimensions")
+    n, heads, pitch = weights.shape
+    if not (0 <= max_len < _U64 and 0 <= budget < _U64 and 0 <= first < _U64 and
+            0 <= recent < _U64):
+        _fits(_U64, max_len, budget, first, recent)
+    stream = _call_stream(stream, from_cache, to_cache)
+    index = from_cache._index
+    if n > from_cache.rows or n > to_cache.rows:
+        raise ValueError(f"{n} sequences, {from_cache.rows} and {to_cache.rows} rows in the page "
+                         "tables")
+    _check(_lib.sz_evict_pages(
+        _array(weights, "float32", n * heads * pitch, index, "weights"), heads, pitch,
+        from_cache._at, _array(lens, "int32", n, index, "lens"), n, max_len, budget, first, recent,
+        to_cache._at, _array(weights_to, "float32", n * heads * budget, index, "weights_to"),
+        _array(kept, "int32", n * heads * budget, index, "kept"),
+        _array(lens_to, "int32", n, index, "lens_to"),
+        _array(d_status, "int32", n, index, "d_status"), stream), "sz_evict_pages")
+
+
 # ---- conveniences (torch allocates; the library computes) -----------------
 
 def encode(x, stream=None):
@@ -959,3 +1021,49 @@ def attend_latent(q, cache, batch, scale: float, max_len: int = 0, causal: bool 
     if check:
         _raise_on(status, "sz_attend_latent")
     return out, lse
+
+
+def weigh_pages(q, lse, cache, batch, weights=None, keep: float = 1.0, max_len: int = 0,
+                scale: float | None = None, softcap: float = 0.0, causal: bool = True,
+                window: int = 0, check: bool = True):
+    """The attention weights that cached tokens receive from queries [tokens,
+    heads, head_dim] whose log-sums attend_pages returned (sz_weigh_pages):
+    added in place to keep * ``weights`` [sequences, KV heads, tokens], or to a
+    new tensor, zero past the lengths.  Other arguments as in attend_pages."""
+    import torch
+    before = weights
+    if weights is None:
+        most = cache.pages_per_seq * cache.page_tokens
+        most = max_len if 0 < max_len < most else most
+        weights = torch.zeros((batch.n_seqs, cache.kv_heads, most), dtype=torch.float32,
+                              device=q.device)
+    elif weights.dim() != 3 or tuple(weights.shape[:2]) != (batch.n_seqs, cache.kv_heads):
+        raise ValueError("weights must be a tensor [sequences, KV heads, tokens]")
+    size = sz_weigh_workspace_size(q.shape[1], cache, batch, max_len)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=q.device) if check else None
+    sz_weigh_pages(q, lse, before, weights, weights.shape[2], keep, cache, batch, max_len,
+                   q.shape[2] ** -0.5 if scale is None else scale, softcap, causal, window, ws,
+                   size, status)
+    if check:
+        _raise_on(status, "sz_weigh_pages")
+    return weights
+
+
+def evict_pages(weights, from_cache, to_cache, lens, budget: int, first: int = 0,
+                recent: int = 0, max_len: int = 0, check: bool = True):
+    """Keep at most ``budget`` tokens of each sequence, in the pages of
+    to_cache (sz_evict_pages); returns the kept old positions (int32
+    [sequences, weight heads, budget], -1 past those that stay), their weights
+    (zero there) and the new lengths.  ``check`` as in kv_append."""
+    import torch
+    shape = (*weights.shape[:2], budget)
+    kept = torch.empty(shape, dtype=torch.int32, device=weights.device)
+    weights_to = torch.zeros(shape, dtype=torch.float32, device=weights.device)
+    lens_to = torch.empty_like(lens)
+    status = torch.zeros(lens.shape, dtype=torch.int32, device=lens.device) if check else None
+    sz_evict_pages(weights, weights_to, from_cache, to_cache, lens, lens_to, max_len, budget,
+                   first, recent, kept, status)
+    if check:
+        _raise_on(status, "sz_evict_pages")
+    return kept, weights_to, lens_to

@@ -105,6 +105,11 @@ bool overlap(const void* p, uint64_t bytes, Span s) {
     return bytes > 0 && at < s.end && s.begin < at + bytes;
 }
 
+Span span_of(const void* p, uint64_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return {at, at + bytes};
+}
+
 sz::Rows rows_of(const sz_heads* t) {
     if (t == nullptr) return sz::Rows{};
     return sz::Rows{t->data, t->token_stride, t->head_stride, (uint32_t)t->heads,
@@ -197,6 +202,20 @@ uint64_t most_len(const sz_kv_cache& c) {
 bool attend_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t q_heads, uint64_t kv_heads) {
     return n_tokens * q_heads <= kMaxTokens &&
            n_tokens * q_heads / 128 + 2 * n_seqs * kv_heads < uint64_t{1} << 24;
+}
+
+// (the kernels multiply by scale log2 e, or 2 scale log2 e / softcap)
+bool score_ok(float scale, float softcap, int causal, uint64_t window) {
+    return scale > 0 && scale < 1e38f && softcap >= 0 && softcap < 1e38f &&
+           !(softcap > 0 && !(scale / softcap < 0.99e38f)) && !(window != 0 && !causal);
+}
+
+bool weigh_sizes_ok(uint64_t q_heads, const sz_kv_cache* c, const sz_batch* b) {
+    return c != nullptr && b != nullptr && head_dim_ok(c->head_dim) && c->kv_heads > 0 &&
+           c->kv_heads <= kMaxHeads && q_heads > 0 && q_heads <= kMaxHeads &&
+           q_heads % c->kv_heads == 0 && b->n_seqs <= kMaxSeqs && b->n_tokens <= kMaxTokens &&
+           table_ok(c->pages_per_seq, c->table_pitch, c->page_tokens) &&
+           attend_fits(b->n_seqs, b->n_tokens, q_heads, c->kv_heads);
 }
 
 }  // namespace
@@ -351,10 +370,7 @@ sz_status sz_attend_pages(const sz_heads* q, const sz_heads* out, float* d_lse,
         !attend_fits(batch->n_seqs, n, q->heads, cache->kv_heads) ||
         !apart(*q, *out, n, dim, false))
         return SZ_ERR_INVALID_ARGUMENT;
-    // (the kernels multiply by scale log2 e, or 2 scale log2 e / softcap)
-    if (!(scale > 0 && scale < 1e38f) || !(softcap >= 0 && softcap < 1e38f) ||
-        (softcap > 0 && !(scale / softcap < 0.99e38f)) ||
-        (window != 0 && !causal) || !aligned(d_lse, 4) || !aligned(d_status, 4))
+    if (!score_ok(scale, softcap, causal, window) || !aligned(d_lse, 4) || !aligned(d_status, 4))
         return SZ_ERR_INVALID_ARGUMENT;
     const uint64_t most = most_len(*cache);
     if (max_len == 0 || max_len > most) max_len = most;
@@ -465,6 +481,116 @@ sz_status sz_attend_latent(const sz_heads* q, const sz_heads* out, float* d_lse,
     if (st == SZ_OK && d_status != nullptr)
         st = hip_status(sz::launch_check_seqs(
             sz::SeqCheck{a.cache, a.batch, a.max_len, 0, a.causal, 0, d_status}, stream));
+    return st;
+}
+
+uint64_t sz_weigh_workspace_size(uint64_t q_heads, const sz_kv_cache* cache,
+                                 const sz_batch* batch, uint64_t max_len) {
+    if (!weigh_sizes_ok(q_heads, cache, batch) || batch->n_seqs == 0 || batch->n_tokens == 0)
+        return 0;
+    const uint64_t most = most_len(*cache);
+    return sz::weigh_workspace((uint32_t)q_heads, cache_of(*cache), batch->n_seqs,
+                               batch->n_tokens, max_len == 0 || max_len > most ? most : max_len);
+}
+
+sz_status sz_weigh_pages(const sz_heads* q, const float* d_lse, const float* d_before,
+                         float* d_weights, uint64_t weights_pitch, float keep,
+                         const sz_kv_cache* cache, const sz_batch* batch, uint64_t max_len,
+                         float scale, float softcap, int causal, uint64_t window,
+                         void* d_workspace, uint64_t workspace_bytes, int32_t* d_status,
+                         hipStream_t stream) {
+    if (!cache_ok(cache) || !batch_ok(batch)) return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t n = batch->n_tokens;
+    const uint32_t dim = cache->head_dim;
+    if (!heads_ok(q, n, dim, false) || q->type != SZ_TYPE_BF16 ||
+        !weigh_sizes_ok(q->heads, cache, batch))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (!score_ok(scale, softcap, causal, window) || !std::isfinite(keep) || !aligned(d_lse, 4) ||
+        !aligned(d_before, 4) || !aligned(d_weights, 4) || !aligned(d_status, 4))
+        return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t most = most_len(*cache);
+    if (max_len == 0 || max_len > most) max_len = most;
+    if (window > kMaxLen) window = 0;
+    if (weights_pitch < max_len || weights_pitch > kMaxTokens) return SZ_ERR_INVALID_ARGUMENT;
+    if (keep == 0) d_before = nullptr;
+    const uint64_t bytes = 4 * batch->n_seqs * cache->kv_heads * weights_pitch;
+    const uint64_t need = sz_weigh_workspace_size(q->heads, cache, batch, max_len);
+    if (batch->n_seqs > 0 && n > 0) {
+        if (d_lse == nullptr || d_weights == nullptr) return SZ_ERR_INVALID_ARGUMENT;
+        if (overlap(d_weights, bytes, span(*q, n, dim)) ||
+            overlap(d_weights, bytes, span_of(d_lse, 4 * n * q->heads)) ||
+            (d_before != d_weights && overlap(d_weights, bytes, span_of(d_before, bytes))))
+            return SZ_ERR_INVALID_ARGUMENT;
+        if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 256) ||
+                         workspace_bytes < need || overlap(d_workspace, need, span(*q, n, dim)) ||
+                         overlap(d_workspace, need, span_of(d_lse, 4 * n * q->heads)) ||
+                         overlap(d_workspace, need, span_of(d_before, bytes)) ||
+                         overlap(d_workspace, need, span_of(d_weights, bytes))))
+            return SZ_ERR_INVALID_ARGUMENT;
+        // (a launch holds fewer than 2^32 threads, 256 a workgroup)
+        if (sz::weigh_groups((uint32_t)q->heads, cache_of(*cache), batch->n_seqs, n, max_len) >=
+            uint64_t{1} << 24)
+            return SZ_ERR_INVALID_ARGUMENT;
+    }
+    if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
+    if (sz_status s = check_stream(stream)) return s;
+    sz::Cache c = cache_of(*cache);
+    c.v_pages = c.k_pages;
+    const sz::Weigh a{rows_of(q), d_lse, d_before, d_weights, weights_pitch, keep, c,
+                      batch_of(*batch), (int64_t)max_len, scale, softcap, causal != 0, window};
+    sz_status st = SZ_OK;
+    if (n > 0) st = hip_status(sz::launch_weigh(a, static_cast<float*>(d_workspace), stream));
+    if (st == SZ_OK && d_status != nullptr)
+        st = hip_status(sz::launch_check_seqs(
+            sz::SeqCheck{c, a.batch, a.max_len, 0, a.causal, window, d_status}, stream));
+    return st;
+}
+
+sz_status sz_evict_pages(const float* d_weights, uint64_t weight_heads, uint64_t weights_pitch,
+                         const sz_kv_cache* from, const int32_t* d_lens, uint64_t n_seqs,
+                         uint64_t max_len, uint64_t budget, uint64_t first, uint64_t recent,
+                         const sz_kv_cache* to, float* d_weights_to, int32_t* d_kept,
+                         int32_t* d_lens_to, int32_t* d_status, hipStream_t stream) {
+    if (!cache_ok(from) || !cache_ok(to) || from->kv_heads != to->kv_heads ||
+        from->head_dim != to->head_dim || n_seqs > kMaxSeqs)
+        return SZ_ERR_INVALID_ARGUMENT;
+    if ((weight_heads != 1 && weight_heads != from->kv_heads) || budget == 0 || budget > kMaxLen ||
+        first > budget || recent > budget - first || weights_pitch > kMaxTokens)
+        return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t most = most_len(*from);
+    if (max_len == 0 || max_len > most) max_len = most;
+    const uint64_t room = budget < max_len ? budget : max_len;
+    if (weights_pitch < max_len || most_len(*to) < room ||
+        n_seqs * weight_heads >= uint64_t{1} << 22 ||
+        (room + 15) / 16 * n_seqs >= uint64_t{1} << 24)
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (!aligned(d_weights, 4) || !aligned(d_weights_to, 4) || !aligned(d_kept, 4) ||
+        !aligned(d_lens, 4) || !aligned(d_lens_to, 4) || !aligned(d_status, 4))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (n_seqs == 0) return SZ_OK;
+    if (d_weights == nullptr || d_weights_to == nullptr || d_kept == nullptr ||
+        d_lens == nullptr || d_lens_to == nullptr)
+        return SZ_ERR_INVALID_ARGUMENT;
+    // what is read and what is written, apart
+    const uint64_t lines = 4 * n_seqs * weight_heads, lens = 4 * n_seqs;
+    const Span read[2] = {span_of(d_weights, lines * weights_pitch), span_of(d_lens, lens)};
+    const Span written[4] = {span_of(d_weights_to, lines * budget), span_of(d_kept, lines * budget),
+                             span_of(d_lens_to, lens),
+                             span_of(d_status, d_status == nullptr ? 0 : lens)};
+    for (int i = 0; i < 4; i++) {
+        for (const Span& r : read)
+            if (written[i].begin < r.end && r.begin < written[i].end) return SZ_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; j++)
+            if (written[i].begin < written[j].end && written[j].begin < written[i].end)
+                return SZ_ERR_INVALID_ARGUMENT;
+    }
+    if (sz_status s = check_stream(stream)) return s;
+    const sz::Evict a{d_weights, weights_pitch, (uint32_t)weight_heads, (uint32_t)budget,
+                      (uint32_t)first, (uint32_t)recent, cache_of(*from), cache_of(*to), d_lens,
+                      (int64_t)max_len, d_weights_to, d_kept, d_lens_to};
+    sz_status st = hip_status(sz::launch_evict(a, (uint32_t)n_seqs, stream));
+    if (st == SZ_OK && d_status != nullptr)
+        st = hip_status(sz::launch_evict_check(a, (uint32_t)n_seqs, d_status, stream));
     return st;
 }
 

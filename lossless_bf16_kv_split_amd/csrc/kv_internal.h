@@ -133,6 +133,43 @@ uint64_t attend_latent_workspace(uint32_t heads, const Cache& cache, uint32_t la
                                  uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len);
 hipError_t launch_attend_latent(const Attend& a, uint8_t* ws, hipStream_t stream);
 
+struct Weigh {
+    Rows q;
+    const float* lse;
+    const float* before;  // NULL: none (or keep is 0)
+    float* weights;
+    uint64_t pitch;
+    float keep;
+    Cache cache;
+    Batch batch;
+    int64_t max_len;
+    float scale, softcap;
+    uint32_t causal;
+    uint64_t window;
+};
+// Workgroups of the largest of its launches; bytes of workspace.
+uint64_t weigh_groups(uint32_t q_heads, const Cache& cache, uint64_t n_seqs, uint64_t n_tokens,
+                      uint64_t max_len);
+uint64_t weigh_workspace(uint32_t q_heads, const Cache& cache, uint64_t n_seqs, uint64_t n_tokens,
+                         uint64_t max_len);
+hipError_t launch_weigh(const Weigh& a, float* ws, hipStream_t stream);
+
+struct Evict {
+    const float* weights;  // [sequence][weight_heads][pitch]
+    uint64_t pitch;
+    uint32_t weight_heads;
+    uint32_t budget, first, recent;
+    Cache from, to;
+    const int32_t* lens;
+    int64_t max_len;
+    float* weights_to;     // [sequence][weight_heads][budget]
+    int32_t* kept;         // the same
+    int32_t* lens_to;
+};
+hipError_t launch_evict(const Evict& a, uint32_t n_seqs, hipStream_t stream);
+hipError_t launch_evict_check(const Evict& a, uint32_t n_seqs, int32_t* status,
+                              hipStream_t stream);
+
 // Every sequence's status: one wave per sequence checks its range, its
 // length and the pages that the call touches (append: those of the new
 // tokens; attention: those of the visible ones).
