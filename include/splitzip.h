@@ -655,6 +655,36 @@ sz_status sz_attend_latent(const sz_heads *q, const sz_heads *out, float *d_lse,
                            float scale, int causal, void *d_workspace, uint64_t workspace_bytes,
                            int32_t *d_status, hipStream_t stream);
 
+/* Attention of every new token over keys and values that have been expanded
+ * from latents, every head with its own: sequence s has the rows
+ * d_key_starts[s] .. + d_lens[s] - 1 of k, v and k_rotary.  Scores are scale *
+ * (first key_dim elements of the query head . k + the following rotary_dim
+ * ones . k_rotary); the rest as in sz_attend_latent.
+ *   q         BF16, heads of key_dim + rotary_dim elements
+ *   out       BF16 or F32, as many heads of value_dim elements
+ *   k, v      BF16, as many heads of key_dim and value_dim elements, n_keys
+ *             rows, token strides below 2^26; may be slices of one tensor
+ *   k_rotary  BF16, one head (shared by all) or as many, of rotary_dim
+ *             elements, n_keys rows; NULL where rotary_dim is 0
+ *   key_dim, value_dim   multiples of 8, 8 .. 128
+ *   rotary_dim           a multiple of 8, 0 .. 64
+ *   d_key_starts  device i32[n_seqs]; any order, rows may be shared
+ *   n_keys    < 2^31
+ *   max_len   a host-side bound of d_lens (longer sequences are refused); 0, or
+ *             anything past it, means n_keys
+ *   n_tokens * heads < 2^31, n_tokens * heads / 128 + 2 * n_seqs * heads < 2^24
+ *   d_status  SZ_ERR_INVALID_ARGUMENT also for a sequence whose rows do not
+ *             lie in 0 .. n_keys */
+uint64_t sz_attend_expanded_workspace_size(uint64_t heads, uint32_t value_dim,
+                                           const sz_batch *batch, uint64_t max_len);
+sz_status sz_attend_expanded(const sz_heads *q, const sz_heads *out, float *d_lse,
+                             const sz_heads *k, const sz_heads *k_rotary, const sz_heads *v,
+                             uint32_t key_dim, uint32_t rotary_dim, uint32_t value_dim,
+                             const int32_t *d_key_starts, uint64_t n_keys,
+                             const sz_batch *batch, uint64_t max_len, float scale, int causal,
+                             void *d_workspace, uint64_t workspace_bytes, int32_t *d_status,
+                             hipStream_t stream);
+
 /* ---- eviction from a paged cache ---------------------------------------
  * A cache over its budget gives up the tokens that attention has looked at
  * the least: sz_weigh_pages adds up what each cached token has received,

@@ -35,6 +35,7 @@ __all__ = [
     "rope_phases", "rope", "paged_cache", "qk_norm_rope", "kv_append", "attend_pages",
     "sz_latent_append", "sz_attend_latent_workspace_size", "sz_attend_latent", "LatentCache",
     "latent_cache", "latent_append", "attend_latent",
+    "sz_attend_expanded_workspace_size", "sz_attend_expanded", "attend_expanded",
     "sz_weigh_workspace_size", "sz_weigh_pages", "sz_evict_pages", "weigh_pages", "evict_pages",
     "sz_status_string", "encode",
     "decode", "encode_blocks", "decode_blocks", "BlockContainers",
@@ -131,11 +132,17 @@ def _load() -> ctypes.CDLL:
     L.sz_attend_latent_workspace_size.argtypes = [u64, p, p, u64]
     L.sz_attend_latent_workspace_size.restype = u64
     L.sz_attend_latent.argtypes = [p, p, p, p, p, u64, f32, i32, p, u64, p, p]
+    L.sz_attend_expanded_workspace_size.argtypes = [u64, ctypes.c_uint32, p, u64]
+    L.sz_attend_expanded_workspace_size.restype = u64
+    u32 = ctypes.c_uint32
+    L.sz_attend_expanded.argtypes = [p, p, p, p, p, p, u32, u32, u32, p, u64, p, u64, f32, i32, p,
+                                     u64, p, p]
     L.sz_weigh_workspace_size.argtypes = [u64, p, p, u64]
     L.sz_weigh_workspace_size.restype = u64
     L.sz_weigh_pages.argtypes = [p, p, p, p, u64, f32, p, p, u64, f32, f32, i32, u64, p, u64, p, p]
     L.sz_evict_pages.argtypes = [p, u64, u64, p, p, u64, u64, u64, u64, u64, p, p, p, p, p, p]
-    for name in ("sz_latent_append", "sz_attend_latent", "sz_weigh_pages", "sz_evict_pages",
+    for name in ("sz_latent_append", "sz_attend_latent", "sz_attend_expanded",
+                 "sz_weigh_pages", "sz_evict_pages",
                  "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
                  "sz_attend_pages", "sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
                  "sz_encode_pack", "sz_encode_pack_ranked", "sz_encode_sample",
@@ -710,6 +717,36 @@ def sz_attend_latent(q, out, lse, cache, batch, max_len: int, scale: float, caus
         "sz_attend_latent")
 
 
+def sz_attend_expanded_workspace_size(heads: int, value_dim: int, batch, max_len: int = 0) -> int:
+    _fits(_U64, heads, max_len)
+    _fits(_U32, value_dim)
+    return int(_lib.sz_attend_expanded_workspace_size(heads, value_dim, _at(batch), max_len))
+
+
+def sz_attend_expanded(q, out, lse, k, k_rotary, v, key_starts, batch, max_len: int, scale: float,
+                       causal: bool = True, workspace=None, workspace_bytes: int = 0,
+                       d_status=None, stream=None) -> None:
+    """q, out, k, k_rotary (or None), v: Heads, or tensors [rows, heads,
+    elements]; key_starts: an int32 tensor [sequences]; lse: a float32 tensor
+    [tokens, heads] or None; batch: a Batch."""
+    q, out, k, k_rotary, v = (_heads(x) for x in (q, out, k, k_rotary, v))
+    if not (0 <= max_len < _U64 and 0 <= workspace_bytes < _U64):
+        _fits(_U64, max_len, workspace_bytes)
+    stream = _call_stream(stream, batch, q, out, k, k_rotary, v)
+    index, n = batch._index, batch.n_tokens
+    _tokens(n, q, out)
+    _tokens(k.tokens, v, k_rotary)
+    rotary = 0 if k_rotary is None else k_rotary.dim
+    _dims(k.dim + rotary, q)
+    _dims(v.dim, out)
+    _check(_lib.sz_attend_expanded(
+        q._at, out._at, _array(lse, "float32", n * q.heads, index, "lse"), k._at, _at(k_rotary),
+        v._at, k.dim, rotary, v.dim, _array(key_starts, "int32", batch.n_seqs, index, "key_starts"),
+        k.tokens, batch._at, max_len, scale, int(causal),
+        _array(workspace, "uint8", workspace_bytes, index, "workspace"), workspace_bytes,
+        _array(d_status, "int32", batch.n_seqs, index, "d_status"), stream), "sz_attend_expanded")
+
+
 def sz_weigh_workspace_size(q_heads: int, cache, batch, max_len: int = 0) -> int:
     _fits(_U64, q_heads, max_len)
     return int(_lib.sz_weigh_workspace_size(q_heads, _at(cache), _at(batch), max_len))
@@ -1020,6 +1057,28 @@ def attend_latent(q, cache, batch, scale: float, max_len: int = 0, causal: bool 
     sz_attend_latent(q, out, lse, cache, batch, max_len, scale, causal, ws, size, status)
     if check:
         _raise_on(status, "sz_attend_latent")
+    return out, lse
+
+
+def attend_expanded(q, k, v, key_starts, batch, scale: float, k_rotary=None, max_len: int = 0,
+                    causal: bool = True, out_dtype=None, check: bool = True):
+    """Attention of queries [tokens, heads, key_dim + rotary_dim] over keys and
+    values [keys, heads, ..] expanded from latents, their rotary part [keys, 1
+    or heads, rotary_dim] beside them (sz_attend_expanded); returns the output
+    [tokens, heads, value_dim] (bfloat16 unless ``out_dtype`` is float32) and
+    the log-sums, zero for rows of no sequence; ``check`` as in kv_append."""
+    import torch
+    out = torch.zeros((*q.shape[:2], v.shape[2]), dtype=out_dtype or torch.bfloat16,
+                      device=q.device)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+    most = max_len if 0 < max_len < k.shape[0] else k.shape[0]
+    size = sz_attend_expanded_workspace_size(q.shape[1], v.shape[2], batch, most) if most else 0
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    status = torch.zeros(batch.n_seqs, dtype=torch.int32, device=q.device) if check else None
+    sz_attend_expanded(q, out, lse, k, k_rotary, v, key_starts, batch, max_len, scale, causal, ws,
+                       size, status)
+    if check:
+        _raise_on(status, "sz_attend_expanded")
     return out, lse
 
 

@@ -429,7 +429,10 @@ __global__ __launch_bounds__(kWave) void k_check_seqs(SeqCheck c, uint32_t each)
                        first_new >= 0) {
                 from = first_new + 1 - (int64_t)c.window;
             }
-            if (good && q.begin < q.end && from < q.len) {
+            if (c.key_starts != nullptr) {
+                const int64_t start = c.key_starts[s];
+                good = start >= 0 && start + q.len <= c.n_keys;
+            } else if (good && q.begin < q.end && from < q.len) {
                 const uint64_t row = (uint64_t)s * c.cache.table_pitch;
                 const uint64_t last = (uint64_t)(q.len - 1) >> c.cache.page_log2;
                 for (uint64_t p = ((uint64_t)from >> c.cache.page_log2) + lane; p <= last;

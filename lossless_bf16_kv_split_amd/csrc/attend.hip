@@ -468,27 +468,108 @@ __device__ __forceinline__ constexpr uint32_t v_mix(uint32_t j) {
     return DP == 64 ? (j >> 1 & 1) << 2 : (j & 3) << 2;
 }
 
-// Bytes of LDS: K of two steps of 64 keys, V of three
-template <int DP>
-constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP;
-static_assert(2 * kChunkLds<128> <= 160 * 1024, "two workgroups a CU");
-static_assert(kChunkLds<256> <= 160 * 1024, "");
+// Where a step's keys and values come from.  Paged: from the cache's pages,
+// looked up a step ahead.
+struct Paged {
+    static constexpr bool kRotary = false;
+    const Attend& a;
+    uint64_t table_row, k_page, v_page;
+    uint32_t kv;
+    int32_t last;
 
-template <int DP, int QB, int CAP, bool SHARED>
+    __device__ __forceinline__ Paged(const Attend& attend, const Part& part, uint32_t head)
+        : a(attend), table_row((uint64_t)part.t.seq * attend.cache.table_pitch), kv(head),
+          last(part.last) {}
+    __device__ __forceinline__ uint32_t k_step() const { return 2 * (uint32_t)a.cache.token_stride; }
+    __device__ __forceinline__ uint32_t v_step() const { return 2 * (uint32_t)a.cache.token_stride; }
+    __device__ __forceinline__ uint32_t k_dim() const { return a.cache.head_dim; }
+    // the block of 16 keys at jb (a load that nothing waits for: the step's
+    // own wait covers it)
+    __device__ __forceinline__ void look_up(int32_t jb, int32_t lo) {
+        const bool seen = jb < last && jb + 16 > lo;
+        const uint64_t entry = table_row + ((uint32_t)jb >> a.cache.page_log2);
+        k_page = seen ? a.cache.k_pages[entry] : 0;
+        v_page = seen ? a.cache.v_pages[entry] : 0;
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(uint64_t page, int32_t jb) const {
+        const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
+        const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(page >> 32))
+                                << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)page);
+        return block_rows(a.cache, at, slot, kv, last - jb);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(int32_t jb) const {
+        return rows(k_page, jb);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(int32_t jb) const {
+        return rows(v_page, jb);
+    }
+};
+
+// Ragged: from tensors of rows, sequence after sequence, every head with keys
+// and values of its own and a rotary part of the key beside them.
+struct Ragged {
+    static constexpr bool kRotary = true;
+    const Expanded& e;
+    int64_t start;
+    uint32_t head;
+    int32_t last;
+
+    __device__ __forceinline__ Ragged(const Expanded& expanded, int64_t key_start, uint32_t h,
+                                      int32_t past)
+        : e(expanded), start(key_start), head(h), last(past) {}
+    __device__ __forceinline__ uint32_t k_step() const { return 2 * (uint32_t)e.k.token_stride; }
+    __device__ __forceinline__ uint32_t v_step() const { return 2 * (uint32_t)e.v.token_stride; }
+    __device__ __forceinline__ uint32_t r_step() const { return 2 * (uint32_t)e.r.token_stride; }
+    __device__ __forceinline__ uint32_t k_dim() const { return e.key_dim; }
+    __device__ __forceinline__ void look_up(int32_t, int32_t) {}
+    // (row numbers come from the device: uniform, but not to the compiler)
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const Rows& r, uint32_t h, uint32_t dim,
+                                                           int32_t jb) const {
+        const bool some = jb < last;
+        const uint64_t at = reinterpret_cast<uint64_t>(r.data) +
+                            2 * ((uint64_t)(start + jb) * r.token_stride + h * r.head_stride);
+        const uint64_t to = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32))
+                                << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        const uint32_t n = last - jb > 16 ? 15 : (uint32_t)(last - jb) - 1;
+        const uint32_t bytes = some ? 2 * (n * (uint32_t)r.token_stride + dim) : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(some ? to : 0), 0, bytes,
+                                                 kBufferFlags);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(int32_t jb) const {
+        return rows(e.k, head, e.key_dim, jb);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(int32_t jb) const {
+        return rows(e.v, head, e.value_dim, jb);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rotary(int32_t jb) const {
+        return rows(e.r, e.r.heads == 1 ? 0 : head, e.rotary_dim, jb);
+    }
+};
+
+// Bytes of LDS: K of two steps of 64 keys, V of three; and of two steps 64
+// elements of the keys' rotary part, in rows of their own.
+template <int DP, bool ROTARY>
+constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP + (ROTARY ? 2 * 64 * 128 : 0);
+static_assert(2 * kChunkLds<128, false> <= 160 * 1024, "two workgroups a CU");
+static_assert(kChunkLds<256, false> <= 160 * 1024, "");
+
+template <int DP, int QB, int CAP, bool SHARED, class Source>
 __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                                            const Score& score, uint8_t* ws, const Part& part,
-                                           uint32_t kv, uint8_t* lds) {
+                                           uint32_t kv, uint8_t* lds, Source source) {
+    constexpr bool kRotary = Source::kRotary;
     constexpr int kKeys = 64;
     constexpr uint32_t kRow = 2 * DP;             // bytes of a row in LDS
     constexpr uint32_t kBuffer = kKeys * kRow;    // K or V of a step
     constexpr int kLoads = DP / 32;               // per wave, of K or V
-    constexpr int kSlices = DP / 16, kParts = DP / 32;
+    constexpr int kMain = DP / 16, kParts = DP / 32;
+    constexpr int kSlices = kMain + (kRotary ? 4 : 0);  // those of the rotary part last
     const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Tile& t = part.t;
-    const int32_t first = part.first, last = part.last;
+    const int32_t first = part.first, last = source.last;
 
-    const uint32_t dim = a.cache.head_dim;
+    const uint32_t dim = source.k_dim(), v_dim = a.value_dim;
     bf16x8 q[QB][kSlices];
     int32_t low[QB], high[QB];
 #pragma unroll
@@ -502,8 +583,14 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
 #pragma unroll
         for (int s = 0; s < kSlices; s++) {
             u32x4 v = {0, 0, 0, 0};
-            if (w.on && 16 * s + 8 * h < dim)
-                v = *(const SZ_GLOBAL u32x4*)(row + 16 * s + 8 * h);
+            uint32_t e = 16 * s + 8 * h, past = dim;
+            if constexpr (kRotary) {
+                if (s >= kMain) {
+                    e = dim + 16 * (s - kMain) + 8 * h;
+                    past = dim + source.e.rotary_dim;
+                }
+            }
+            if (w.on && e < past) v = *(const SZ_GLOBAL u32x4*)(row + e);
             q[b][s] = __builtin_bit_cast(bf16x8, v);
         }
     }
@@ -519,43 +606,35 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
 
     // this wave's part of a step: 16 keys, kLoads KB of K and of V
     constexpr uint32_t kPast = 0x80000000u;
-    const uint32_t step = 2 * (uint32_t)a.cache.token_stride;
-    uint32_t k_off[kLoads], v_off[kLoads];
+    uint32_t k_off[kLoads], v_off[kLoads], r_off[2];
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
         const uint32_t at = 1024 * i + 16 * lane, row = at / kRow, piece = at % kRow / 16;
         const uint32_t kp = piece ^ k_mix<DP>(row), vp = piece ^ v_mix<DP>(row);
-        k_off[i] = 8 * kp < dim ? row * step + 16 * kp : kPast;
-        v_off[i] = 8 * vp < dim ? row * step + 16 * vp : kPast;
+        k_off[i] = 8 * kp < dim ? row * source.k_step() + 16 * kp : kPast;
+        v_off[i] = 8 * vp < v_dim ? row * source.v_step() + 16 * vp : kPast;
+    }
+    if constexpr (kRotary) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t at = 1024 * i + 16 * lane, row = at / 128;
+            const uint32_t piece = at % 128 / 16 ^ k_mix<64>(row);
+            r_off[i] = 8 * piece < source.e.rotary_dim ? row * source.r_step() + 16 * piece : kPast;
+        }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SZ_LDS uint8_t*)lds;
-    const uint64_t table_row = (uint64_t)t.seq * a.cache.table_pitch;
-    // The page of this wave's block of the step at j: its address, looked up
-    // a step before it is used (a load that nothing waits for: the step's
-    // own wait covers it).
-    const auto page_at = [&](const uint64_t* pages, int32_t j) {
-        const int32_t jb = j + 16 * (int32_t)wave;
-        return jb < last && jb + 16 > t.lo
-                   ? pages[table_row + ((uint32_t)jb >> a.cache.page_log2)]
-                   : 0;
-    };
-    // K or V of the step at j to a buffer (V's are 2, 3 and 4)
-    const auto fetch = [&](uint64_t page, const uint32_t (&off)[kLoads], int32_t j,
-                           uint32_t buffer) {
-        const int32_t jb = j + 16 * (int32_t)wave;
-        const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
-        const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(page >> 32))
-                                << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)page);
-        const auto rows = block_rows(a.cache, at, slot, kv, last - jb);
-        const uint32_t to = lds0 + buffer * kBuffer + wave * 16 * kRow;
-        load_to_lds<kLoads>(rows, off, to);
-    };
-    uint64_t next_k = page_at(a.cache.k_pages, first), next_v = page_at(a.cache.v_pages, first);
+    constexpr uint32_t kRotaryAt = 5 * kBuffer;  // of LDS
+    source.look_up(first + 16 * (int32_t)wave, t.lo);
+    // K and V of the step at j to their buffers, the next step's block looked up
     const auto fetch_step = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer) {
-        fetch(next_k, k_off, j, k_buffer);
-        fetch(next_v, v_off, j, 2 + v_buffer);
-        next_k = page_at(a.cache.k_pages, j + kKeys);
-        next_v = page_at(a.cache.v_pages, j + kKeys);
+        const int32_t jb = j + 16 * (int32_t)wave;
+        load_to_lds<kLoads>(source.keys(jb), k_off, lds0 + k_buffer * kBuffer + wave * 16 * kRow);
+        load_to_lds<kLoads>(source.values(jb), v_off,
+                            lds0 + (2 + v_buffer) * kBuffer + wave * 16 * kRow);
+        if constexpr (kRotary)
+            load_to_lds<2>(source.rotary(jb), r_off,
+                           lds0 + kRotaryAt + k_buffer * 8192 + wave * 2048);
+        source.look_up(jb + kKeys, t.lo);
     };
 
     // LDS addresses of this lane's reads.  Slice s of K is at its first
@@ -568,7 +647,14 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                             ((2 * (lane / 16 % 2) + lane % 4 / 2) ^ v_mix<DP>(v_key)) * 16 +
                             lane % 2 * 8;
     // K of 32 keys (block of a buffer) at `at`, V of 16 keys
+    const uint32_t r_lane = lds0 + kRotaryAt + n * 128 + (h ^ k_mix<64>(n)) * 16;
     const auto keys_at = [&](uint32_t at, int s) {
+        if constexpr (kRotary) {  // (rows of 128 bytes, half of those of 128 elements)
+            static_assert(!kRotary || kRow == 256, "");
+            if (s >= kMain)
+                return *(const SZ_LDS bf16x8*)(uintptr_t)((r_lane + (at - k_lane) / 2) ^
+                                                          32 * (s - kMain));
+        }
         return *(const SZ_LDS bf16x8*)(uintptr_t)(at ^ 32 * s);
     };
     const auto value_words = [&](uint32_t at, int t16, int d) {
@@ -722,8 +808,8 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         f32x16 s[QB];
         float top[QB];
     };
-    constexpr int kGroups = 2 * kParts;  // of either product: DP / 16 slices; 2 x DP / 32 parts
-    static_assert(kGroups == kSlices, "");
+    // groups: a slice of the first product, a part of 16 keys of the second
+    constexpr int kGroups = kSlices, kGroups2 = 2 * kParts;
     constexpr int kUnits = 8 * QB;       // pairs of weights in a lane
     constexpr int kAhead = 3;            // groups that operands are read ahead
     const auto zero = [&](Half& x) {
@@ -756,7 +842,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         const auto read = [&](int g) {  // group g's operand
             if (g < kGroups) {
                 if constexpr (kProduct) kf[g % (kAhead + 1)] = keys_at(ka, g);
-            } else if (g < 2 * kGroups) {
+            } else if (g < kGroups + kGroups2) {
                 vf[g % (kAhead + 1)] =
                     value_words(va, (g - kGroups) / kParts, (g - kGroups) % kParts);
             }
@@ -783,7 +869,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
             for (int b = 0; b < QB; b++) next.top[b] = -INFINITY;
         }
 #pragma unroll
-        for (int g = 0; g < kGroups; g++) {
+        for (int g = 0; g < kGroups2; g++) {
             read(kGroups + g + kAhead);
             const int t16 = g / kParts, d = g % kParts;
 #pragma unroll
@@ -906,7 +992,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                     const uint32_t e = 32 * d + 8 * g + 4 * h;
                     const float x[4] = {o[b][d][4 * g] * inv, o[b][d][4 * g + 1] * inv,
                                         o[b][d][4 * g + 2] * inv, o[b][d][4 * g + 3] * inv};
-                    if (e < dim) store_out<4>(a.out, at + e, x);
+                    if (e < v_dim) store_out<4>(a.out, at + e, x);
                 }
             if (h == 0 && a.lse != nullptr)
                 a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(m[b], total);
@@ -917,8 +1003,8 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
                     const uint32_t e = 32 * d + 8 * g + 4 * h;
-                    if (e < dim)
-                        store_global(reinterpret_cast<uint4*>(u.o + (uint64_t)r * dim + e),
+                    if (e < v_dim)
+                        store_global(reinterpret_cast<uint4*>(u.o + (uint64_t)r * v_dim + e),
                                      make_uint4(__float_as_uint(o[b][d][4 * g]),
                                                 __float_as_uint(o[b][d][4 * g + 1]),
                                                 __float_as_uint(o[b][d][4 * g + 2]),
@@ -936,13 +1022,34 @@ template <int DP, int QB, int CAP, bool SHARED>
 __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<DP>];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<DP, false>];
     Walk<SHARED> walk(a, p);
     Part part;
     // whole tiles: the last ones of a prompt see the most keys and go first
     if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
     do {
-        chunk_part<DP, QB, CAP, SHARED>(a, p, score, ws, part, kv, lds);
+        chunk_part<DP, QB, CAP, SHARED>(a, p, score, ws, part, kv, lds, Paged(a, part, kv));
+    } while (walk.next(a, p, index, part));
+}
+
+// The same over keys and values expanded from latents: 192 elements of keys,
+// 128 of values.  One workgroup a CU.
+template <int QB, bool SHARED>
+__global__ __launch_bounds__(kThreads, 1) void k_attend_expanded(Attend a, Expanded e,
+                                                                 AttendPlan p, Score score,
+                                                                 uint8_t* ws) {
+    const uint32_t head = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<128, true>];
+    Walk<SHARED> walk(a, p);
+    Part part;
+    if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
+    do {
+        // (a sequence whose keys lie outside the tensors: none are read)
+        const int64_t start = __builtin_amdgcn_readfirstlane(e.key_starts[part.t.seq]);
+        const int32_t len = __builtin_amdgcn_readfirstlane(a.batch.lens[part.t.seq]);
+        const bool good = start >= 0 && start + len <= e.n_keys;
+        chunk_part<128, QB, kUncapped, SHARED>(a, p, score, ws, part, head, lds,
+                                               Ragged(e, start, head, good ? part.last : part.first));
     } while (walk.next(a, p, index, part));
 }
 
@@ -975,7 +1082,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     const uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
     if (from == upto) return;
-    const uint32_t dim = a.cache.head_dim;
+    const uint32_t dim = a.value_dim;
     const uint32_t e = 4 * (lane % LANES);
     const uint64_t stride = (uint64_t)dim << p.tile_log2;
     const int32_t rows = 1 << p.tile_log2;
@@ -1077,6 +1184,53 @@ uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uin
     if (p.shares == 0) return 0;
     const uint64_t rows = c.kv_heads * partial_slots(p) << p.tile_log2;
     return (rows * (c.head_dim + 2) * 4 + 255) / 256 * 256;
+}
+
+// Keys and values expanded from latents: a head is a KV head of its own.
+// Tiles of 256 rows where sequences have that many on average, of 128
+// otherwise; whole where they fill the chip, one workgroup a CU.
+AttendPlan plan_expanded(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len) {
+    AttendPlan p{};
+    p.group = 1;
+    p.tile_log2 = n_tokens >= 192 * n_seqs && (n_tokens >> 8) * heads >= kCus ? 8 : 7;
+    p.tiles = (uint32_t)((n_tokens >> p.tile_log2) + n_seqs);
+    const uint64_t full = n_tokens >> p.tile_log2;
+    const uint64_t groups = (full > n_seqs ? full : n_seqs) * heads;
+    const bool whole = n_seqs > kShareSeqs || heads > kCus || groups >= kCus ||
+                       p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= 512;
+    p.shares = whole ? 0 : (uint32_t)(kCus / heads);
+    return p;
+}
+
+uint64_t attend_expanded_workspace(uint32_t heads, uint32_t value_dim, uint64_t n_seqs,
+                                   uint64_t n_tokens, uint64_t max_len) {
+    const AttendPlan p = plan_expanded(heads, n_seqs, n_tokens, max_len);
+    if (p.shares == 0) return 0;
+    const uint64_t rows = heads * partial_slots(p) << p.tile_log2;
+    return (rows * (value_dim + 2) * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_attend_expanded(const Attend& a, const Expanded& e, uint8_t* ws,
+                                  hipStream_t stream) {
+    if (a.batch.n_seqs == 0 || a.batch.n_tokens == 0) return hipSuccess;
+    const AttendPlan p =
+        plan_expanded(a.q.heads, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
+    const Score score = score_of(a);
+    const dim3 grid((p.shares != 0 ? p.shares : p.tiles) * a.cache.kv_heads), block(kThreads);
+    if (p.tile_log2 == 8 && p.shares != 0)
+        k_attend_expanded<2, true><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    else if (p.tile_log2 == 8)
+        k_attend_expanded<2, false><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    else if (p.shares != 0)
+        k_attend_expanded<1, true><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    else
+        k_attend_expanded<1, false><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess || p.shares == 0) return st;
+    const dim3 join(p.tiles * a.cache.kv_heads * join_pieces(p));
+    if (a.value_dim <= 64) k_attend_join<16><<<join, block, 0, stream>>>(a, p, ws);
+    else k_attend_join<32><<<join, block, 0, stream>>>(a, p, ws);
+    return hipGetLastError();
 }
 
 hipError_t launch_attend(const Attend& a, uint8_t* ws, hipStream_t stream) {

@@ -204,6 +204,12 @@ bool attend_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t q_heads, uint64_t 
            n_tokens * q_heads / 128 + 2 * n_seqs * kv_heads < uint64_t{1} << 24;
 }
 
+bool expanded_dim_ok(uint64_t d) { return d >= 8 && d <= 128 && d % 8 == 0; }
+
+bool spans_meet(Span a, Span b) {
+    return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
+}
+
 // (the kernels multiply by scale log2 e, or 2 scale log2 e / softcap)
 bool score_ok(float scale, float softcap, int causal, uint64_t window) {
     return scale > 0 && scale < 1e38f && softcap >= 0 && softcap < 1e38f &&
@@ -484,6 +490,80 @@ sz_status sz_attend_latent(const sz_heads* q, const sz_heads* out, float* d_lse,
     return st;
 }
 
+uint64_t sz_attend_expanded_workspace_size(uint64_t heads, uint32_t value_dim,
+                                           const sz_batch* batch, uint64_t max_len) {
+    if (batch == nullptr || heads == 0 || heads > kMaxHeads || !expanded_dim_ok(value_dim) ||
+        batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxTokens ||
+        !attend_fits(batch->n_seqs, batch->n_tokens, heads, heads) || batch->n_seqs == 0 ||
+        batch->n_tokens == 0)
+        return 0;
+    return sz::attend_expanded_workspace((uint32_t)heads, value_dim, batch->n_seqs,
+                                         batch->n_tokens,
+                                         max_len == 0 || max_len > kMaxLen ? kMaxLen : max_len);
+}
+
+sz_status sz_attend_expanded(const sz_heads* q, const sz_heads* out, float* d_lse,
+                             const sz_heads* k, const sz_heads* k_rotary, const sz_heads* v,
+                             uint32_t key_dim, uint32_t rotary_dim, uint32_t value_dim,
+                             const int32_t* d_key_starts, uint64_t n_keys,
+                             const sz_batch* batch, uint64_t max_len, float scale, int causal,
+                             void* d_workspace, uint64_t workspace_bytes, int32_t* d_status,
+                             hipStream_t stream) {
+    if (!batch_ok(batch) || !expanded_dim_ok(key_dim) || !expanded_dim_ok(value_dim) ||
+        rotary_dim > 64 || rotary_dim % 8 != 0 || n_keys > kMaxTokens)
+        return SZ_ERR_INVALID_ARGUMENT;
+    const uint64_t n = batch->n_tokens;
+    const uint32_t dim = key_dim + rotary_dim;
+    if (!heads_ok(q, n, dim, false) || !heads_ok(out, n, value_dim, true) ||
+        q->type != SZ_TYPE_BF16 || q->heads != out->heads ||
+        !attend_fits(batch->n_seqs, n, q->heads, q->heads) ||
+        !apart(*q, dim, *out, value_dim, n, false))
+        return SZ_ERR_INVALID_ARGUMENT;
+    const auto keys_ok = [&](const sz_heads* x, uint32_t d) {
+        return heads_ok(x, n_keys, d, false) && x->type == SZ_TYPE_BF16 &&
+               x->token_stride < kMaxPageStride && !spans_meet(span(*x, n_keys, d), span(*out, n, value_dim));
+    };
+    if (!keys_ok(k, key_dim) || !keys_ok(v, value_dim) || k->heads != q->heads ||
+        v->heads != q->heads || (k_rotary == nullptr) != (rotary_dim == 0))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (k_rotary != nullptr && (!keys_ok(k_rotary, rotary_dim) ||
+                                (k_rotary->heads != 1 && k_rotary->heads != q->heads)))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (!(scale > 0 && scale < 1e38f) || !aligned(d_lse, 4) || !aligned(d_status, 4) ||
+        !aligned(d_key_starts, 4) || (batch->n_seqs > 0 && d_key_starts == nullptr))
+        return SZ_ERR_INVALID_ARGUMENT;
+    if (max_len == 0 || max_len > n_keys) max_len = n_keys;
+    if (max_len > kMaxLen) max_len = kMaxLen;
+    const uint64_t need =
+        max_len == 0 ? 0 : sz_attend_expanded_workspace_size(q->heads, value_dim, batch, max_len);
+    const Span lse = span_of(d_lse, d_lse == nullptr ? 0 : 4 * n * q->heads);
+    const Span work = span_of(d_workspace, need);
+    if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 256) ||
+                     workspace_bytes < need || spans_meet(work, lse)))
+        return SZ_ERR_INVALID_ARGUMENT;
+    const Span others[5] = {span(*q, n, dim), span(*out, n, value_dim), span(*k, n_keys, key_dim),
+                            span(*v, n_keys, value_dim),
+                            k_rotary == nullptr ? Span{0, 0} : span(*k_rotary, n_keys, rotary_dim)};
+    for (const Span& x : others)
+        if (spans_meet(lse, x) || spans_meet(work, x)) return SZ_ERR_INVALID_ARGUMENT;
+    if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
+    if (sz_status s = check_stream(stream)) return s;
+    sz::Cache heads{};
+    heads.kv_heads = (uint32_t)q->heads;
+    heads.head_dim = value_dim;
+    const sz::Attend a{rows_of(q), rows_of(out), d_lse, heads, batch_of(*batch), (int64_t)max_len,
+                       scale, 0, causal != 0, 0, value_dim};
+    const sz::Expanded e{rows_of(k), rows_of(k_rotary), rows_of(v), key_dim, rotary_dim, value_dim,
+                         d_key_starts, (int64_t)n_keys};
+    sz_status st =
+        hip_status(sz::launch_attend_expanded(a, e, static_cast<uint8_t*>(d_workspace), stream));
+    if (st == SZ_OK && d_status != nullptr)
+        st = hip_status(sz::launch_check_seqs(
+            sz::SeqCheck{heads, a.batch, a.max_len, 0, a.causal, 0, d_status, d_key_starts,
+                         (int64_t)n_keys}, stream));
+    return st;
+}
+
 uint64_t sz_weigh_workspace_size(uint64_t q_heads, const sz_kv_cache* cache,
                                  const sz_batch* batch, uint64_t max_len) {
     if (!weigh_sizes_ok(q_heads, cache, batch) || batch->n_seqs == 0 || batch->n_tokens == 0)
@@ -579,10 +659,9 @@ sz_status sz_evict_pages(const float* d_weights, uint64_t weight_heads, uint64_t
                              span_of(d_status, d_status == nullptr ? 0 : lens)};
     for (int i = 0; i < 4; i++) {
         for (const Span& r : read)
-            if (written[i].begin < r.end && r.begin < written[i].end) return SZ_ERR_INVALID_ARGUMENT;
+            if (spans_meet(written[i], r)) return SZ_ERR_INVALID_ARGUMENT;
         for (int j = 0; j < i; j++)
-            if (written[i].begin < written[j].end && written[j].begin < written[i].end)
-                return SZ_ERR_INVALID_ARGUMENT;
+            if (spans_meet(written[i], written[j])) return SZ_ERR_INVALID_ARGUMENT;
     }
     if (sz_status s = check_stream(stream)) return s;
     const sz::Evict a{d_weights, weights_pitch, (uint32_t)weight_heads, (uint32_t)budget,

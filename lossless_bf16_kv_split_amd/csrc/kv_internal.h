@@ -133,6 +133,19 @@ uint64_t attend_latent_workspace(uint32_t heads, const Cache& cache, uint32_t la
                                  uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len);
 hipError_t launch_attend_latent(const Attend& a, uint8_t* ws, hipStream_t stream);
 
+// Over keys and values of every head, in tensors: the Attend's cache has only
+// the number of heads (kv_heads), value_dim is head_dim too.
+struct Expanded {
+    Rows k, r, v;  // r: no heads without a rotary part, one for all, or as many as k
+    uint32_t key_dim, rotary_dim, value_dim;
+    const int32_t* key_starts;
+    int64_t n_keys;
+};
+uint64_t attend_expanded_workspace(uint32_t heads, uint32_t value_dim, uint64_t n_seqs,
+                                   uint64_t n_tokens, uint64_t max_len);
+hipError_t launch_attend_expanded(const Attend& a, const Expanded& e, uint8_t* ws,
+                                  hipStream_t stream);
+
 struct Weigh {
     Rows q;
     const float* lse;
@@ -181,6 +194,8 @@ struct SeqCheck {
     uint32_t causal;
     uint64_t window;
     int32_t* status;
+    const int32_t* key_starts = nullptr;  // not pages but rows from here on, of n_keys
+    int64_t n_keys = 0;
 };
 hipError_t launch_check_seqs(const SeqCheck& c, hipStream_t stream);
 
