@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kKeys = 64;  // of a step
 constexpr uint64_t kCus = 256;
+constexpr int kAhead = 6;  // products that operands are read from LDS ahead of
 
 // A workgroup's four waves: RW groups of 32 rows, each KW waves that share
 // its keys (in blocks of 32) and its elements of the output.
@@ -28,11 +29,12 @@ struct Shape {
     static constexpr int kLoads = DT / 32;                // KB that a wave fetches of them
     static constexpr int kSlices = DT / 16;               // of the first product
     static constexpr int kParts = DL / 32 / kKw;          // of the second, a wave's
-    static constexpr int kBlocks = kKw == 1 ? 2 : 1;      // of 32 keys, a wave's scores
     static constexpr uint32_t kWeights = 2 * kBuffer;     // LDS: weights [RW][2][2][64 lanes][16 B]
-    static constexpr uint32_t kTops = kWeights + (kKw > 1 ? RW * 4096 : 0);  // [RW][2][32] floats
-    static constexpr uint32_t kLds = kTops + (kKw > 1 ? RW * 256 : 0);
-    static_assert(kRow % 256 == 128, "rows start at alternating halves of the banks");
+    static constexpr uint32_t kTops = kWeights + RW * 4096;  // [RW][2][32] floats
+    static constexpr uint32_t kFlags = kTops + RW * 256;     // of each wave
+    static constexpr uint32_t kLds = kFlags + 16;
+    static_assert(RW <= 2 && kRow % 256 == 128, "rows start at alternating halves of the banks");
+    static_assert(2 * kLoads <= kSlices, "a load for every other product");
     static_assert(kLds <= 160 * 1024, "");
 };
 
@@ -44,15 +46,14 @@ __device__ __forceinline__ constexpr uint32_t mix(uint32_t j) {
     return (j >> 1 & 1) << 2 | (j >> 2 & 1) << 1 | (j >> 3 & 1);
 }
 
-template <int N>
-__device__ __forceinline__ void fetch_rows(__amdgpu_buffer_rsrc_t from, const uint32_t* at,
-                                           uint32_t lds) {
-    if constexpr (N >= 8) {
-        load_to_lds<8>(from, at, lds);
-        if constexpr (N > 8) fetch_rows<N - 8>(from, at + 8, lds + 8 * 1024);
-    } else {
-        load_to_lds<N>(from, at, lds);
-    }
+// 64 lanes' 16 bytes each from offsets of a buffer to consecutive bytes of LDS
+// (load_to_lds, one load, to stand between products: issuing one takes as long
+// as half a product).
+__device__ __forceinline__ void load_piece(__amdgpu_buffer_rsrc_t from, uint32_t at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds"
+                 :
+                 : "s"(lds), "s"(from), "v"(at)
+                 : "memory");
 }
 
 __device__ __forceinline__ void lds_barrier() {
@@ -61,19 +62,21 @@ __device__ __forceinline__ void lds_barrier() {
 
 template <int DL, int DT, int RW>
 __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p, float by,
-                                            uint8_t* ws, const Part& part, uint8_t* lds) {
+                                            uint8_t* ws, const Part& part, uint32_t half,
+                                            uint8_t* lds) {
     using S = Shape<DL, DT, RW>;
-    constexpr int kKw = S::kKw, kParts = S::kParts, kBlocks = S::kBlocks;
+    constexpr int kKw = S::kKw, kParts = S::kParts;
     constexpr uint32_t kRow = S::kRow;
     const uint32_t lane = threadIdx.x % kWave, n = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t rw = wave / kKw, kw = wave % kKw;
+    const uint32_t rw = wave / kKw, kw = wave % kKw, block = kw % 2;
+    const uint32_t r = 32 * (RW * half + rw) + n;  // the lane's row of the tile
     const Tile& t = part.t;
     const int32_t first = part.first, last = part.last;
     const uint32_t dim = a.cache.head_dim;
 
     // the row's query
-    const Row mine = find_row(a, p, t, (int32_t)(32 * rw + n));
+    const Row mine = find_row(a, p, t, (int32_t)r);
     bf16x8 q[S::kSlices];
     {
         const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
@@ -85,9 +88,12 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
             if (mine.on && 16 * s + 8 * h < dim)
                 v = *(const SZ_GLOBAL u32x4*)(row + 16 * s + 8 * h);
             q[s] = __builtin_bit_cast(bf16x8, v);
+            // (in accumulation registers, which the product reads as well: the
+            // output's sums have the others, where they can be scaled)
+            asm volatile("" : "+a"(q[s]));
         }
     }
-    const bool works = 32 * (int32_t)rw < t.rows;
+    const bool works = 32 * (int32_t)(RW * half + rw) < t.rows;
 
     // this wave's part of a step: 16 keys
     constexpr uint32_t kPast = 0x80000000u;
@@ -106,16 +112,23 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
         return jb < last ? a.cache.k_pages[table_row + ((uint32_t)jb >> a.cache.page_log2)] : 0;
     };
     uint64_t next_page = page_at(first);
-    const auto fetch = [&](int32_t j, uint32_t buffer) {
+    // A step's fetch: the rows of this wave's block (none past the last step),
+    // and their loads, one at a time
+    struct Fetch {
+        __amdgpu_buffer_rsrc_t rows;
+        uint32_t to;
+    };
+    const auto begin_fetch = [&](int32_t j, uint32_t buffer) {
         const int32_t jb = j + 16 * (int32_t)wave;
         const uint32_t slot = (uint32_t)jb & ((1u << a.cache.page_log2) - 1);
         const uint64_t at =
             (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(next_page >> 32)) << 32 |
             (uint32_t)__builtin_amdgcn_readfirstlane((int)next_page);
-        const auto rows = block_rows(a.cache, at, slot, 0, last - jb);
-        fetch_rows<S::kLoads>(rows, off, lds0 + buffer * S::kBuffer + wave * 16 * kRow);
         next_page = page_at(j + kKeys);
+        return Fetch{block_rows(a.cache, at, slot, 0, last - jb),
+                     lds0 + buffer * S::kBuffer + wave * 16 * kRow};
     };
+    const auto fetch = [&](const Fetch& f, int i) { load_piece(f.rows, off[i], f.to + 1024 * i); };
 
     // LDS addresses of this lane's reads.  Slice s of the keys: the first
     // one's address with bits 5 and 6 turned over by s % 4, and s / 4 times 128
@@ -146,114 +159,129 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
 #pragma unroll
         for (int i = 0; i < 16; i++) o[d][i] = 0;
 
-    const auto follow = [&](float top) {  // (the same top in both of a row's lanes)
-        if (__ballot(top > m + kLag) == 0) return;
-        top = fmaxf(top, m);
-        const float keep = __builtin_amdgcn_exp2f(m - top);
-        m = top;
-        l *= keep;
-#pragma unroll
-        for (int d = 0; d < kParts; d++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) o[d][i] *= keep;
-    };
-
     const uint32_t my_weights = lds0 + S::kWeights + rw * 4096 + 16 * lane;
     const uint32_t my_tops = lds0 + S::kTops + rw * 256 + 4 * n;
+    const uint32_t flags = lds0 + S::kFlags;
+    enum { kRise = 1, kOdd = 2 };
 
-    const auto compute = [&](int32_t j, uint32_t buffer) {
-        const bool edge = j + kKeys > t.all_hi;
-        const uint32_t ka = k_lane + buffer * S::kBuffer;
-        f32x16 s[kBlocks];
+    // A step, with the next one's fetch.  EDGE: some row does not see some key.
+    const auto compute = [&](int32_t j, uint32_t buffer, const Fetch& next, auto edge_step) {
+        constexpr bool edge = decltype(edge_step)::value;
+        const uint32_t ka = k_lane + buffer * S::kBuffer + block * 32 * kRow;
+        const uint32_t va = v_lane + buffer * S::kBuffer + kw * kParts * 64;
+        f32x16 s;
         float top = -INFINITY;
-        const uint32_t block0 = kKw == 1 ? 0 : kw % 2;
+        bool odd = false;  // an infinity or a NaN among the keys: no score is a number
         if (works) {
+            bf16x8 f[kAhead];
 #pragma unroll
-            for (int b = 0; b < kBlocks; b++) {
+            for (int c = 0; c < kAhead; c++) f[c] = keys_at(ka, c);
 #pragma unroll
-                for (int i = 0; i < 16; i++) s[b][i] = 0;
+            for (int i = 0; i < 16; i++) s[i] = 0;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int c = 0; c < S::kSlices; c++) {
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        keys_at(ka + (block0 + b) * 32 * kRow, c), q[c], s[b], 0, 0, 0);
-                    if (c % 6 == 5) __builtin_amdgcn_sched_barrier(0);
-                }
-                if (edge) {
-                    const Sees sees(0, mine.high, j + 32 * (int32_t)(block0 + b) + 4 * (int32_t)h);
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        if (!sees(8 * (i / 4) + i % 4)) s[b][i] = -INFINITY;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][i]);
+            for (int c = 0; c < S::kSlices; c++) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[c % kAhead], q[c], s, 0, 0, 0);
+                if (c + kAhead < S::kSlices) f[c % kAhead] = keys_at(ka, c + kAhead);
+                if (c % 2 == 0 && c / 2 < S::kLoads) fetch(next, c / 2);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < S::kLoads; i++) fetch(next, i);
+        }
+        u32x4 f[kAhead];
+        const auto words = [&](int g) { return value_words(va, g / kParts, g % kParts); };
+        // weights of this wave's 32 keys, and their sum
+        u32x4 w[4];
+        float sum = 0;
+        const auto weigh = [&] {
+            uint32_t x[8];
+            sum = 0;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float u = __builtin_amdgcn_exp2f(fmaf(s[i], by, -m));
+                const float v = __builtin_amdgcn_exp2f(fmaf(s[i + 1], by, -m));
+                sum += u + v;
+                x[i / 2] = pack_bf16(u, v);
+            }
+            if (kw < 2) {
+                *(SZ_LDS u32x4*)(uintptr_t)(my_weights + 2048 * kw) = u32x4{x[0], x[1], x[2], x[3]};
+                *(SZ_LDS u32x4*)(uintptr_t)(my_weights + 2048 * kw + 1024) =
+                    u32x4{x[4], x[5], x[6], x[7]};
+            }
+        };
+        if (works) {
+            if constexpr (edge) {
+                const Sees sees(0, mine.high, j + 32 * (int32_t)block + 4 * (int32_t)h);
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    odd = odd || !(fabsf(s[i]) <= FLT_MAX);
+                    if (!sees(8 * (i / 4) + i % 4)) s[i] = -INFINITY;
+                }
+                odd = __ballot(odd) != 0;
+            }
+#pragma unroll
+            for (int g = 0; g < kAhead; g++) f[g] = words(g);  // (under way meanwhile)
+#pragma unroll
+            for (int i = 0; i < 16; i++) top = fmaxf(top, s[i]);
             top *= by;
-            top = fmaxf(top, __shfl_xor(top, 32));
+            weigh();
         }
-        if constexpr (kKw > 1) {
-            if (works && kw < 2 && h == 0)
-                *(SZ_LDS float*)(uintptr_t)(my_tops + 128 * kw) = top;
-            lds_barrier();
-            if (works) top = fmaxf(top, *(const SZ_LDS float*)(uintptr_t)(my_tops + 128 * (1 - block0)));
-        }
-        u32x4 w[4];  // weights of 16 keys each
-        if (works) {
-            follow(top);
-#pragma unroll
-            for (int b = 0; b < kBlocks; b++) {
-                uint32_t x[8];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float u = __builtin_amdgcn_exp2f(fmaf(s[b][i], by, -m));
-                    const float v = __builtin_amdgcn_exp2f(fmaf(s[b][i + 1], by, -m));
-                    l += u + v;
-                    x[i / 2] = pack_bf16(u, v);
-                }
-                w[2 * b] = u32x4{x[0], x[1], x[2], x[3]};
-                w[2 * b + 1] = u32x4{x[4], x[5], x[6], x[7]};
-            }
-        }
-        if constexpr (kKw > 1) {
-            if (works && kw < 2) {
-                *(SZ_LDS u32x4*)(uintptr_t)(my_weights + 2048 * kw) = w[0];
-                *(SZ_LDS u32x4*)(uintptr_t)(my_weights + 2048 * kw + 1024) = w[1];
+        // The maximum belongs to all the waves of a row group: where a score
+        // rises above it too far, all take part in moving it, and weigh again.
+        const bool rise = __ballot(top > m + kLag) != 0;
+        if (lane == 0)
+            *(SZ_LDS uint32_t*)(uintptr_t)(flags + 4 * wave) = (rise ? kRise : 0) | (odd ? kOdd : 0);
+        lds_barrier();
+        const u32x4 any = *(const SZ_LDS u32x4*)(uintptr_t)flags;
+        const uint32_t all = __builtin_amdgcn_readfirstlane((int)(any.x | any.y | any.z | any.w));
+        if (all & kRise) {
+            if (works) {
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (kw < 2 && h == 0) *(SZ_LDS float*)(uintptr_t)(my_tops + 128 * kw) = top;
             }
             lds_barrier();
             if (works) {
+                top = fmaxf(top, *(const SZ_LDS float*)(uintptr_t)(my_tops + 128 * (1 - block)));
+                // (each row by its own scores: none depends on another's)
+                top = top > m + kLag ? top : m;
+                const float keep = __builtin_amdgcn_exp2f(m - top);
+                m = top;
+                l *= keep;
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    w[i] = *(const SZ_LDS u32x4*)(uintptr_t)(my_weights + 1024 * i);
+                for (int d = 0; d < kParts; d++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[d][i] *= keep;
+                weigh();
             }
+            lds_barrier();
         }
         if (!works) return;
-        const uint32_t va = v_lane + buffer * S::kBuffer + kw * kParts * 64;
-        // keys that some row of the tile sees and another does not: an
-        // infinity or a NaN among them must not reach the rows that do not
+        odd = edge && (all & kOdd) != 0;
+        l += sum;
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = *(const SZ_LDS u32x4*)(uintptr_t)(my_weights + 1024 * i);
+        // At an edge an infinity or a NaN must not reach the rows that do not
         // see it, where 0 times it would be NaN.  The values go in without it;
         // rows that see it get NaN for it (their score with it is infinite or
         // NaN, and so is its weight times it), by a product of ones in its
         // place with what each row sees.
-        const bool rim = edge && t.all_hi < last;
-        uint32_t halves = 0;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t16 = 0; t16 < 4; t16++)
+        for (int g = 0; g < 4 * kParts; g++) {
+            u32x4 x = f[g % kAhead];
+            if (edge && odd) {
 #pragma unroll
-            for (int d = 0; d < kParts; d++) {
-                u32x4 x = value_words(va, t16, d);
-                if (rim) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        halves |= odd_halves(x[i]);
-                        x[i] = plain_pair(x[i]);
-                    }
-                }
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w[t16]), o[d], 0, 0,
-                    0);
-                // (or operands are read far ahead, into registers that are not there)
-                if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 4; i++) x[i] = plain_pair(x[i]);
             }
-        if (__ballot(any_odd(halves)) == 0) return;
+            o[g % kParts] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w[g / kParts]),
+                o[g % kParts], 0, 0, 0);
+            if (g + kAhead < 4 * kParts) f[g % kAhead] = words(g + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!edge || !odd) return;
         const Sees sees(0, mine.high, j + 4 * (int32_t)h);
 #pragma unroll 1
         for (int t16 = 0; t16 < 4; t16++) {
@@ -288,21 +316,38 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
     };
     const int32_t steps = first < last ? (last - first + kKeys - 1) / kKeys : 0;
     arrived();  // (every wave is done with the part before)
-    if (steps > 0) fetch(first, 0);
-    for (int32_t x = 0; x < steps; x++) {
-        arrived();
-        if (x + 1 < steps) fetch(first + (x + 1) * kKeys, (x + 1) & 1);
-        compute(first + x * kKeys, x & 1);
+    if (steps > 0) {
+        const Fetch f = begin_fetch(first, 0);
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i++) fetch(f, i);
     }
+    // (the steps that every row sees all of come first)
+    int32_t inner = t.all_hi > first ? (t.all_hi - first) / kKeys : 0;
+    inner = inner < steps ? inner : steps;
+    const auto begin_step = [&](int32_t x) {
+        arrived();
+        return begin_fetch(first + (x + 1) * kKeys, (x + 1) & 1);
+    };
+    int32_t x = 0;
+#pragma unroll 1
+    for (; x < inner; x++) {
+        const Fetch f = begin_step(x);
+        compute(first + x * kKeys, x & 1, f, std::false_type{});
+    }
+#pragma unroll 1
+    for (; x < steps; x++) {
+        const Fetch f = begin_step(x);
+        compute(first + x * kKeys, x & 1, f, std::true_type{});
+    }
+    // nothing may still be on its way to this workgroup's LDS when it ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     float total = l + __shfl_xor(l, 32);
-    if constexpr (kKw > 1) {
-        // each of two waves has the sum over its block of every step's keys
-        lds_barrier();
-        if (kw < 2 && h == 0) *(SZ_LDS float*)(uintptr_t)(my_tops + 128 * kw) = total;
-        lds_barrier();
-        total += *(const SZ_LDS float*)(uintptr_t)(my_tops + 128 * (1 - kw % 2));
-    }
+    // each of two waves has the sum over its block of every step's keys
+    lds_barrier();
+    if (kw < 2 && h == 0) *(SZ_LDS float*)(uintptr_t)(my_tops + 128 * kw) = total;
+    lds_barrier();
+    total += *(const SZ_LDS float*)(uintptr_t)(my_tops + 128 * (1 - block));
     if (!mine.on) return;
     if (part.alone) {
         const float inv = inverse(total);
@@ -321,7 +366,6 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
             a.lse[(uint64_t)mine.token * a.q.heads + mine.head] = log_sum(m, total);
     } else {
         const Partial u = partial_of(ws, a, p, 0, part.slot);
-        const uint32_t r = 32 * rw + n;
 #pragma unroll
         for (int d = 0; d < kParts; d++)
 #pragma unroll
@@ -341,16 +385,23 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
     }
 }
 
-template <int DL, int DT, int RW, bool SHARED>
+// HALVES workgroups have a tile's rows between them and read the same keys at
+// the same time: numbers that differ by eight, which share an L2, so that the
+// keys come from memory once.
+template <int DL, int DT, int RW, int HALVES, bool SHARED>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_latent(Attend a, AttendPlan p, float by,
                                                                uint8_t* ws) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Shape<DL, DT, RW>::kLds];
-    const uint32_t index = blockIdx.x;
+    const uint32_t index =
+        HALVES == 1 ? blockIdx.x : blockIdx.x / (8 * HALVES) * 8 + blockIdx.x % 8;
+    const uint32_t half = HALVES == 1 ? 0 : blockIdx.x / 8 % HALVES;
+    if (!SHARED && index >= p.tiles) return;
     Walk<SHARED> walk(a, p);
     Part part;
     if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
     do {
-        latent_part<DL, DT, RW>(a, p, by, ws, part, lds);
+        if (32 * RW * (int32_t)half < part.t.rows)
+            latent_part<DL, DT, RW>(a, p, by, ws, part, half, lds);
     } while (walk.next(a, p, index, part));
 }
 
@@ -423,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
         a.lse[(uint64_t)w.token * a.q.heads + w.head] = log_sum(top, total);
 }
 
-// Tiles of 32 or 64 rows by what sequences have on average; whole where
+// Tiles of 32, 64 or 128 rows by what sequences have on average; whole where
 // they fill the chip or have few keys, shared out among one workgroup a CU
 // otherwise (attend_parts.h).
 constexpr uint64_t kManyTiles = 1024;
@@ -431,33 +482,38 @@ constexpr uint64_t kWholeKeys = 256;
 constexpr uint64_t kShareSeqs = 1024;
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 
+uint32_t halves(const AttendPlan& p) { return p.tile_log2 == 7 ? 2 : 1; }
+
 AttendPlan plan_latent(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len) {
     AttendPlan p{};
     p.group = heads;
     const uint64_t rows = n_tokens * heads;
-    p.tile_log2 = rows <= 32 * n_seqs ? 5 : 6;
+    p.tile_log2 = rows <= 32 * n_seqs ? 5 : rows <= 64 * n_seqs ? 6 : 7;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     const uint64_t full = rows >> p.tile_log2;
     const bool whole = n_seqs > kShareSeqs || (full > n_seqs ? full : n_seqs) >= kManyTiles ||
                        p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= kWholeKeys;
-    p.shares = whole ? 0 : (uint32_t)kCus;
-    p.alone = (uint32_t)kCus;
+    p.shares = whole ? 0 : (uint32_t)(kCus / halves(p));
+    p.alone = p.shares;
     return p;
 }
 
-template <int DL, int DT, int RW>
+template <int DL, int DT, int RW, int HALVES>
 void go(const Attend& a, const AttendPlan& p, float by, uint8_t* ws, hipStream_t stream) {
     const dim3 block(kThreads);
+    const uint32_t units = p.shares != 0 ? p.shares : p.tiles;
+    const dim3 grid(HALVES == 1 ? units : (units + 7) / 8 * 8 * HALVES);
     if (p.shares != 0)
-        k_attend_latent<DL, DT, RW, true><<<dim3(p.shares), block, 0, stream>>>(a, p, by, ws);
+        k_attend_latent<DL, DT, RW, HALVES, true><<<grid, block, 0, stream>>>(a, p, by, ws);
     else
-        k_attend_latent<DL, DT, RW, false><<<dim3(p.tiles), block, 0, stream>>>(a, p, by, ws);
+        k_attend_latent<DL, DT, RW, HALVES, false><<<grid, block, 0, stream>>>(a, p, by, ws);
 }
 
 template <int DL, int DT>
 void go(const Attend& a, const AttendPlan& p, float by, uint8_t* ws, hipStream_t stream) {
-    if (p.tile_log2 == 5) go<DL, DT, 1>(a, p, by, ws, stream);
-    else go<DL, DT, 2>(a, p, by, ws, stream);
+    if (p.tile_log2 == 5) go<DL, DT, 1, 1>(a, p, by, ws, stream);
+    else if (p.tile_log2 == 6) go<DL, DT, 2, 1>(a, p, by, ws, stream);
+    else go<DL, DT, 2, 2>(a, p, by, ws, stream);
 }
 
 }  // namespace
