@@ -75,24 +75,7 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
     const int32_t first = part.first, last = part.last;
     const uint32_t dim = a.cache.head_dim;
 
-    // the row's query
     const Row mine = find_row(a, p, t, (int32_t)r);
-    bf16x8 q[S::kSlices];
-    {
-        const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
-                              (uint64_t)mine.token * a.q.token_stride +
-                              (uint64_t)mine.head * a.q.head_stride;
-#pragma unroll
-        for (int s = 0; s < S::kSlices; s++) {
-            u32x4 v = {0, 0, 0, 0};
-            if (mine.on && 16 * s + 8 * h < dim)
-                v = *(const SZ_GLOBAL u32x4*)(row + 16 * s + 8 * h);
-            q[s] = __builtin_bit_cast(bf16x8, v);
-            // (in accumulation registers, which the product reads as well: the
-            // output's sums have the others, where they can be scaled)
-            asm volatile("" : "+a"(q[s]));
-        }
-    }
     const bool works = 32 * (int32_t)(RW * half + rw) < t.rows;
 
     // this wave's part of a step: 16 keys
@@ -112,6 +95,22 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
         return jb < last ? a.cache.k_pages[table_row + ((uint32_t)jb >> a.cache.page_log2)] : 0;
     };
     uint64_t next_page = page_at(first);
+
+    // the row's query, asked for before anything is waited for
+    bf16x8 q[S::kSlices];
+    {
+        const uint16_t* row = static_cast<const uint16_t*>(a.q.data) +
+                              (uint64_t)mine.token * a.q.token_stride +
+                              (uint64_t)mine.head * a.q.head_stride;
+#pragma unroll
+        for (int s = 0; s < S::kSlices; s++) {
+            u32x4 v = {0, 0, 0, 0};
+            if (mine.on && 16 * s + 8 * h < dim)
+                v = *(const SZ_GLOBAL u32x4*)(row + 16 * s + 8 * h);
+            q[s] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+
     // A step's fetch: the rows of this wave's block (none past the last step),
     // and their loads, one at a time
     struct Fetch {
@@ -315,12 +314,16 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
     const int32_t steps = first < last ? (last - first + kKeys - 1) / kKeys : 0;
-    arrived();  // (every wave is done with the part before)
+    lds_barrier();  // (every wave is done with the part before)
     if (steps > 0) {
         const Fetch f = begin_fetch(first, 0);
 #pragma unroll
         for (int i = 0; i < S::kLoads; i++) fetch(f, i);
     }
+    // (in accumulation registers, which the product reads as well: the output's
+    // sums have the others, where they can be scaled)
+#pragma unroll
+    for (int s = 0; s < S::kSlices; s++) asm volatile("" : "+a"(q[s]));
     // (the steps that every row sees all of come first)
     int32_t inner = t.all_hi > first ? (t.all_hi - first) / kKeys : 0;
     inner = inner < steps ? inner : steps;
