@@ -563,6 +563,12 @@ __device__ __forceinline__ float log_sum(float m, float l) {
     return l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// A barrier after which every wave's writes to LDS are there; loads from
+// memory that are under way stay so.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // N times 64 lanes' 16 bytes each, from offsets of a buffer to consecutive LDS
 // bytes, 1024 a time; offsets past the buffer's end store zeros.  Completion is
 // counted by vmcnt.  A load reads m0 and the resource's scalar registers, and

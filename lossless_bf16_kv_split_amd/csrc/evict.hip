@@ -14,23 +14,90 @@ namespace sz {
 namespace {
 
 constexpr uint64_t kCus = 256;
-constexpr int kBlocks = 4;           // of 16 keys, a wave's
-constexpr int kWaveKeys = 16 * kBlocks;
 
-// ROWS: the four waves have the same keys and share the rows; otherwise each
-// has keys of its own and all rows.  `splits` workgroups share a tile's rows.
+// Two forms.  Few rows a sequence (a token's heads, drafts): k_weigh_few, a
+// wave streams blocks of 32 keys against the rows that it holds.  Many:
+// k_weigh_tile, a wave holds 64 keys and the rows pass by, staged in LDS for
+// the four waves of a workgroup; `splits` workgroups share a tile's rows.
 struct WeighPlan {
     uint32_t group;   // G
+    bool few;
+    uint32_t keys;    // of a workgroup
+    uint32_t chunks;  // of so many keys up to max_len
     uint32_t splits;
-    uint32_t chunks;  // tiles of keys up to max_len
-    bool rows;
-    __host__ __device__ uint32_t tile() const { return rows ? kWaveKeys : kWaves * kWaveKeys; }
+};
+constexpr int kBlocks = 4;  // of 16 keys, a wave's of a tile
+constexpr int kWaveKeys = 16 * kBlocks;
+constexpr uint32_t kTileKeys = kWaves * kWaveKeys;
+
+// What a workgroup works on
+struct Work {
+    uint32_t kv, s, split;
+    int32_t tile;  // its first key
+    __device__ __forceinline__ Work(const Weigh& a, const WeighPlan& p) {
+        uint32_t rest = blockIdx.x;
+        kv = rest % a.cache.kv_heads;
+        rest /= a.cache.kv_heads;
+        s = rest % a.batch.n_seqs;
+        rest /= a.batch.n_seqs;
+        split = rest % p.splits;
+        tile = (int32_t)(rest / p.splits * p.keys);
+    }
 };
 
-// The sum over a row of 16 lanes of each of 16 values: lane n gets value n's.
-__device__ __forceinline__ float sum_lanes(float (&x)[16], uint32_t n) {
+// The new tokens of a sequence, of which `count` stand from c0 on, that see any
+// of the keys key0 .. key0 + keys - 1
+struct Tokens {
+    int64_t lo, hi;
+    __device__ __forceinline__ Tokens(const Weigh& a, int32_t count, int32_t c0, int32_t key0,
+                                      int32_t keys)
+        : lo(0), hi(count) {
+        if (a.causal) {
+            if (key0 > c0) lo = (int64_t)key0 - c0;
+            const int64_t past = (int64_t)key0 + keys - 1 + (int64_t)a.window - c0;
+            if (a.window != 0 && past < hi) hi = past;
+        }
+        if (lo > hi) hi = lo;
+    }
+};
+
+// Keys that the row of a token at position c sees: low .. high - 1
+__device__ __forceinline__ void seen_keys(const Weigh& a, int32_t len, int32_t c, int32_t& low,
+                                          int32_t& high) {
+    low = 0;
+    high = len;
+    if (a.causal) {
+        high = c + 1;
+        if (a.window != 0 && (int64_t)c + 1 > (int64_t)a.window) low = c + 1 - (int32_t)a.window;
+    }
+}
+
+// 16 keys' rows as the first operand: key n, elements 32 c + 8 h .. + 7
+template <int SLICES>
+__device__ __forceinline__ void load_keys(const Weigh& a, uint32_t s, uint32_t kv, int32_t j,
+                                          int32_t len, uint32_t lane, bf16x8 (&k)[SLICES]) {
+    const uint32_t n = lane % 16, h = lane / 16;
+    uint64_t page = 0;
+    if (j < len)
+        page = page_address(a.cache.k_pages, (uint64_t)s * a.cache.table_pitch +
+                                                 ((uint32_t)j >> a.cache.page_log2));
+    const auto rows = block_rows(a.cache, page, (uint32_t)j & ((1u << a.cache.page_log2) - 1), kv,
+                                 len - j);
 #pragma unroll
-    for (int half = 8; half >= 1; half /= 2) {
+    for (int c = 0; c < SLICES; c++) {
+        const uint32_t off = 32 * c + 8 * h < a.cache.head_dim
+                                 ? n * 2 * (uint32_t)a.cache.token_stride + 64 * c + 16 * h
+                                 : 0x80000000u;
+        k[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rows, off, 0, 0));
+    }
+}
+
+// The sum over a row of 16 lanes of each of N values: lane n gets value n %
+// N's.
+template <int N>
+__device__ __forceinline__ float sum_lanes(float (&x)[N], uint32_t n) {
+#pragma unroll
+    for (int half = N / 2; half >= 1; half /= 2) {
         const bool upper = n & half;
 #pragma unroll
         for (int i = 0; i < half; i++) {
@@ -39,187 +106,283 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16], uint32_t n) {
             x[i] = mine + __shfl_xor(other, half);
         }
     }
+#pragma unroll
+    for (int d = N; d < 16; d *= 2) x[0] += __shfl_xor(x[0], d);
     return x[0];
 }
 
-template <int DP, bool CAPPED, bool ROWS>
-__global__ __launch_bounds__(kThreads, 2) void k_weigh(Weigh a, WeighPlan p, Score score,
-                                                       float* ws) {
+template <bool CAPPED>
+__device__ __forceinline__ float weight_of(const Score& score, float z, float minus) {
+    const float x = CAPPED ? capped(score, z) + minus : fmaf(z, score.by, minus);
+    return __builtin_amdgcn_exp2f(x);
+}
+
+// ---- few rows ----------------------------------------------------------------
+template <int DP, bool CAPPED>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh a, WeighPlan p,
+                                                                          Score score) {
     constexpr int kSlices = DP / 32;
-    constexpr int kRowBlocks = DP > 128 ? 1 : 2;  // of 16 rows, worked on at a time
-    constexpr uint32_t kStepRows = 16 * kRowBlocks;
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    uint32_t rest = blockIdx.x;
-    const uint32_t kv = rest % a.cache.kv_heads;
-    rest /= a.cache.kv_heads;
-    const uint32_t s = rest % a.batch.n_seqs;
-    rest /= a.batch.n_seqs;
-    const uint32_t split = rest % p.splits;
-    const int32_t tile = (int32_t)(rest / p.splits * p.tile());
-    const Seq seq = load_seq(a.batch, s, a.max_len);
-    if (!seq.good || tile >= seq.len) return;
-    const int32_t key0 = tile + (ROWS ? 0 : kWaveKeys * (int32_t)wave);
+    const Work w(a, p);
+    const Seq seq = load_seq(a.batch, w.s, a.max_len);
+    if (!seq.good || w.tile >= seq.len) return;
+    const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
+    const int32_t past = seq.len - w.tile < (int32_t)p.keys ? seq.len : w.tile + (int32_t)p.keys;
+    const uint32_t dim = a.cache.head_dim;
+    const uint64_t line = ((uint64_t)w.s * a.cache.kv_heads + w.kv) * a.pitch;
+
+    // 16 rows from r0 on: the lane's own, its log-sum and what it sees
+    struct RowBlock {
+        bf16x8 q[kSlices];
+        float minus;
+        int32_t low, high, least;  // least: of its tokens' positions
+    };
+    const uint32_t rows = (uint32_t)count * p.group;
+    const auto load_rows = [&](uint32_t r0, RowBlock& b) {
+        const uint32_t row = r0 + n;
+        const bool on = row < rows;
+        const uint32_t token = on ? row / p.group : 0, head = on ? row % p.group : 0;
+        const uint64_t t = (uint32_t)seq.begin + token;
+        const uint32_t at = w.kv * p.group + head;
+        float lse = -INFINITY;
+        if (on) lse = *(const SZ_GLOBAL float*)(a.lse + t * a.q.heads + at);
+        const uint16_t* x = static_cast<const uint16_t*>(a.q.data) + t * a.q.token_stride +
+                            at * a.q.head_stride;
+#pragma unroll
+        for (int u = 0; u < kSlices; u++) {
+            u32x4 v = {0, 0, 0, 0};
+            if (on && 32 * u + 8 * h < dim) v = *(const SZ_GLOBAL u32x4*)(x + 32 * u + 8 * h);
+            b.q[u] = __builtin_bit_cast(bf16x8, v);
+        }
+        seen_keys(a, seq.len, c0 + (int32_t)token, b.low, b.high);
+        // (a row whose log-sum is -infinity has seen nothing)
+        if (lse == -INFINITY) b.high = b.low;
+        b.minus = -lse * kLog2e;
+    };
+    RowBlock row;
+    const uint32_t blocks = (rows + 15) / 16;
+    struct Keys {
+        bf16x8 k[2][kSlices];
+        float before;
+    };
+    // Keys of a block of 32, and what the lane's key had before.  Lane (n, h)
+    // ends with the sum of key 16 (n / 4 % 2) + 4 h + n % 4.
+    const int32_t mine = 16 * (int32_t)(n / 4 % 2) + 4 * (int32_t)h + (int32_t)(n % 4);
+    const auto load = [&](Keys& x, int32_t j) {
+        // (keys that no row sees are not read)
+        const Tokens t(a, count, c0, j, 32);
+        const int32_t upto = t.lo < t.hi ? past : j;
+        load_keys<kSlices>(a, w.s, w.kv, j, upto, lane, x.k[0]);
+        load_keys<kSlices>(a, w.s, w.kv, j + 16, upto, lane, x.k[1]);
+        x.before = 0;
+        if (a.before != nullptr && j + mine < past && j + mine < c0)
+            x.before = *(const SZ_GLOBAL float*)(a.before + line + (uint32_t)(j + mine));
+    };
+    const auto compute = [&](const Keys& x, int32_t j) {
+        float acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] = 0;
+        for (uint32_t b = 0; b < blocks; b++) {
+            if (blocks > 1) load_rows(16 * b, row);
+            f32x4 z[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                z[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int u = 0; u < kSlices; u++)
+                    z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.k[i][u], row.q[u], z[i], 0, 0,
+                                                                   0);
+            }
+            const Sees sees(row.low, row.high, j + 4 * (int32_t)h);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float e = weight_of<CAPPED>(score, z[i / 4][i % 4], row.minus);
+                acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
+            }
+        }
+        const float sum = sum_lanes<8>(acc, n);
+        if (n < 8 && j + mine < past)
+            a.weights[line + (uint32_t)(j + mine)] = fmaf(a.keep, x.before, sum);
+    };
+    constexpr int32_t kStride = 32 * kWaves;
+    int32_t j = w.tile + 32 * (int32_t)wave;
+    Keys even, odd;
+    load(even, j);
+    if (blocks == 1) load_rows(0, row);
+    for (; j < past; j += 2 * kStride) {
+        load(odd, j + kStride);
+        compute(even, j);
+        load(even, j + 2 * kStride);
+        if (j + kStride < past) compute(odd, j + kStride);
+    }
+}
+
+// ---- many rows ---------------------------------------------------------------
+//
+// Rows pass in steps of 32 through LDS: each wave fetches eight of them while
+// the step before is worked on, one barrier a step.  LDS rows are cut into
+// 16-byte pieces, piece c of row r at c ^ (r & 15) (r >> 1 & 7 with 64
+// elements), so that 16 rows' same piece lies in 16 places.
+template <int DP, bool CAPPED>
+__global__ __launch_bounds__(kThreads, 2) void k_weigh_tile(Weigh a, WeighPlan p, Score score,
+                                                            float* ws) {
+    constexpr int kSlices = DP / 32;
+    constexpr uint32_t kStepRows = 32, kRowBytes = 2 * DP;
+    constexpr int kLoads = DP / 64;  // 16-byte pieces of a lane, eight lanes a row
+    constexpr uint32_t kMixMask = DP == 64 ? 7 : 15;
+    __shared__ __attribute__((aligned(256))) uint8_t staged[2][kStepRows * kRowBytes];
+    __shared__ float minus_of[2][kStepRows];
+    __shared__ int32_t place_of[2][kStepRows];  // positions; none: INT32_MIN
+    const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Work w(a, p);
+    const Seq seq = load_seq(a.batch, w.s, a.max_len);
+    if (!seq.good || w.tile >= seq.len) return;
+    const int32_t key0 = w.tile + kWaveKeys * (int32_t)wave;
     const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
     const uint32_t dim = a.cache.head_dim;
 
-    // the rows (tokens of the sequence) that see any of this wave's keys
-    int64_t i_lo = 0, i_hi = count;
-    if (a.causal) {
-        if (key0 > c0) i_lo = (int64_t)key0 - c0;
-        const int64_t past = (int64_t)key0 + kWaveKeys - 1 + (int64_t)a.window - c0;
-        if (a.window != 0 && past < i_hi) i_hi = past;
-    }
-    if (key0 >= seq.len || i_lo > i_hi) i_hi = i_lo;
-    const uint32_t row_lo = (uint32_t)i_lo * p.group, row_hi = (uint32_t)i_hi * p.group;
+    // the rows of the tokens that see any of the workgroup's keys, in steps
+    const Tokens t(a, count, c0, w.tile, (int32_t)kTileKeys);
+    const uint32_t row_lo = (uint32_t)t.lo * p.group, row_hi = (uint32_t)t.hi * p.group;
     const uint64_t all = (row_hi - row_lo + kStepRows - 1) / kStepRows;
-    const uint32_t step0 = (uint32_t)(all * split / p.splits);
-    const uint32_t steps = (uint32_t)(all * (split + 1) / p.splits) - step0;
+    const uint32_t step0 = (uint32_t)(all * w.split / p.splits);
+    const uint32_t steps = (uint32_t)(all * (w.split + 1) / p.splits) - step0;
 
     float acc[16];  // keys 16 b + 4 h + i of key0
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[i] = 0;
     if (steps > 0) {
+        // the row that this lane fetches a part of
+        const uint32_t mine = 8 * wave + lane / 8;
+        const uint32_t d_token = kStepRows / p.group, d_head = kStepRows % p.group;
+        uint32_t row = row_lo + step0 * kStepRows + mine;
+        uint32_t token = row / p.group, head = row % p.group;
+        struct Fetch {
+            u32x4 v[kLoads];
+            float minus;
+            int32_t place;
+        };
+        const auto fetch = [&](Fetch& f) {
+            const bool on = row < row_hi;
+            const uint64_t x = (uint32_t)seq.begin + token;
+            const uint32_t at = w.kv * p.group + head;
+            const uint16_t* from = static_cast<const uint16_t*>(a.q.data) + x * a.q.token_stride +
+                                   at * a.q.head_stride;
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) {
+                const uint32_t e = 8 * (8 * i + lane % 8);
+                f.v[i] = u32x4{0, 0, 0, 0};
+                if (on && e < dim) f.v[i] = *(const SZ_GLOBAL u32x4*)(from + e);
+            }
+            float lse = -INFINITY;
+            if (on) lse = *(const SZ_GLOBAL float*)(a.lse + x * a.q.heads + at);
+            f.minus = lse;
+            f.place = on ? c0 + (int32_t)token : INT32_MIN;
+            token += d_token;
+            head += d_head;
+            if (head >= p.group) {
+                head -= p.group;
+                token++;
+            }
+            row += kStepRows;
+        };
+        const auto put = [&](const Fetch& f, uint32_t buffer) {
+            const uint32_t m = DP == 64 ? mine >> 1 : mine;
+#pragma unroll
+            for (int i = 0; i < kLoads; i++)
+                *reinterpret_cast<u32x4*>(&staged[buffer][mine * kRowBytes +
+                                                          ((8 * i + lane % 8) ^ (m & kMixMask)) *
+                                                              16]) = f.v[i];
+            if (lane % 8 == 0) {
+                // (a row whose log-sum is -infinity has seen nothing)
+                minus_of[buffer][mine] = -f.minus * kLog2e;
+                place_of[buffer][mine] = f.minus == -INFINITY ? INT32_MIN : f.place;
+            }
+        };
+        Fetch next;
+        fetch(next);
         bf16x8 k[kBlocks][kSlices];
 #pragma unroll
-        for (int b = 0; b < kBlocks; b++) {
-            const int32_t j = key0 + 16 * b;
-            uint64_t page = 0;
-            if (j < seq.len)
-                page = page_address(a.cache.k_pages, (uint64_t)s * a.cache.table_pitch +
-                                                         ((uint32_t)j >> a.cache.page_log2));
-            const auto rows = block_rows(a.cache, page,
-                                         (uint32_t)j & ((1u << a.cache.page_log2) - 1), kv,
-                                         seq.len - j);
-#pragma unroll
-            for (int c = 0; c < kSlices; c++) {
-                const uint32_t off = 32 * c + 8 * h < dim
-                                         ? n * 2 * (uint32_t)a.cache.token_stride + 64 * c + 16 * h
-                                         : 0x80000000u;
-                k[b][c] = __builtin_bit_cast(
-                    bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rows, off, 0, 0));
-            }
-        }
-        // this lane's row of each block: token and head advance by a step's rows
-        constexpr uint32_t kWalk = ROWS ? kWaves : 1;
-        const uint32_t stride = kWalk * kStepRows;
-        const uint32_t d_token = stride / p.group, d_head = stride % p.group;
-        uint32_t row = row_lo + (step0 + (ROWS ? wave : 0)) * kStepRows + n;
-        uint32_t token[kRowBlocks], head[kRowBlocks];
-#pragma unroll
-        for (int r = 0; r < kRowBlocks; r++) {
-            token[r] = (row + 16 * r) / p.group;
-            head[r] = (row + 16 * r) % p.group;
-        }
-        bf16x8 q[kRowBlocks][kSlices];
-        float lse[kRowBlocks];
-        int32_t c[kRowBlocks];
-        const auto load = [&] {
-#pragma unroll
-            for (int r = 0; r < kRowBlocks; r++) {
-                const bool on = row + 16 * r < row_hi;
-                c[r] = c0 + (int32_t)token[r];
-                lse[r] = INFINITY;
-                const uint64_t t = (uint32_t)seq.begin + token[r];
-                const uint32_t at = kv * p.group + head[r];
-                if (on) lse[r] = *(const SZ_GLOBAL float*)(a.lse + t * a.q.heads + at);
-                const uint16_t* x = static_cast<const uint16_t*>(a.q.data) +
-                                    t * a.q.token_stride + at * a.q.head_stride;
-#pragma unroll
-                for (int u = 0; u < kSlices; u++) {
-                    u32x4 v = {0, 0, 0, 0};
-                    if (on && 32 * u + 8 * h < dim)
-                        v = *(const SZ_GLOBAL u32x4*)(x + 32 * u + 8 * h);
-                    q[r][u] = __builtin_bit_cast(bf16x8, v);
-                }
-                token[r] += d_token;
-                head[r] += d_head;
-                if (head[r] >= p.group) {
-                    head[r] -= p.group;
-                    token[r]++;
-                }
-            }
-            row += stride;
-        };
-        load();
-        for (uint32_t step = ROWS ? wave : 0; step < steps; step += kWalk) {
-            // rows of this step, and whether each of them sees each key
+        for (int b = 0; b < kBlocks; b++)
+            load_keys<kSlices>(a, w.s, w.kv, key0 + 16 * b, seq.len, lane, k[b]);
+        put(next, 0);
+        fetch(next);
+        const uint32_t q_mix = (DP == 64 ? n >> 1 : n) & kMixMask;
+        for (uint32_t step = 0; step < steps; step++) {
+            lds_barrier();
+            const uint32_t buffer = step & 1;
+            // the step's rows: do all of them see all keys, or none any
             const uint32_t r0 = row_lo + (step0 + step) * kStepRows;
+            const uint32_t r1 = row_hi - r0 < kStepRows ? row_hi - 1 : r0 + kStepRows - 1;
             const int32_t first = c0 + (int32_t)(r0 / p.group);
-            const int32_t last = c0 + (int32_t)((r0 + kStepRows - 1) / p.group);
-            bool full = r0 + kStepRows <= row_hi &&
+            const int32_t last = c0 + (int32_t)(r1 / p.group);
+            const bool none = a.causal && last < key0;
+            const bool full = r0 + kStepRows <= row_hi &&
                               (!a.causal || (first >= key0 + kWaveKeys - 1 &&
-                                             (a.window == 0 || (int64_t)last - (int64_t)a.window <
-                                                                   key0)));
-            f32x4 z[kRowBlocks][kBlocks];
-            float minus[kRowBlocks];
-            int32_t low[kRowBlocks], high[kRowBlocks];  // keys that a row sees
+                                             (a.window == 0 ||
+                                              (int64_t)last - (int64_t)a.window < key0)));
+            if (!none && key0 < seq.len) {
+                float minus[2];
+                int32_t place[2];
+                f32x4 z[2][kBlocks];
 #pragma unroll
-            for (int r = 0; r < kRowBlocks; r++) {
-                minus[r] = -lse[r] * kLog2e;
-                low[r] = 0;
-                high[r] = seq.len;
-                if (a.causal) {
-                    high[r] = c[r] + 1;
-                    if (a.window != 0 && (int64_t)c[r] + 1 > (int64_t)a.window)
-                        low[r] = c[r] + 1 - (int32_t)a.window;
-                }
-                // (a row whose log-sum is -infinity has seen nothing)
-                const bool none = lse[r] == -INFINITY;
-                if (none || row - stride + 16 * r >= row_hi) high[r] = low[r];
-                full = full && __ballot(none) == 0;
-#pragma unroll
-                for (int b = 0; b < kBlocks; b++) {
-                    z[r][b] = f32x4{0, 0, 0, 0};
+                for (int r = 0; r < 2; r++) {
+                    minus[r] = minus_of[buffer][16 * r + n];
+                    place[r] = place_of[buffer][16 * r + n];
+                    bf16x8 q[kSlices];
 #pragma unroll
                     for (int u = 0; u < kSlices; u++)
-                        z[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[b][u], q[r][u], z[r][b],
-                                                                          0, 0, 0);
+                        q[u] = *reinterpret_cast<const bf16x8*>(
+                            &staged[buffer][(16 * r + n) * kRowBytes + ((4 * u + h) ^ q_mix) * 16]);
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++) {
+                        z[r][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                        for (int u = 0; u < kSlices; u++)
+                            z[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[b][u], q[u],
+                                                                              z[r][b], 0, 0, 0);
+                    }
+                }
+                const bool plain = full && __ballot(place[0] == INT32_MIN ||
+                                                    place[1] == INT32_MIN) == 0;
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        acc[i] += weight_of<CAPPED>(score, z[0][i / 4][i % 4], minus[0]) +
+                                  weight_of<CAPPED>(score, z[1][i / 4][i % 4], minus[1]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        int32_t low, high;
+                        seen_keys(a, seq.len, place[r], low, high);
+                        if (place[r] == INT32_MIN) high = low;
+                        const Sees sees(low, high, key0 + 4 * (int32_t)h);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            const float e = weight_of<CAPPED>(score, z[r][i / 4][i % 4], minus[r]);
+                            acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
+                        }
+                    }
                 }
             }
-            load();
-#pragma unroll
-            for (int b = 0; b < kBlocks; b++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float sum = 0;
-#pragma unroll
-                    for (int r = 0; r < kRowBlocks; r++) {
-                        const float x = CAPPED ? capped(score, z[r][b][i]) + minus[r]
-                                               : fmaf(z[r][b][i], score.by, minus[r]);
-                        float w = __builtin_amdgcn_exp2f(x);
-                        if (!full && !Sees(low[r], high[r], key0 + 4 * (int32_t)h)(16 * b + i))
-                            w = 0;
-                        sum += w;
-                    }
-                    acc[4 * b + i] += sum;
-                }
+            put(next, buffer ^ 1);
+            fetch(next);
         }
     }
 
     // lane (n, h) gets the sum of key 16 (n / 4) + 4 h + n % 4
-    const float sum = sum_lanes(acc, n);
-    const int32_t mine = 16 * (int32_t)(n / 4) + 4 * (int32_t)h + (int32_t)(n % 4);
-    float total = sum;
-    if constexpr (ROWS) {
-        __shared__ float parts[kWaves][kWaveKeys];
-        parts[wave][mine] = sum;
-        __syncthreads();
-        if (wave != 0) return;
-        total = 0;
-#pragma unroll
-        for (uint32_t w = 0; w < kWaves; w++) total += parts[w][mine];
-    }
-    const int32_t j = key0 + mine;
+    const float sum = sum_lanes<16>(acc, n);
+    const int32_t j = key0 + 16 * (int32_t)(n / 4) + 4 * (int32_t)h + (int32_t)(n % 4);
     if (j >= seq.len) return;
-    const uint64_t line = (uint64_t)s * a.cache.kv_heads + kv;
+    const uint64_t line = (uint64_t)w.s * a.cache.kv_heads + w.kv;
     if (p.splits > 1) {
-        ws[((uint64_t)split * a.batch.n_seqs * a.cache.kv_heads + line) * (uint64_t)a.max_len +
-           (uint32_t)j] = total;
+        ws[((uint64_t)w.split * a.batch.n_seqs * a.cache.kv_heads + line) * (uint64_t)a.max_len +
+           (uint32_t)j] = sum;
     } else {
         const uint64_t at = line * a.pitch + (uint32_t)j;
-        if (a.before != nullptr && j < c0) total = fmaf(a.keep, a.before[at], total);
-        a.weights[at] = total;
+        a.weights[at] = a.before != nullptr && j < c0 ? fmaf(a.keep, a.before[at], sum) : sum;
     }
 }
 
@@ -234,6 +397,7 @@ __global__ __launch_bounds__(kThreads) void k_weigh_join(Weigh a, WeighPlan p, c
     const int32_t c0 = seq.len - (seq.end - seq.begin);
     const uint64_t lines = (uint64_t)a.batch.n_seqs * a.cache.kv_heads;
     float total = 0;
+#pragma unroll 8
     for (uint32_t i = 0; i < p.splits; i++) total += ws[(i * lines + line) * (uint64_t)a.max_len + j];
     const uint64_t at = line * a.pitch + j;
     if (a.before != nullptr && (int32_t)j < c0) total = fmaf(a.keep, a.before[at], total);
@@ -244,18 +408,28 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
                      uint64_t max_len) {
     WeighPlan p;
     p.group = q_heads / c.kv_heads;
-    const uint64_t rows = n_tokens * p.group;
-    const uint64_t lines = n_seqs * c.kv_heads;
-    // rows among the waves where a sequence has many, unless whole waves' keys
-    // fill the chip
-    const uint64_t wide = (max_len + kWaves * kWaveKeys - 1) / (kWaves * kWaveKeys);
-    p.rows = rows >= 128 * n_seqs && wide * lines < 4 * kCus;
-    p.chunks = (uint32_t)((max_len + p.tile() - 1) / p.tile());
-    const uint64_t groups = p.chunks * lines;
-    uint64_t splits = 2 * kCus / groups;
-    const uint64_t most = rows / n_seqs / 512;  // 512 rows each at least
-    splits = splits < most ? splits : most;
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
+    const uint64_t rows = n_tokens * p.group, lines = n_seqs * c.kv_heads;
+    p.few = rows <= 32 * n_seqs;
+    p.splits = 1;
+    if (p.few) {
+        // as many keys a workgroup as leave four of them to a CU, 128 (a block a
+        // wave) to 1024
+        uint64_t keys = 1024;
+        while (keys > 128 && (max_len + keys - 1) / keys * lines < 4 * kCus) keys /= 2;
+        p.keys = (uint32_t)keys;
+    } else {
+        p.keys = kTileKeys;
+    }
+    p.chunks = (uint32_t)((max_len + p.keys - 1) / p.keys);
+    if (!p.few) {
+        // rows among so many workgroups that the causal ones' uneven shares even
+        // out, 256 rows each at least
+        const uint64_t groups = p.chunks * lines;
+        uint64_t splits = 8 * kCus / groups;
+        const uint64_t most = rows / n_seqs / 256;
+        splits = splits < most ? splits : most;
+        p.splits = (uint32_t)(splits < 1 ? 1 : splits);
+    }
     return p;
 }
 
@@ -270,8 +444,8 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
         x.softcap = a.softcap;
         score = score_of(x);
     }
-    if (p.rows) k_weigh<DP, CAPPED, true><<<grid, block, 0, stream>>>(a, p, score, ws);
-    else k_weigh<DP, CAPPED, false><<<grid, block, 0, stream>>>(a, p, score, ws);
+    if (p.few) k_weigh_few<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score);
+    else k_weigh_tile<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score, ws);
 }
 
 // ---- eviction --------------------------------------------------------------

@@ -56,10 +56,6 @@ __device__ __forceinline__ void load_piece(__amdgpu_buffer_rsrc_t from, uint32_t
                  : "memory");
 }
 
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 template <int DL, int DT, int RW>
 __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p, float by,
                                             uint8_t* ws, const Part& part, uint32_t half,
