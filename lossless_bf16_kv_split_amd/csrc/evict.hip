@@ -101,9 +101,11 @@ __device__ __forceinline__ float sum_lanes(float (&x)[N], uint32_t n) {
         const bool upper = n & half;
 #pragma unroll
         for (int i = 0; i < half; i++) {
-            const float mine = upper ? x[i + half] : x[i];
-            const float other = upper ? x[i] : x[i + half];
-            x[i] = mine + __shfl_xor(other, half);
+            float low = x[i], high = x[i + half];
+            // (two values to choose from; unseen, the compiler makes all the
+            // steps' choices one index into x, a chain of a thousand selects)
+            asm("" : "+v"(low), "+v"(high));
+            x[i] = (upper ? high : low) + __shfl_xor(upper ? low : high, half);
         }
     }
 #pragma unroll
@@ -162,10 +164,20 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
     };
     RowBlock row;
     const uint32_t blocks = (rows + 15) / 16;
+    // 32 keys as they are loaded, DP / 8 lanes a row (rows of consecutive lanes
+    // leave the address units a quarter of the work that the operands' order
+    // does: 104 us, not .., for 48 tokens); LDS turns them into operands.
+    constexpr int kLanes = DP / 8, kLoads = 32 * kLanes / (int)kWave;
+    constexpr uint32_t kRowBytes = 2 * DP, kMixMask = DP == 64 ? 7 : 15;
+    __shared__ __attribute__((aligned(256))) uint8_t turned[kWaves][32 * kRowBytes];
+    const auto mix = [](uint32_t r) { return (DP == 64 ? r >> 1 : r) & kMixMask; };
     struct Keys {
-        bf16x8 k[2][kSlices];
+        u32x4 k[kLoads];
         float before;
     };
+    const uint32_t piece = lane % kLanes;
+    const uint32_t off0 = 8 * piece < dim ? lane / kLanes * 2 * (uint32_t)a.cache.token_stride + 16 * piece
+                                          : 0x80000000u;
     // Keys of a block of 32, and what the lane's key had before.  Lane (n, h)
     // ends with the sum of key 16 (n / 4 % 2) + 4 h + n % 4.
     const int32_t mine = 16 * (int32_t)(n / 4 % 2) + 4 * (int32_t)h + (int32_t)(n % 4);
@@ -173,13 +185,43 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
         // (keys that no row sees are not read)
         const Tokens t(a, count, c0, j, 32);
         const int32_t upto = t.lo < t.hi ? past : j;
-        load_keys<kSlices>(a, w.s, w.kv, j, upto, lane, x.k[0]);
-        load_keys<kSlices>(a, w.s, w.kv, j + 16, upto, lane, x.k[1]);
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            const int32_t jb = j + 16 * b;
+            uint64_t page = 0;
+            if (jb < upto)
+                page = page_address(a.cache.k_pages, (uint64_t)w.s * a.cache.table_pitch +
+                                                         ((uint32_t)jb >> a.cache.page_log2));
+            const auto rows =
+                block_rows(a.cache, page, (uint32_t)jb & ((1u << a.cache.page_log2) - 1), w.kv,
+                           upto - jb);
+#pragma unroll
+            for (int i = 0; i < kLoads / 2; i++)
+                x.k[kLoads / 2 * b + i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rows,
+                    off0 + i * ((int)kWave / kLanes) * 2 * (uint32_t)a.cache.token_stride, 0, 0);
+        }
         x.before = 0;
         if (a.before != nullptr && j + mine < past && j + mine < c0)
             x.before = *(const SZ_GLOBAL float*)(a.before + line + (uint32_t)(j + mine));
     };
     const auto compute = [&](const Keys& x, int32_t j) {
+        bf16x8 k[2][kSlices];
+        {
+            uint8_t* lds = turned[wave];
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) {
+                const uint32_t r = i * (kWave / kLanes) + lane / kLanes;
+                *reinterpret_cast<u32x4*>(lds + r * kRowBytes + (piece ^ mix(r)) * 16) = x.k[i];
+            }
+            __builtin_amdgcn_wave_barrier();  // (the wave's own: in order)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int u = 0; u < kSlices; u++)
+                    k[i][u] = *reinterpret_cast<const bf16x8*>(
+                        lds + (16 * i + n) * kRowBytes + ((4 * u + h) ^ mix(n)) * 16);
+        }
         float acc[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[i] = 0;
@@ -191,7 +233,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
                 z[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int u = 0; u < kSlices; u++)
-                    z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.k[i][u], row.q[u], z[i], 0, 0,
+                    z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[i][u], row.q[u], z[i], 0, 0,
                                                                    0);
             }
             const Sees sees(row.low, row.high, j + 4 * (int32_t)h);
