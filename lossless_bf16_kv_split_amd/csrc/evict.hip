@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
 // 16-byte pieces, piece c of row r at c ^ (r & 15) (r >> 1 & 7 with 64
 // elements), so that 16 rows' same piece lies in 16 places.
 template <int DP, bool CAPPED>
-__global__ __launch_bounds__(kThreads, 2) void k_weigh_tile(Weigh a, WeighPlan p, Score score,
+__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p, Score score,
                                                             float* ws) {
     constexpr int kSlices = DP / 32;
     constexpr uint32_t kStepRows = 32, kRowBytes = 2 * DP;
@@ -296,53 +296,86 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh_tile(Weigh a, WeighPlan p
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[i] = 0;
     if (steps > 0) {
-        // the row that this lane fetches a part of
+        // the row that this lane fetches a part of: its address and its
+        // log-sum's move on by a step's tokens and heads, with or without a
+        // token more
         const uint32_t mine = 8 * wave + lane / 8;
         const uint32_t d_token = kStepRows / p.group, d_head = kStepRows % p.group;
+        const int64_t q_step = 2 * ((int64_t)d_token * (int64_t)a.q.token_stride +
+                                    (int64_t)d_head * (int64_t)a.q.head_stride);
+        const int64_t q_wrap = 2 * ((int64_t)a.q.token_stride -
+                                    (int64_t)p.group * (int64_t)a.q.head_stride);
+        const int64_t l_step = 4 * ((int64_t)d_token * a.q.heads + d_head);
+        const int64_t l_wrap = 4 * ((int64_t)a.q.heads - p.group);
         uint32_t row = row_lo + step0 * kStepRows + mine;
-        uint32_t token = row / p.group, head = row % p.group;
+        uint32_t head = row % p.group;
+        int32_t place = c0 + (int32_t)(row / p.group);
+        uint64_t from, lse_at;
+        {
+            const uint64_t token = (uint32_t)seq.begin + row / p.group;
+            const uint32_t at = w.kv * p.group + head;
+            from = reinterpret_cast<uint64_t>(a.q.data) +
+                   2 * (token * a.q.token_stride + at * a.q.head_stride + 8 * (lane % 8));
+            lse_at = reinterpret_cast<uint64_t>(a.lse) + 4 * (token * a.q.heads + at);
+        }
         struct Fetch {
             u32x4 v[kLoads];
-            float minus;
+            float lse;
             int32_t place;
         };
         const auto fetch = [&](Fetch& f) {
             const bool on = row < row_hi;
-            const uint64_t x = (uint32_t)seq.begin + token;
-            const uint32_t at = w.kv * p.group + head;
-            const uint16_t* from = static_cast<const uint16_t*>(a.q.data) + x * a.q.token_stride +
-                                   at * a.q.head_stride;
 #pragma unroll
-            for (int i = 0; i < kLoads; i++) {
-                const uint32_t e = 8 * (8 * i + lane % 8);
-                f.v[i] = u32x4{0, 0, 0, 0};
-                if (on && e < dim) f.v[i] = *(const SZ_GLOBAL u32x4*)(from + e);
+            for (int i = 0; i < kLoads; i++) f.v[i] = u32x4{0, 0, 0, 0};
+            f.lse = -INFINITY;
+            if (on) {
+                f.lse = *(const SZ_GLOBAL float*)lse_at;
+#pragma unroll
+                for (int i = 0; i < kLoads; i++)
+                    if (64 * i + 8 * (lane % 8) < dim)
+                        f.v[i] = *(const SZ_GLOBAL u32x4*)(from + 128 * i);
             }
-            float lse = -INFINITY;
-            if (on) lse = *(const SZ_GLOBAL float*)(a.lse + x * a.q.heads + at);
-            f.minus = lse;
-            f.place = on ? c0 + (int32_t)token : INT32_MIN;
-            token += d_token;
-            head += d_head;
-            if (head >= p.group) {
-                head -= p.group;
-                token++;
-            }
+            f.place = place;
             row += kStepRows;
+            head += d_head;
+            const bool wraps = head >= p.group;
+            head -= wraps ? p.group : 0;
+            place += (int32_t)d_token + wraps;
+            from += q_step + (wraps ? q_wrap : 0);
+            lse_at += l_step + (wraps ? l_wrap : 0);
         };
+        const uint32_t put_mix = (DP == 64 ? mine >> 1 : mine) & kMixMask;
         const auto put = [&](const Fetch& f, uint32_t buffer) {
-            const uint32_t m = DP == 64 ? mine >> 1 : mine;
 #pragma unroll
             for (int i = 0; i < kLoads; i++)
                 *reinterpret_cast<u32x4*>(&staged[buffer][mine * kRowBytes +
-                                                          ((8 * i + lane % 8) ^ (m & kMixMask)) *
-                                                              16]) = f.v[i];
+                                                          ((8 * i + lane % 8) ^ put_mix) * 16]) =
+                    f.v[i];
             if (lane % 8 == 0) {
                 // (a row whose log-sum is -infinity has seen nothing)
-                minus_of[buffer][mine] = -f.minus * kLog2e;
-                place_of[buffer][mine] = f.minus == -INFINITY ? INT32_MIN : f.place;
+                minus_of[buffer][mine] = -f.lse * kLog2e;
+                place_of[buffer][mine] = f.lse == -INFINITY ? INT32_MIN : f.place;
             }
         };
+        // Steps [none, ..) have a row that sees one of this wave's keys, steps
+        // [full0, full1) only rows that see all of them.
+        const auto step_of = [&](int64_t rows_before, bool up) {
+            int64_t x = rows_before - row_lo + (up ? (int64_t)kStepRows - 1 : 0);
+            x = (x < 0 ? 0 : x) / kStepRows - step0;
+            return (uint32_t)(x < 0 ? 0 : x > steps ? steps : x);
+        };
+        const int64_t group = p.group;
+        uint32_t none = key0 < seq.len ? 0 : steps, full0 = 0, full1 = step_of(row_hi, false);
+        if (a.causal) {
+            const int64_t first = key0 - (int64_t)c0;  // the token that stands at key0
+            if (key0 < seq.len && first > 0)
+                none = first * group >= row_hi ? steps : step_of(first * group, false);
+            full0 = step_of((first + kWaveKeys - 1) * group, true);
+            if (a.window != 0) {
+                const uint32_t end = step_of((first + (int64_t)a.window) * group, false);
+                full1 = end < full1 ? end : full1;
+            }
+        }
         Fetch next;
         fetch(next);
         bf16x8 k[kBlocks][kSlices];
@@ -350,68 +383,92 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh_tile(Weigh a, WeighPlan p
         for (int b = 0; b < kBlocks; b++)
             load_keys<kSlices>(a, w.s, w.kv, key0 + 16 * b, seq.len, lane, k[b]);
         put(next, 0);
+        // (here, or every step waits for them again, and for the rows behind)
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+            for (int u = 0; u < kSlices; u++) asm volatile("" : "+v"(k[b][u]));
         fetch(next);
         const uint32_t q_mix = (DP == 64 ? n >> 1 : n) & kMixMask;
-        for (uint32_t step = 0; step < steps; step++) {
-            lds_barrier();
+        uint32_t step = 0;
+        // 16 of a step's rows: the lane's, its products with the keys
+        struct Products {
+            f32x4 z[kBlocks];
+            float minus;
+            int32_t place;
+        };
+        const auto products = [&](Products& x, int r) {
             const uint32_t buffer = step & 1;
-            // the step's rows: do all of them see all keys, or none any
-            const uint32_t r0 = row_lo + (step0 + step) * kStepRows;
-            const uint32_t r1 = row_hi - r0 < kStepRows ? row_hi - 1 : r0 + kStepRows - 1;
-            const int32_t first = c0 + (int32_t)(r0 / p.group);
-            const int32_t last = c0 + (int32_t)(r1 / p.group);
-            const bool none = a.causal && last < key0;
-            const bool full = r0 + kStepRows <= row_hi &&
-                              (!a.causal || (first >= key0 + kWaveKeys - 1 &&
-                                             (a.window == 0 ||
-                                              (int64_t)last - (int64_t)a.window < key0)));
-            if (!none && key0 < seq.len) {
-                float minus[2];
-                int32_t place[2];
-                f32x4 z[2][kBlocks];
+            x.minus = minus_of[buffer][16 * r + n];
+            x.place = place_of[buffer][16 * r + n];
+            bf16x8 q[kSlices];
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    minus[r] = minus_of[buffer][16 * r + n];
-                    place[r] = place_of[buffer][16 * r + n];
-                    bf16x8 q[kSlices];
+            for (int u = 0; u < kSlices; u++)
+                q[u] = *reinterpret_cast<const bf16x8*>(
+                    &staged[buffer][(16 * r + n) * kRowBytes + ((4 * u + h) ^ q_mix) * 16]);
 #pragma unroll
-                    for (int u = 0; u < kSlices; u++)
-                        q[u] = *reinterpret_cast<const bf16x8*>(
-                            &staged[buffer][(16 * r + n) * kRowBytes + ((4 * u + h) ^ q_mix) * 16]);
+            for (int b = 0; b < kBlocks; b++) {
+                x.z[b] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int b = 0; b < kBlocks; b++) {
-                        z[r][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int u = 0; u < kSlices; u++)
-                            z[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[b][u], q[u],
-                                                                              z[r][b], 0, 0, 0);
-                    }
-                }
-                const bool plain = full && __ballot(place[0] == INT32_MIN ||
-                                                    place[1] == INT32_MIN) == 0;
-                if (plain) {
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        acc[i] += weight_of<CAPPED>(score, z[0][i / 4][i % 4], minus[0]) +
-                                  weight_of<CAPPED>(score, z[1][i / 4][i % 4], minus[1]);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        int32_t low, high;
-                        seen_keys(a, seq.len, place[r], low, high);
-                        if (place[r] == INT32_MIN) high = low;
-                        const Sees sees(low, high, key0 + 4 * (int32_t)h);
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const float e = weight_of<CAPPED>(score, z[r][i / 4][i % 4], minus[r]);
-                            acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
-                        }
-                    }
-                }
+                for (int u = 0; u < kSlices; u++)
+                    x.z[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[b][u], q[u], x.z[b], 0, 0,
+                                                                     0);
             }
-            put(next, buffer ^ 1);
+        };
+        const auto end_step = [&] {
+            put(next, (step & 1) ^ 1);
             fetch(next);
+            step++;
+        };
+        const auto edges = [&](uint32_t stop) {
+#pragma unroll 1
+            while (step < stop) {
+                lds_barrier();
+#pragma unroll 1
+                for (int r = 0; r < 2; r++) {
+                    Products x;
+                    products(x, r);
+                    int32_t low, high;
+                    seen_keys(a, seq.len, x.place, low, high);
+                    if (x.place == INT32_MIN) high = low;
+                    const Sees sees(low, high, key0 + 4 * (int32_t)h);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const float e = weight_of<CAPPED>(score, x.z[i / 4][i % 4], x.minus);
+                        acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
+                    }
+                }
+                end_step();
+            }
+        };
+#pragma unroll 1
+        while (step < none) {
+            lds_barrier();
+            end_step();
         }
+        edges(full0 < steps ? full0 : steps);
+#pragma unroll 1
+        while (step < full1) {
+            lds_barrier();
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                Products x;
+                products(x, r);
+                const bool nothing = x.place == INT32_MIN;
+                if (__ballot(nothing) != 0) {
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) x.z[b][i] = nothing ? 0 : x.z[b][i];
+                    x.minus = nothing ? -INFINITY : x.minus;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    acc[i] += weight_of<CAPPED>(score, x.z[i / 4][i % 4], x.minus);
+            }
+            end_step();
+        }
+        edges(steps);
     }
 
     // lane (n, h) gets the sum of key 16 (n / 4) + 4 h + n % 4
