@@ -550,20 +550,27 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
 // ---- eviction --------------------------------------------------------------
 //
 // One workgroup for every row of weights finds which tokens stay; then the
-// rows of those are copied into other pages.  Order-preserving: FP32 weights
-// as unsigned numbers (NaN lowest, both zeros the same) and the key of the last
-// one that stays by counting digits, eleven bits at a time, from the top;
-// among equals the first ones stay.  Bound by latency: five passes over the
-// weights by one workgroup.
+// rows of those are copied into other pages.  Tokens get order-preserving keys:
+// FP32 weights as unsigned numbers, tokens that stay in any case above them
+// all.  The key of the last one that stays is found by counting digits, eleven
+// bits at a time, from the top; of equal keys the first stay.  Up to 32,768
+// weights and keys stay in registers over the passes, every load under way at
+// once; more are read again in pieces of so many for each.  A wave has
+// consecutive weights, 64 at a time, so that ballots give each token its place.
+// Bound by the vector instructions of one CU, about thirty for 64 weights.
 constexpr uint32_t kPickThreads = 1024;
 constexpr uint32_t kPickWaves = kPickThreads / kWave;
-constexpr uint32_t kDigit = 11, kBins = 1u << kDigit, kCopies = 4;
-constexpr uint32_t kRun = 8;  // consecutive weights of a thread in the last pass
+constexpr uint32_t kDigit = 11, kBins = 1u << kDigit, kCopies = 2;
+constexpr uint32_t kHold = 32;  // weights of a thread
+constexpr uint32_t kPiece = kHold * kPickThreads;
 
-__device__ __forceinline__ uint32_t rank_of(float w) {
-    if (w != w) return 0;
+// Keys: 0 no token, kNan, numbers from 0x007FFFFF (-infinity) to 0xFF800000,
+// kSafe.  Both zeros have the same.
+constexpr uint32_t kNan = 1, kSafe = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t key_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.0f);  // (-0 + 0 is 0)
-    return u >> 31 ? ~u : u | 0x80000000u;
+    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return w != w ? kNan : key;
 }
 
 // Running sums over the lanes of a wave
@@ -577,31 +584,28 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
     return x;
 }
 
-// The sum of x over the threads before this one, and over all of them
-struct Scan {
-    uint32_t before, all;
-};
-__device__ __forceinline__ Scan group_scan(uint32_t x, uint32_t* lds) {
-    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const uint32_t upto = wave_scan(x);
-    __syncthreads();  // (lds has been read)
-    if (lane == kWave - 1) lds[wave] = upto;
-    __syncthreads();
-    Scan r{upto - x, 0};
+// What the waves before this one have, and all of them, of a number for each
+struct Before {
+    uint32_t before = 0, all = 0;
+    __device__ __forceinline__ Before(const uint32_t* of, uint32_t wave) {
+        u32x4 v[kPickWaves / 4];
 #pragma unroll
-    for (uint32_t i = 0; i < kPickWaves; i++) {
-        const uint32_t y = lds[i];
-        if (i < wave) r.before += y;
-        r.all += y;
+        for (uint32_t i = 0; i < kPickWaves / 4; i++) v[i] = reinterpret_cast<const u32x4*>(of)[i];
+#pragma unroll
+        for (uint32_t i = 0; i < kPickWaves; i++) {
+            const uint32_t x = __builtin_amdgcn_readfirstlane(v[i / 4][i % 4]);
+            before += i < wave ? x : 0;
+            all += x;
+        }
     }
-    return r;
-}
+};
 
 __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
     __shared__ uint32_t bins[kCopies][kBins];
-    __shared__ uint32_t sums[kPickWaves];
+    __shared__ __attribute__((aligned(16))) uint32_t sums[2][kPickWaves];
     __shared__ uint32_t chosen[2];
-    const uint32_t s = blockIdx.x / a.weight_heads, t = threadIdx.x;
+    const uint32_t s = blockIdx.x / a.weight_heads, t = threadIdx.x, lane = t % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(t / kWave);
     const int32_t len = a.lens[s];
     const bool good = len >= 0 && len <= a.max_len;
     const uint32_t n = good ? (uint32_t)len : 0;
@@ -618,82 +622,113 @@ __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
         }
         return;
     }
-    // the tokens between the first and the recent ones; `left` of them stay
-    const uint32_t lo = a.first, hi = n - a.recent;
-    const uint32_t left = a.budget - a.first - a.recent;
-    uint32_t prefix = 0, mask = 0, take = left;  // of keys that match in `mask`, the top `take`
-    if (left > 0) {
-        for (int32_t shift = 32 - (int32_t)kDigit; shift > -(int32_t)kDigit; shift -= kDigit) {
-            const uint32_t low = shift > 0 ? (uint32_t)shift : 0;
-            const uint32_t width = shift > 0 ? kDigit : kDigit + (uint32_t)shift;
-            for (uint32_t i = t; i < kCopies * kBins; i += kPickThreads) (&bins[0][0])[i] = 0;
-            __syncthreads();
-            for (uint32_t i = lo + t; i < hi; i += kPickThreads) {
-                const uint32_t key = rank_of(w[i]);
-                if ((key & mask) == prefix)
-                    atomicAdd(&bins[t % kCopies][key >> low & ((1u << width) - 1)], 1u);
-            }
-            __syncthreads();
-            // thread t has bins kBins - 2 t - 2 and the one above it
-            uint32_t own[2];
+    // A wave's weights of a piece: rounds of 64 consecutive ones.
+    const uint32_t rounds = n < kPiece ? (n + kPickThreads - 1) / kPickThreads : kHold;
+    const uint32_t mine = (wave * rounds) * kWave + lane;
+    const uint32_t lo = a.first, hi = n - a.recent;  // the tokens that may go
+    float x[kHold];
+    uint32_t key[kHold];
+    const auto each = [&](auto f) {
 #pragma unroll
-            for (uint32_t i = 0; i < 2; i++) {
-                own[i] = 0;
-#pragma unroll
-                for (uint32_t c = 0; c < kCopies; c++) own[i] += bins[c][kBins - 1 - 2 * t - i];
+        for (uint32_t k = 0; k < kHold; k++)
+            if (k < rounds) f(k);
+    };
+    const auto load = [&](uint32_t base) {
+        each([&](uint32_t k) {
+            const uint32_t i = base + mine + k * kWave;
+            x[k] = 0;
+            if (i < n) x[k] = *(const SZ_GLOBAL float*)(w + i);
+        });
+        each([&](uint32_t k) {
+            const uint32_t i = base + mine + k * kWave;
+            key[k] = i - lo < hi - lo ? key_of(x[k]) : i < n ? kSafe : 0;
+        });
+    };
+    const bool whole = n <= kPiece;
+    if (whole) load(0);
+
+    uint32_t prefix = 0, take = stay;  // of the keys that begin with prefix, the top `take`
+    for (int32_t shift = 32 - (int32_t)kDigit; shift > -(int32_t)kDigit; shift -= kDigit) {
+        const uint32_t low = shift > 0 ? (uint32_t)shift : 0;
+        const uint32_t width = shift > 0 ? kDigit : kDigit + (uint32_t)shift;
+        const uint32_t above_digit = low + width;  // bits from here on are settled
+        for (uint32_t i = t; i < kCopies * kBins; i += kPickThreads) (&bins[0][0])[i] = 0;
+        lds_barrier();
+        for (uint32_t base = 0; base < n; base += kPiece) {
+            if (!whole) load(base);
+            uint32_t* const copy = bins[lane % kCopies];
+            if (above_digit >= 32) {  // the first digit: every key counts
+                each([&](uint32_t k) { atomicAdd(copy + (key[k] >> low), 1u); });
+            } else {
+                const uint32_t settled = prefix >> above_digit;
+                const uint32_t digit = (1u << width) - 1;
+                each([&](uint32_t k) {
+                    if (key[k] >> above_digit == settled)
+                        atomicAdd(copy + (key[k] >> low & digit), 1u);
+                });
             }
-            const uint32_t above = group_scan(own[0] + own[1], sums).before;
-            if (above < take && above + own[0] + own[1] >= take) {
-                const bool first = above + own[0] >= take;
-                chosen[0] = kBins - 1 - 2 * t - (first ? 0 : 1);
-                chosen[1] = take - above - (first ? 0 : own[0]);
-            }
-            __syncthreads();
-            prefix |= chosen[0] << low;
-            mask |= ((1u << width) - 1) << low;
-            take = chosen[1];
-            __syncthreads();
         }
+        lds_barrier();
+        // thread t has bins kBins - 2 t - 2 and the one above it
+        uint32_t own[2];
+#pragma unroll
+        for (uint32_t i = 0; i < 2; i++) {
+            own[i] = 0;
+#pragma unroll
+            for (uint32_t c = 0; c < kCopies; c++) own[i] += bins[c][kBins - 1 - 2 * t - i];
+        }
+        const uint32_t upto = wave_scan(own[0] + own[1]);
+        if (lane == kWave - 1) sums[0][wave] = upto;
+        lds_barrier();
+        const uint32_t above = upto - own[0] - own[1] + Before(sums[0], wave).before;
+        if (above < take && above + own[0] + own[1] >= take) {
+            const bool first = above + own[0] >= take;
+            chosen[0] = kBins - 1 - 2 * t - (first ? 0 : 1);
+            chosen[1] = take - above - (first ? 0 : own[0]);
+        }
+        lds_barrier();
+        prefix = above_digit >= 32 ? chosen[0] << low
+                                   : (prefix >> above_digit << above_digit) | chosen[0] << low;
+        take = chosen[1];
     }
     // every key above `prefix` stays, and of those equal to it the first `take`
-    uint32_t base = 0, ties = 0;
-    for (uint32_t i0 = 0; i0 < n; i0 += kRun * kPickThreads) {
-        const uint32_t first = i0 + kRun * t;
-        float x[kRun];
-        uint32_t sure = 0, equal = 0;
-#pragma unroll
-        for (uint32_t e = 0; e < kRun; e++) {
-            const uint32_t i = first + e;
-            x[e] = 0;
-            if (i >= n) continue;
-            x[e] = w[i];
-            if (i < lo || i >= hi) {
-                sure |= 1u << e;
-            } else if (left > 0) {
-                const uint32_t key = rank_of(x[e]);
-                if (key > prefix) sure |= 1u << e;
-                if (key == prefix) equal |= 1u << e;
-            }
+    uint32_t base_sure = 0, base_ties = 0;
+    for (uint32_t base = 0; base < n; base += kPiece) {
+        if (!whole) load(base);
+        uint32_t sures = 0, ties = 0;
+        each([&](uint32_t k) {
+            sures += __popcll(__ballot(key[k] > prefix));
+            ties += __popcll(__ballot(key[k] == prefix));
+        });
+        lds_barrier();  // (sums have been read)
+        if (lane == 0) {
+            sums[0][wave] = sures;
+            sums[1][wave] = ties;
         }
-        const Scan r = group_scan(__popc(sure) | __popc(equal) << 16, sums);
-        uint32_t at = base + (r.before & 0xFFFFu);
-        uint32_t rank = ties + (r.before >> 16);
-        at += rank < take ? rank : take;
-#pragma unroll
-        for (uint32_t e = 0; e < kRun; e++) {
-            bool stays = sure >> e & 1;
-            if (equal >> e & 1) {
-                stays = rank < take;
-                rank++;
+        lds_barrier();
+        const Before more_before(sums[0], wave), same_before(sums[1], wave);
+        uint32_t at = base_sure + more_before.before, rank = base_ties + same_before.before;
+        base_sure += more_before.all;
+        base_ties += same_before.all;
+        each([&](uint32_t k) {
+            // (ties that stay counted in, as far as they go)
+            const uint64_t more = __ballot(key[k] > prefix), same = __ballot(key[k] == prefix);
+            uint64_t stays = more;
+            uint32_t place = at + (rank < take ? rank : take);
+            if (same != 0 && rank < take) {
+                const uint32_t before = __builtin_amdgcn_mbcnt_hi(
+                    (uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+                stays |= __ballot(key[k] == prefix && rank + before < take);
             }
-            if (stays) {
-                kept[at] = (int32_t)(first + e);
-                out[at] = x[e];
-                at++;
+            if (stays >> lane & 1) {
+                place += __builtin_amdgcn_mbcnt_hi(
+                    (uint32_t)(stays >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)stays, 0));
+                kept[place] = (int32_t)(base + mine + k * kWave);
+                out[place] = x[k];
             }
-        }
-        base += r.all & 0xFFFFu;
-        ties += r.all >> 16;
+            at += __popcll(more);
+            rank += __popcll(same);
+        });
     }
 }
 
