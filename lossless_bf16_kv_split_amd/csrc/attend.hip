@@ -531,9 +531,10 @@ struct Ragged {
         const uint64_t to = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32))
                                 << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
         const uint32_t n = last - jb > 16 ? 15 : (uint32_t)(last - jb) - 1;
-        const uint32_t bytes = some ? 2 * (n * (uint32_t)r.token_stride + dim) : 0;
-        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(some ? to : 0), 0, bytes,
-                                                 kBufferFlags);
+        const uint32_t bytes = __builtin_amdgcn_readfirstlane(
+            some ? 2 * (n * (uint32_t)r.token_stride + dim) : 0);
+        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(bytes != 0 ? to : 0), 0,
+                                                 bytes, kBufferFlags);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(int32_t jb) const {
         return rows(e.k, head, e.key_dim, jb);
@@ -546,18 +547,27 @@ struct Ragged {
     }
 };
 
-// Bytes of LDS: K of two steps of 64 keys, V of three; and of two steps 64
-// elements of the keys' rotary part, in rows of their own.
-template <int DP, bool ROTARY>
-constexpr uint32_t kChunkLds = 5 * 64 * 2 * DP + (ROTARY ? 2 * 64 * 128 : 0);
-static_assert(2 * kChunkLds<128, false> <= 160 * 1024, "two workgroups a CU");
-static_assert(kChunkLds<256, false> <= 160 * 1024, "");
+// Bytes of LDS: K of two steps of 64 keys, V of three (or two), and of two
+// steps 64 elements of the keys' rotary part, in rows of their own.
+template <int DP, bool ROTARY, int VS>
+constexpr uint32_t kChunkLds = (2 + VS) * 64 * 2 * DP + (ROTARY ? 2 * 64 * 128 : 0);
+static_assert(2 * kChunkLds<128, false, 3> <= 160 * 1024, "two workgroups a CU");
+static_assert(kChunkLds<256, false, 3> <= 160 * 1024, "");
+static_assert(2 * kChunkLds<128, true, 2> <= 160 * 1024, "two workgroups a CU");
 
 template <int DP, int QB, int CAP, bool SHARED, class Source>
 __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                                            const Score& score, uint8_t* ws, const Part& part,
                                            uint32_t kv, uint8_t* lds, Source source) {
     constexpr bool kRotary = Source::kRotary;
+    // With the rotary part there is room for two workgroups only if V has two
+    // buffers.  A step's values are then asked for when it begins, into those
+    // of the step before the last, and waited for in its middle, a barrier more
+    // (four chunks of 20 heads, 128 rows: 98.7 us, 113 with three buffers and
+    // one workgroup; a prompt of 8192 tokens of 32 heads 618, 753, and 638 with
+    // 256 rows).  Shared out, a tile takes more registers than half of them.
+    constexpr bool kLate = kRotary && !SHARED;
+    constexpr uint32_t kVs = kLate ? 2 : 3;
     constexpr int kKeys = 64;
     constexpr uint32_t kRow = 2 * DP;             // bytes of a row in LDS
     constexpr uint32_t kBuffer = kKeys * kRow;    // K or V of a step
@@ -623,18 +633,25 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SZ_LDS uint8_t*)lds;
-    constexpr uint32_t kRotaryAt = 5 * kBuffer;  // of LDS
+    constexpr uint32_t kRotaryAt = (2 + kVs) * kBuffer;  // of LDS
     source.look_up(first + 16 * (int32_t)wave, t.lo);
-    // K and V of the step at j to their buffers, the next step's block looked up
-    const auto fetch_step = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer) {
+    // K and V of the step at j to their buffers
+    const auto fetch_keys = [&](int32_t j, uint32_t buffer) {
         const int32_t jb = j + 16 * (int32_t)wave;
-        load_to_lds<kLoads>(source.keys(jb), k_off, lds0 + k_buffer * kBuffer + wave * 16 * kRow);
-        load_to_lds<kLoads>(source.values(jb), v_off,
-                            lds0 + (2 + v_buffer) * kBuffer + wave * 16 * kRow);
+        load_to_lds<kLoads>(source.keys(jb), k_off, lds0 + buffer * kBuffer + wave * 16 * kRow);
         if constexpr (kRotary)
             load_to_lds<2>(source.rotary(jb), r_off,
-                           lds0 + kRotaryAt + k_buffer * 8192 + wave * 2048);
-        source.look_up(jb + kKeys, t.lo);
+                           lds0 + kRotaryAt + buffer * 8192 + wave * 2048);
+    };
+    const auto fetch_values = [&](int32_t j, uint32_t buffer) {
+        load_to_lds<kLoads>(source.values(j + 16 * (int32_t)wave), v_off,
+                            lds0 + (2 + buffer) * kBuffer + wave * 16 * kRow);
+    };
+    // both, and the next step's block looked up
+    const auto fetch_step = [&](int32_t j, uint32_t k_buffer, uint32_t v_buffer) {
+        fetch_keys(j, k_buffer);
+        fetch_values(j, v_buffer);
+        source.look_up(j + kKeys + 16 * (int32_t)wave, t.lo);
     };
 
     // LDS addresses of this lane's reads.  Slice s of K is at its first
@@ -927,43 +944,59 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     if (in1 > steps) in1 = steps;
     if (in0 >= in1) in0 = in1 = steps;
     if (SHARED) arrived();  // (every wave is done with the part before)
-    if (steps > 0) fetch_step(first, 0, 0);
+    if (kLate) fetch_keys(first, 0);
+    else if (steps > 0) fetch_step(first, 0, 0);
     // (waves without rows, of a token among chunks, leave LDS to the others:
     // 24 tokens and two chunks of 833, 256 elements, capped, 137 -> 132 us;
     // whole tiles run 2% slower with the test)
     const bool works = !SHARED || 32 * QB * (int32_t)wave < t.rows;
     int32_t x = 0;
-    uint32_t vb = 0;  // x % 3
+    uint32_t vb = 0;  // x % kVs
     const auto begin_step = [&] {
         arrived();
-        fetch_step(first + (x + 1) * kKeys, (x + 1) & 1, vb == 2 ? 0 : vb + 1);
+        if constexpr (kLate) {
+            fetch_values(first + x * kKeys, vb);
+            fetch_keys(first + (x + 1) * kKeys, (x + 1) & 1);
+        } else {
+            fetch_step(first + (x + 1) * kKeys, (x + 1) & 1, vb == kVs - 1 ? 0 : vb + 1);
+        }
+    };
+    // the step's values have arrived from every wave (the next keys, whose
+    // loads came last, may still be under way)
+    const auto values_here = [&] {
+        if constexpr (kLate) {
+            static_assert(!kLate || kLoads + 2 == 6, "");
+            asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
     };
     const auto end_step = [&] {
         x++;
-        vb = vb == 2 ? 0 : vb + 1;
+        vb = vb == kVs - 1 ? 0 : vb + 1;
     };
     for (int pass = 0; pass < 2; pass++) {
         const int32_t stop = pass == 0 ? in0 : steps;
         while (x < stop) {
             const int32_t j = first + x * kKeys;
             begin_step();
-            if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1, vb, vb == 0 ? 2 : vb - 1);
+            values_here();
+            if (j < w_hi && j + kKeys > w_lo) rim(j, x & 1, vb, vb == 0 ? kVs - 1 : vb - 1);
             end_step();
         }
         if (pass == 1 || in0 == in1) continue;
         Half even, uneven;
         uint32_t va = v_lane + vb * kBuffer;
         begin_step();
-        if (works) {
-            ahead(even, k_lane + (x & 1) * kBuffer);
+        if (works) ahead(even, k_lane + (x & 1) * kBuffer);
+        values_here();
+        if (works)
             inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
-        }
         end_step();
         while (x < in1) {
             const uint32_t ka = k_lane + (x & 1) * kBuffer;
             begin_step();
+            if (works) inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
+            values_here();
             if (works) {
-                inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
                 va = v_lane + vb * kBuffer;
                 inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
             }
@@ -1022,7 +1055,7 @@ template <int DP, int QB, int CAP, bool SHARED>
 __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_attend_chunk(
     Attend a, AttendPlan p, Score score, uint8_t* ws) {
     const uint32_t kv = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<DP, false>];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<DP, false, 3>];
     Walk<SHARED> walk(a, p);
     Part part;
     // whole tiles: the last ones of a prompt see the most keys and go first
@@ -1033,13 +1066,12 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 }
 
 // The same over keys and values expanded from latents: 192 elements of keys,
-// 128 of values.  One workgroup a CU.
-template <int QB, bool SHARED>
-__global__ __launch_bounds__(kThreads, 1) void k_attend_expanded(Attend a, Expanded e,
-                                                                 AttendPlan p, Score score,
-                                                                 uint8_t* ws) {
+// 128 of values.
+template <bool SHARED>
+__global__ __launch_bounds__(kThreads, SHARED ? 1 : 2) void k_attend_expanded(
+    Attend a, Expanded e, AttendPlan p, Score score, uint8_t* ws) {
     const uint32_t head = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<128, true>];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<128, true, SHARED ? 3 : 2>];
     Walk<SHARED> walk(a, p);
     Part part;
     if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
@@ -1048,8 +1080,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_expanded(Attend a, Expan
         const int64_t start = __builtin_amdgcn_readfirstlane(e.key_starts[part.t.seq]);
         const int32_t len = __builtin_amdgcn_readfirstlane(a.batch.lens[part.t.seq]);
         const bool good = start >= 0 && start + len <= e.n_keys;
-        chunk_part<128, QB, kUncapped, SHARED>(a, p, score, ws, part, head, lds,
-                                               Ragged(e, start, head, good ? part.last : part.first));
+        chunk_part<128, 1, kUncapped, SHARED>(a, p, score, ws, part, head, lds,
+                                              Ragged(e, start, head, good ? part.last : part.first));
     } while (walk.next(a, p, index, part));
 }
 
@@ -1187,17 +1219,18 @@ uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uin
 }
 
 // Keys and values expanded from latents: a head is a KV head of its own.
-// Tiles of 256 rows where sequences have that many on average, of 128
-// otherwise; whole where they fill the chip, one workgroup a CU.
+// Tiles of 128 rows, whole where there is one for each CU (1024 tokens of 16
+// heads on 8192 keys, 128 tiles: 159 us whole, 123 shared out) or with few keys
+// (1024 of 16 heads on as many keys: 28 and 34; 512 of 5 on 2048: 46 and 28).
 AttendPlan plan_expanded(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len) {
     AttendPlan p{};
     p.group = 1;
-    p.tile_log2 = n_tokens >= 192 * n_seqs && (n_tokens >> 8) * heads >= kCus ? 8 : 7;
+    p.tile_log2 = 7;
     p.tiles = (uint32_t)((n_tokens >> p.tile_log2) + n_seqs);
     const uint64_t full = n_tokens >> p.tile_log2;
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * heads;
     const bool whole = n_seqs > kShareSeqs || heads > kCus || groups >= kCus ||
-                       p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= 512;
+                       p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= 1024;
     p.shares = whole ? 0 : (uint32_t)(kCus / heads);
     return p;
 }
@@ -1217,14 +1250,8 @@ hipError_t launch_attend_expanded(const Attend& a, const Expanded& e, uint8_t* w
         plan_expanded(a.q.heads, a.batch.n_seqs, a.batch.n_tokens, (uint64_t)a.max_len);
     const Score score = score_of(a);
     const dim3 grid((p.shares != 0 ? p.shares : p.tiles) * a.cache.kv_heads), block(kThreads);
-    if (p.tile_log2 == 8 && p.shares != 0)
-        k_attend_expanded<2, true><<<grid, block, 0, stream>>>(a, e, p, score, ws);
-    else if (p.tile_log2 == 8)
-        k_attend_expanded<2, false><<<grid, block, 0, stream>>>(a, e, p, score, ws);
-    else if (p.shares != 0)
-        k_attend_expanded<1, true><<<grid, block, 0, stream>>>(a, e, p, score, ws);
-    else
-        k_attend_expanded<1, false><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    if (p.shares != 0) k_attend_expanded<true><<<grid, block, 0, stream>>>(a, e, p, score, ws);
+    else k_attend_expanded<false><<<grid, block, 0, stream>>>(a, e, p, score, ws);
     const hipError_t st = hipGetLastError();
     if (st != hipSuccess || p.shares == 0) return st;
     const dim3 join(p.tiles * a.cache.kv_heads * join_pieces(p));
