@@ -404,47 +404,48 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_latent(Attend a, AttendP
     } while (walk.next(a, p, index, part));
 }
 
-// Joins the parts of the tiles that were cut: a wave a row, eight elements a
-// lane; the parts' maxima and sums 64 at a time, one a lane.
+// Joins the parts of the tiles that were cut, eight elements a lane; the parts'
+// maxima and sums 64 at a time, one a lane.  A row is one wave's, or (TOGETHER,
+// where tiles have many parts) the four waves of a workgroup take a quarter
+// of its parts each.
+template <bool TOGETHER>
 __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p, uint8_t* ws) {
+    constexpr uint32_t kRows = TOGETHER ? 1 : kWaves;
+    __shared__ float sums[TOGETHER ? kWaves : 1][8][kWave];
+    __shared__ float ml[TOGETHER ? kWaves : 1][2];
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t pieces = (1u << p.tile_log2) / kWaves;
+    const uint32_t pieces = (1u << p.tile_log2) / kRows;
     const uint32_t number = blockIdx.x / pieces;
     const Shares shares(a, p);
     if (number >= Shares::from_lane(shares.tiles1, kWave - 1)) return;
     const Shares::Found f = shares.find(a, p, true, number);
     const uint32_t at = number - f.tiles0;
     const uint32_t step = f.steps0 + at * f.x.steps;
-    const uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
+    uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     if (from == upto) return;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
-    const int32_t r = (int32_t)(blockIdx.x % pieces * kWaves + wave);
+    const int32_t r = (int32_t)(blockIdx.x % pieces * kRows + (TOGETHER ? 0 : wave));
     if (r >= t.rows) return;
+    if (TOGETHER) {
+        const uint32_t each = (upto - from + kWaves) / kWaves, past = upto + 1;
+        from += wave * each;
+        upto = from + each < past ? from + each : past;  // (from here: past the last)
+    } else {
+        upto++;
+    }
     const Row w = find_row(a, p, t, r);
     const uint32_t e = 8 * lane;
     const bool on = e < a.value_dim;
     const uint64_t stride = (uint64_t)a.value_dim << p.tile_log2;
     float top = kNoKey, total = 0, x[8] = {};
-    for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
-        const uint32_t parts = upto - i0 + 1 < kWave ? upto - i0 + 1 : kWave;
+    for (uint32_t i0 = from; i0 < upto; i0 += kWave) {
+        const uint32_t parts = upto - i0 < kWave ? upto - i0 : kWave;
         const Partial u = partial_of(ws, a, p, 0, i0 + number);
-        float m = kNoKey, l = 0;
-        if (lane < parts) {
-            m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
-            l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
-        }
-        const float most = wave_max(fmaxf(m, top));
-        const float weight = __builtin_amdgcn_exp2f(m - most);
-        const float keep = __builtin_amdgcn_exp2f(top - most);
-        top = most;
-        total = total * keep + wave_sum(l * weight);
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] *= keep;
         const float* o = u.o + (uint64_t)r * a.value_dim + e;
-        constexpr uint32_t kBatch = 4;
-        for (uint32_t s0 = 0; s0 < parts; s0 += kBatch) {
-            f32x4 v[kBatch][2];
+        constexpr uint32_t kBatch = 8;
+        f32x4 v[kBatch][2];
+        const auto read = [&](uint32_t s0) {
 #pragma unroll
             for (uint32_t k = 0; k < kBatch; k++)
 #pragma unroll
@@ -453,6 +454,22 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
                     if (on && s0 + k < parts)
                         v[k][i] = *(const SZ_GLOBAL f32x4*)(o + (s0 + k) * stride + 4 * i);
                 }
+        };
+        float m = kNoKey, l = 0;
+        if (lane < parts) {
+            m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];
+            l = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r) + 1];
+        }
+        read(0);  // (under way while the weights are made)
+        const float most = wave_max(fmaxf(m, top));
+        const float weight = __builtin_amdgcn_exp2f(m - most);
+        const float keep = __builtin_amdgcn_exp2f(top - most);
+        top = most;
+        total = total * keep + wave_sum(l * weight);
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] *= keep;
+        for (uint32_t s0 = 0; s0 < parts; s0 += kBatch) {
+            if (s0 > 0) read(s0);
 #pragma unroll
             for (uint32_t k = 0; k < kBatch; k++) {
                 const float by = __int_as_float(
@@ -461,6 +478,25 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
                 for (int i = 0; i < 8; i++)
                     if (s0 + k < parts) x[i] = fmaf(v[k][i / 4][i % 4], by, x[i]);
             }
+        }
+    }
+    if constexpr (TOGETHER) {
+        ml[wave][0] = top;
+        ml[wave][1] = total;
+#pragma unroll
+        for (int i = 0; i < 8; i++) sums[wave][i][lane] = x[i];
+        __syncthreads();
+        if (wave != 0) return;
+        top = fmaxf(fmaxf(ml[0][0], ml[1][0]), fmaxf(ml[2][0], ml[3][0]));
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kWaves; k++) {
+            const float weight = __builtin_amdgcn_exp2f(ml[k][0] - top);
+            total = fmaf(ml[k][1], weight, total);
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[i] = fmaf(sums[k][i][lane], weight, x[i]);
         }
     }
     const float inv = inverse(total);
@@ -478,6 +514,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
 // otherwise (attend_parts.h).
 constexpr uint64_t kManyTiles = 1024;
 constexpr uint64_t kWholeKeys = 256;
+constexpr uint32_t kTogether = 8;  // shares a tile from which on four waves join a row
 constexpr uint64_t kShareSeqs = 1024;
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 
@@ -534,8 +571,12 @@ hipError_t launch_attend_latent(const Attend& a, uint8_t* ws, hipStream_t stream
     else go<512, 576>(a, p, by, ws, stream);
     if (hipError_t e = hipGetLastError()) return e;
     if (p.shares == 0) return hipSuccess;
-    const dim3 grid(p.tiles * ((1u << p.tile_log2) / kWaves));
-    k_latent_join<<<grid, dim3(kThreads), 0, stream>>>(a, p, ws);
+    const dim3 block(kThreads);
+    if (p.shares >= kTogether * p.tiles)
+        k_latent_join<true><<<dim3(p.tiles << p.tile_log2), block, 0, stream>>>(a, p, ws);
+    else
+        k_latent_join<false>
+            <<<dim3((p.tiles << p.tile_log2) / kWaves), block, 0, stream>>>(a, p, ws);
     return hipGetLastError();
 }
 
