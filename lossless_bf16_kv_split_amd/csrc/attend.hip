@@ -92,6 +92,7 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
     p.alone = p.few() ? (uint32_t)(kCus / c.kv_heads) : 0;
     p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
+    p.extra = 0;
     return p;
 }
 

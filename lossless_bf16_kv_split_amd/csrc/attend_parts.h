@@ -88,6 +88,7 @@ struct AttendPlan {
     uint32_t shares;     // workgroups that share it out for a KV head; 0: whole tiles
     uint32_t alone;      // up to so many steps in all, shares of one step
     bool wide;           // few rows, whole tiles, a CU each: eight waves
+    uint32_t extra;      // steps that a tile is counted as more than its keys make
     __host__ __device__ bool few() const { return tile_log2 == 4; }
 };
 
@@ -159,7 +160,7 @@ struct Shares {
     struct Load {
         Seq q;
         uint32_t tiles;   // of the sequence, 0 where it is faulty or has no rows
-        uint32_t steps;   // of each of its tiles, at least 1
+        uint32_t steps;   // of each of its tiles, at least 1, `extra` ones first
         int32_t from;     // the key of step 0
     };
     uint32_t each;
@@ -192,7 +193,7 @@ struct Shares {
         if (a.causal && a.window != 0 && (int64_t)c0 + 1 > (int64_t)a.window)
             x.from = (c0 + 1 - (int32_t)a.window) & ~31;
         x.steps = (uint32_t)(x.q.len - x.from + kStep - 1) / kStep;
-        x.steps = x.steps == 0 ? 1 : x.steps;
+        x.steps = (x.steps == 0 ? 1 : x.steps) + p.extra;
         return x;
     }
 
@@ -340,6 +341,8 @@ struct Walk<false> {
         return false;
     }
 };
+// A tile begins with `extra` steps that have no keys, which stand for what it
+// costs to begin one: a border among them counts as one before the tile.
 template <>
 struct Walk<true> {
     uint32_t step, end;
@@ -349,34 +352,33 @@ struct Walk<true> {
         const Shares shares(a, p);
         step = index * shares.quota;
         end = step + shares.quota < shares.total ? step + shares.quota : shares.total;
-        if (step >= end) return false;
-        take(shares, a, p, index, part);
-        return true;
+        return step < end && take(shares, a, p, index, part);
     }
     // (the sums are made anew: they would hold registers through the part)
     __device__ __forceinline__ bool next(const Attend& a, const AttendPlan& p, uint32_t index,
                                          Part& part) {
-        if (step >= end) return false;
-        take(Shares(a, p), a, p, index, part);
-        return true;
+        return step < end && take(Shares(a, p), a, p, index, part);
     }
-    __device__ __forceinline__ void take(const Shares& shares, const Attend& a,
+    __device__ __forceinline__ bool take(const Shares& shares, const Attend& a,
                                          const AttendPlan& p, uint32_t index, Part& part) {
         const Shares::Found f = shares.find(a, p, false, step);
         const uint32_t at = (step - f.steps0) / f.x.steps;
         const uint32_t base = f.steps0 + at * f.x.steps, stop = base + f.x.steps;
+        if (end < stop && end - base <= p.extra) return false;
         const uint32_t upto = stop < end ? stop : end;
+        const uint32_t done = step - base <= p.extra ? 0 : step - base - p.extra;
         part.t = make_tile(a, p, f.seq, f.tiles0 + at, f.x.q, (int64_t)at << p.tile_log2);
         // (a part begins at one of the steps, even where a window shows the
         // tile's rows fewer keys than the sequence's first one: whole steps
         // up to the part's end, which masks nothing)
         const uint32_t skip = (uint32_t)(part.t.from - f.x.from) / kStep;
-        part.first = f.x.from + (int32_t)((step - base > skip ? step - base : skip) * kStep);
-        const int32_t last = f.x.from + (int32_t)((upto - base) * kStep);
+        part.first = f.x.from + (int32_t)((done > skip ? done : skip) * kStep);
+        const int32_t last = f.x.from + (int32_t)((upto - base - p.extra) * kStep);
         part.last = last < part.t.hi ? last : part.t.hi;
-        part.alone = step == base && upto == stop;
+        part.alone = done == 0 && upto == stop;
         part.slot = index + part.t.number;
         step = upto;
+        return true;
     }
 };
 

@@ -18,13 +18,21 @@ constexpr uint64_t kCus = 256;
 // Two forms.  Few rows a sequence (a token's heads, drafts): k_weigh_few, a
 // wave streams blocks of 32 keys against the rows that it holds.  Many:
 // k_weigh_tile, a wave holds 64 keys and the rows pass by, staged in LDS for
-// the four waves of a workgroup; `splits` workgroups share a tile's rows.
+// the four waves of a workgroup; up to `splits` workgroups share a tile's rows,
+// as many as the sequence has kSplitRows of them (the sums then meet in the
+// workspace).
+constexpr uint64_t kSplitRows = 256;
+constexpr uint64_t kSplitBytes = uint64_t{1} << 28;  // of workspace, no more
 struct WeighPlan {
     uint32_t group;   // G
     bool few;
     uint32_t keys;    // of a workgroup
     uint32_t chunks;  // of so many keys up to max_len
     uint32_t splits;
+    __device__ uint32_t splits_of(uint64_t rows) const {
+        const uint64_t most = (rows + kSplitRows - 1) / kSplitRows;
+        return most < 1 ? 1 : most < splits ? (uint32_t)most : splits;
+    }
 };
 constexpr int kBlocks = 4;  // of 16 keys, a wave's of a tile
 constexpr int kWaveKeys = 16 * kBlocks;
@@ -283,14 +291,16 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
     if (!seq.good || w.tile >= seq.len) return;
     const int32_t key0 = w.tile + kWaveKeys * (int32_t)wave;
     const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
+    const uint32_t splits = p.splits_of((uint64_t)count * p.group);
+    if (w.split >= splits) return;
     const uint32_t dim = a.cache.head_dim;
 
     // the rows of the tokens that see any of the workgroup's keys, in steps
     const Tokens t(a, count, c0, w.tile, (int32_t)kTileKeys);
     const uint32_t row_lo = (uint32_t)t.lo * p.group, row_hi = (uint32_t)t.hi * p.group;
     const uint64_t all = (row_hi - row_lo + kStepRows - 1) / kStepRows;
-    const uint32_t step0 = (uint32_t)(all * w.split / p.splits);
-    const uint32_t steps = (uint32_t)(all * (w.split + 1) / p.splits) - step0;
+    const uint32_t step0 = (uint32_t)(all * w.split / splits);
+    const uint32_t steps = (uint32_t)(all * (w.split + 1) / splits) - step0;
 
     float acc[16];  // keys 16 b + 4 h + i of key0
 #pragma unroll
@@ -476,7 +486,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
     const int32_t j = key0 + 16 * (int32_t)(n / 4) + 4 * (int32_t)h + (int32_t)(n % 4);
     if (j >= seq.len) return;
     const uint64_t line = (uint64_t)w.s * a.cache.kv_heads + w.kv;
-    if (p.splits > 1) {
+    if (splits > 1) {
         ws[((uint64_t)w.split * a.batch.n_seqs * a.cache.kv_heads + line) * (uint64_t)a.max_len +
            (uint32_t)j] = sum;
     } else {
@@ -494,10 +504,12 @@ __global__ __launch_bounds__(kThreads) void k_weigh_join(Weigh a, WeighPlan p, c
     const Seq seq = load_seq(a.batch, s, a.max_len);
     if (!seq.good || j >= (uint32_t)seq.len) return;
     const int32_t c0 = seq.len - (seq.end - seq.begin);
+    const uint32_t splits = p.splits_of((uint64_t)(seq.end - seq.begin) * p.group);
+    if (splits == 1) return;  // (written already)
     const uint64_t lines = (uint64_t)a.batch.n_seqs * a.cache.kv_heads;
     float total = 0;
 #pragma unroll 8
-    for (uint32_t i = 0; i < p.splits; i++) total += ws[(i * lines + line) * (uint64_t)a.max_len + j];
+    for (uint32_t i = 0; i < splits; i++) total += ws[(i * lines + line) * (uint64_t)a.max_len + j];
     const uint64_t at = line * a.pitch + j;
     if (a.before != nullptr && (int32_t)j < c0) total = fmaf(a.keep, a.before[at], total);
     a.weights[at] = total;
@@ -512,8 +524,8 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
     p.splits = 1;
     if (p.few) {
         // as many keys a workgroup as leave four of them to a CU, 128 (a block a
-        // wave) to 1024
-        uint64_t keys = 1024;
+        // wave) to 512
+        uint64_t keys = 512;
         while (keys > 128 && (max_len + keys - 1) / keys * lines < 4 * kCus) keys /= 2;
         p.keys = (uint32_t)keys;
     } else {
@@ -521,12 +533,17 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
     }
     p.chunks = (uint32_t)((max_len + p.keys - 1) / p.keys);
     if (!p.few) {
-        // rows among so many workgroups that the causal ones' uneven shares even
-        // out, 256 rows each at least
-        const uint64_t groups = p.chunks * lines;
-        uint64_t splits = 8 * kCus / groups;
-        const uint64_t most = rows / n_seqs / 256;
+        // Rows among so many workgroups that the causal ones' uneven shares even
+        // out, or one long sequence among short ones fills the chip: by the
+        // tiles of those sequences that can have 2048 rows (a prompt of 4096
+        // tokens, 128 tiles: 96 us in 12 parts each, 95 in 16, 100 in 24; 500
+        // tokens beside 24 single ones, 256 elements, capped: 193 us whole).
+        const uint64_t long_seqs = rows / 2048 < 1 ? 1 : rows / 2048 < n_seqs ? rows / 2048 : n_seqs;
+        uint64_t splits = 8 * kCus / (p.chunks * c.kv_heads * long_seqs);
+        const uint64_t most = (rows + kSplitRows - 1) / kSplitRows;
         splits = splits < most ? splits : most;
+        const uint64_t fits = kSplitBytes / (4 * lines * max_len);
+        splits = splits < fits ? splits : fits;
         p.splits = (uint32_t)(splits < 1 ? 1 : splits);
     }
     return p;

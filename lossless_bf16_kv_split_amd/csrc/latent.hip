@@ -422,7 +422,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
     const Shares::Found f = shares.find(a, p, true, number);
     const uint32_t at = number - f.tiles0;
     const uint32_t step = f.steps0 + at * f.x.steps;
-    uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
+    uint32_t from = (step + p.extra) / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     if (from == upto) return;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
     const int32_t r = (int32_t)(blockIdx.x % pieces * kRows + (TOGETHER ? 0 : wave));
@@ -515,6 +515,10 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
 constexpr uint64_t kManyTiles = 1024;
 constexpr uint64_t kWholeKeys = 256;
 constexpr uint32_t kTogether = 8;  // shares a tile from which on four waves join a row
+// What beginning a tile costs, in steps (48 tokens of 128 heads: 104 us without, 96
+// with 2, 94 with 3; drafts of 3 tokens 37, 31, 31; 32 tokens of one sequence on
+// 8192 keys 89, 101, 94).
+constexpr uint32_t kExtra = 3;
 constexpr uint64_t kShareSeqs = 1024;
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 
@@ -528,9 +532,10 @@ AttendPlan plan_latent(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint6
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     const uint64_t full = rows >> p.tile_log2;
     const bool whole = n_seqs > kShareSeqs || (full > n_seqs ? full : n_seqs) >= kManyTiles ||
-                       p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= kWholeKeys;
+                       p.tiles * (max_len / kStep + 2 + kExtra) >= kMostSteps || max_len <= kWholeKeys;
     p.shares = whole ? 0 : (uint32_t)(kCus / halves(p));
     p.alone = p.shares;
+    p.extra = kExtra;
     return p;
 }
 
