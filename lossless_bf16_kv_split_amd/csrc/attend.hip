@@ -92,7 +92,6 @@ AttendPlan plan_attend(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64
     p.shares = whole ? 0 : (uint32_t)(resident / c.kv_heads);
     p.alone = p.few() ? (uint32_t)(kCus / c.kv_heads) : 0;
     p.wide = p.few() && whole && groups <= kCus && c.head_dim <= 128;
-    p.extra = 0;
     return p;
 }
 
@@ -395,7 +394,7 @@ __device__ __forceinline__ void few_part(const Attend& a, const AttendPlan& p, c
                 if (e == 0 && a.lse != nullptr)
                     a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(top, total);
             } else {
-                const Partial u = partial_of(ws, a, p, kv, part.slot);
+                const Partial u = partial_of(ws, a, p, kv, part.slot, a.cache.head_dim);
 #pragma unroll
                 for (int k = 0; k < kPer; k += 4)
                     if (e + k < dim)
@@ -580,7 +579,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     const Tile& t = part.t;
     const int32_t first = part.first, last = source.last;
 
-    const uint32_t dim = source.k_dim(), v_dim = a.value_dim;
+    const uint32_t dim = source.k_dim(), v_dim = a.cache.head_dim;
     bf16x8 q[QB][kSlices];
     int32_t low[QB], high[QB];
 #pragma unroll
@@ -987,17 +986,18 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         Half even, uneven;
         uint32_t va = v_lane + vb * kBuffer;
         begin_step();
-        if (works) ahead(even, k_lane + (x & 1) * kBuffer);
-        values_here();
-        if (works)
+        if (works) {  // (every wave, where values are late)
+            ahead(even, k_lane + (x & 1) * kBuffer);
+            values_here();
             inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
+        }
         end_step();
         while (x < in1) {
             const uint32_t ka = k_lane + (x & 1) * kBuffer;
             begin_step();
-            if (works) inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
-            values_here();
             if (works) {
+                inner(uneven, even, ka, va + 32 * kRow, std::true_type{});
+                values_here();
                 va = v_lane + vb * kBuffer;
                 inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
             }
@@ -1031,7 +1031,7 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
             if (h == 0 && a.lse != nullptr)
                 a.lse[(uint64_t)w.token * a.q.heads + head] = log_sum(m[b], total);
         } else {
-            const Partial u = partial_of(ws, a, p, kv, part.slot);
+            const Partial u = partial_of(ws, a, p, kv, part.slot, a.cache.head_dim);
 #pragma unroll
             for (int d = 0; d < kParts; d++)
 #pragma unroll
@@ -1115,7 +1115,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
     const uint32_t from = step / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
     if (from == upto) return;
-    const uint32_t dim = a.value_dim;
+    const uint32_t dim = a.cache.head_dim;
     const uint32_t e = 4 * (lane % LANES);
     const uint64_t stride = (uint64_t)dim << p.tile_log2;
     const int32_t rows = 1 << p.tile_log2;
@@ -1126,7 +1126,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(Attend a, AttendPlan p
         f32x4 x = {0, 0, 0, 0};
         for (uint32_t i0 = from; i0 <= upto; i0 += kWave) {
             const uint32_t parts = upto - i0 + 1 < kWave ? upto - i0 + 1 : kWave;
-            const Partial u = partial_of(ws, a, p, kv, i0 + number);
+            const Partial u = partial_of(ws, a, p, kv, i0 + number, a.cache.head_dim);
             float m = kNoKey, l = 0;
             if (lane < parts) {
                 m = u.ml[2 * (((uint64_t)lane << p.tile_log2) + r)];

@@ -8,8 +8,16 @@
 #include <cfloat>
 #include <cstdint>
 
+// What beginning a tile costs, in steps of keys (a file that includes this may
+// say so first).
+#ifndef SZ_TILE_EXTRA
+#define SZ_TILE_EXTRA 0
+#endif
+
 namespace sz {
 namespace {
+
+constexpr uint32_t kExtra = SZ_TILE_EXTRA;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -88,7 +96,6 @@ struct AttendPlan {
     uint32_t shares;     // workgroups that share it out for a KV head; 0: whole tiles
     uint32_t alone;      // up to so many steps in all, shares of one step
     bool wide;           // few rows, whole tiles, a CU each: eight waves
-    uint32_t extra;      // steps that a tile is counted as more than its keys make
     __host__ __device__ bool few() const { return tile_log2 == 4; }
 };
 
@@ -160,7 +167,7 @@ struct Shares {
     struct Load {
         Seq q;
         uint32_t tiles;   // of the sequence, 0 where it is faulty or has no rows
-        uint32_t steps;   // of each of its tiles, at least 1, `extra` ones first
+        uint32_t steps;   // of each of its tiles, at least 1, kExtra ones first
         int32_t from;     // the key of step 0
     };
     uint32_t each;
@@ -193,7 +200,7 @@ struct Shares {
         if (a.causal && a.window != 0 && (int64_t)c0 + 1 > (int64_t)a.window)
             x.from = (c0 + 1 - (int32_t)a.window) & ~31;
         x.steps = (uint32_t)(x.q.len - x.from + kStep - 1) / kStep;
-        x.steps = (x.steps == 0 ? 1 : x.steps) + p.extra;
+        x.steps = (x.steps == 0 ? 1 : x.steps) + kExtra;
         return x;
     }
 
@@ -341,7 +348,7 @@ struct Walk<false> {
         return false;
     }
 };
-// A tile begins with `extra` steps that have no keys, which stand for what it
+// A tile begins with kExtra steps that have no keys, which stand for what it
 // costs to begin one: a border among them counts as one before the tile.
 template <>
 struct Walk<true> {
@@ -352,28 +359,31 @@ struct Walk<true> {
         const Shares shares(a, p);
         step = index * shares.quota;
         end = step + shares.quota < shares.total ? step + shares.quota : shares.total;
-        return step < end && take(shares, a, p, index, part);
+        if (step >= end) return false;
+        return take(shares, a, p, index, part);
     }
     // (the sums are made anew: they would hold registers through the part)
     __device__ __forceinline__ bool next(const Attend& a, const AttendPlan& p, uint32_t index,
                                          Part& part) {
-        return step < end && take(Shares(a, p), a, p, index, part);
+        if (step >= end) return false;
+        return take(Shares(a, p), a, p, index, part);
     }
     __device__ __forceinline__ bool take(const Shares& shares, const Attend& a,
                                          const AttendPlan& p, uint32_t index, Part& part) {
         const Shares::Found f = shares.find(a, p, false, step);
         const uint32_t at = (step - f.steps0) / f.x.steps;
         const uint32_t base = f.steps0 + at * f.x.steps, stop = base + f.x.steps;
-        if (end < stop && end - base <= p.extra) return false;
+        if constexpr (kExtra != 0)
+            if (end < stop && end - base <= kExtra) return false;
         const uint32_t upto = stop < end ? stop : end;
-        const uint32_t done = step - base <= p.extra ? 0 : step - base - p.extra;
+        const uint32_t done = step - base <= kExtra ? 0 : step - base - kExtra;
         part.t = make_tile(a, p, f.seq, f.tiles0 + at, f.x.q, (int64_t)at << p.tile_log2);
         // (a part begins at one of the steps, even where a window shows the
         // tile's rows fewer keys than the sequence's first one: whole steps
         // up to the part's end, which masks nothing)
         const uint32_t skip = (uint32_t)(part.t.from - f.x.from) / kStep;
         part.first = f.x.from + (int32_t)((done > skip ? done : skip) * kStep);
-        const int32_t last = f.x.from + (int32_t)((upto - base - p.extra) * kStep);
+        const int32_t last = f.x.from + (int32_t)((upto - base - kExtra) * kStep);
         part.last = last < part.t.hi ? last : part.t.hi;
         part.alone = done == 0 && upto == stop;
         part.slot = index + part.t.number;
@@ -514,7 +524,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const Cache& c, uin
                                              kBufferFlags);
 }
 
-// Results of a part: for (KV head, slot), tile_rows rows of value_dim sums and
+// Results of a part: for (KV head, slot), tile_rows rows of dim sums and
 // of (maximum, sum of weights).
 struct Partial {
     float* o;
@@ -524,12 +534,12 @@ __host__ __device__ inline uint64_t partial_slots(const AttendPlan& p) {
     return (uint64_t)p.tiles + p.shares;
 }
 __device__ __forceinline__ Partial partial_of(uint8_t* ws, const Attend& a, const AttendPlan& p,
-                                              uint32_t kv, uint32_t slot) {
+                                              uint32_t kv, uint32_t slot, uint32_t dim) {
     const uint64_t slots = partial_slots(p);
     const uint64_t unit = kv * slots + slot;
     float* f = reinterpret_cast<float*>(ws);
     return Partial{f + 2 * (a.cache.kv_heads * slots << p.tile_log2) +
-                       (unit << p.tile_log2) * a.value_dim,
+                       (unit << p.tile_log2) * dim,
                    f + 2 * (unit << p.tile_log2)};
 }
 

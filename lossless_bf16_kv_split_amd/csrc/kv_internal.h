@@ -121,7 +121,7 @@ struct Attend {
     float scale, softcap;
     uint32_t causal;
     uint64_t window;
-    uint32_t value_dim;  // elements of an output row
+    uint32_t value_dim;  // elements of an output row (latents)
 };
 // Bytes of workspace that launch_attend may use, whatever the window.
 uint64_t attend_workspace(uint32_t q_heads, const Cache& cache, uint64_t n_seqs,
@@ -134,7 +134,7 @@ uint64_t attend_latent_workspace(uint32_t heads, const Cache& cache, uint32_t la
 hipError_t launch_attend_latent(const Attend& a, uint8_t* ws, hipStream_t stream);
 
 // Over keys and values of every head, in tensors: the Attend's cache has only
-// the number of heads (kv_heads), value_dim is head_dim too.
+// the number of heads (kv_heads) and value_dim (head_dim).
 struct Expanded {
     Rows k, r, v;  // r: no heads without a rotary part, one for all, or as many as k
     uint32_t key_dim, rotary_dim, value_dim;

@@ -10,6 +10,9 @@
 // Both products run on the matrix cores, S^T = C Q^T and O^T = C^T P^T, from
 // the same copy of the keys in LDS: what is loaded once is read as keys and,
 // transposed by the LDS reads, as values.
+// (48 tokens of 128 heads: 104 us with 0, 96 with 2, 94 with 3; drafts of 3 tokens
+// 37, 31, 31; 32 tokens of one sequence on 8192 keys 89, 101, 94)
+#define SZ_TILE_EXTRA 3
 #include "attend_parts.h"
 
 namespace sz {
@@ -364,7 +367,7 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
         if (h == 0 && kw == 0 && a.lse != nullptr)
             a.lse[(uint64_t)mine.token * a.q.heads + mine.head] = log_sum(m, total);
     } else {
-        const Partial u = partial_of(ws, a, p, 0, part.slot);
+        const Partial u = partial_of(ws, a, p, 0, part.slot, a.value_dim);
 #pragma unroll
         for (int d = 0; d < kParts; d++)
 #pragma unroll
@@ -422,7 +425,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
     const Shares::Found f = shares.find(a, p, true, number);
     const uint32_t at = number - f.tiles0;
     const uint32_t step = f.steps0 + at * f.x.steps;
-    uint32_t from = (step + p.extra) / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
+    uint32_t from = (step + kExtra) / shares.quota, upto = (step + f.x.steps - 1) / shares.quota;
     if (from == upto) return;
     const Tile t = make_tile(a, p, f.seq, number, f.x.q, (int64_t)at << p.tile_log2);
     const int32_t r = (int32_t)(blockIdx.x % pieces * kRows + (TOGETHER ? 0 : wave));
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
     float top = kNoKey, total = 0, x[8] = {};
     for (uint32_t i0 = from; i0 < upto; i0 += kWave) {
         const uint32_t parts = upto - i0 < kWave ? upto - i0 : kWave;
-        const Partial u = partial_of(ws, a, p, 0, i0 + number);
+        const Partial u = partial_of(ws, a, p, 0, i0 + number, a.value_dim);
         const float* o = u.o + (uint64_t)r * a.value_dim + e;
         constexpr uint32_t kBatch = 8;
         f32x4 v[kBatch][2];
@@ -515,10 +518,6 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
 constexpr uint64_t kManyTiles = 1024;
 constexpr uint64_t kWholeKeys = 256;
 constexpr uint32_t kTogether = 8;  // shares a tile from which on four waves join a row
-// What beginning a tile costs, in steps (48 tokens of 128 heads: 104 us without, 96
-// with 2, 94 with 3; drafts of 3 tokens 37, 31, 31; 32 tokens of one sequence on
-// 8192 keys 89, 101, 94).
-constexpr uint32_t kExtra = 3;
 constexpr uint64_t kShareSeqs = 1024;
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 
@@ -535,7 +534,6 @@ AttendPlan plan_latent(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint6
                        p.tiles * (max_len / kStep + 2 + kExtra) >= kMostSteps || max_len <= kWholeKeys;
     p.shares = whole ? 0 : (uint32_t)(kCus / halves(p));
     p.alone = p.shares;
-    p.extra = kExtra;
     return p;
 }
 
