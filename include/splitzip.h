@@ -647,7 +647,7 @@ sz_status sz_latent_append(const sz_heads *latent, const float *d_weight, float 
  * sz_attend_pages, with one KV head, no window and no cap.
  *   q    BF16, heads of latent_dim + rotary_dim elements
  *   out  BF16 or F32, as many heads of latent_dim elements
- *   n_tokens * heads < 2^31, n_tokens * heads / 128 + 2 * n_seqs < 2^24 */
+ *   n_tokens * heads < 2^30, n_tokens * heads / 64 + 2 * n_seqs < 2^24 - 16 */
 uint64_t sz_attend_latent_workspace_size(uint64_t heads, const sz_latent_cache *cache,
                                          const sz_batch *batch, uint64_t max_len);
 sz_status sz_attend_latent(const sz_heads *q, const sz_heads *out, float *d_lse,
@@ -696,12 +696,12 @@ sz_status sz_attend_expanded(const sz_heads *q, const sz_heads *out, float *d_ls
  *   w[s][v][j] = keep * before[s][v][j] + sum exp(score - lse)
  * over the rows (new tokens and query heads of v) that see j, with the
  * scores and visibility of sz_attend_pages and the log-sums that it left in
- * d_lse.  The new tokens' own positions (the last ones) have no `before`;
- * entries from d_lens[s] on are left as they were.  A row whose log-sum is
- * -infinity adds nothing; a row adds nothing to keys that it does not see,
- * whatever its bits and theirs.  FP32 throughout; the order of additions is
- * fixed by the call's sizes.  Only keys are read: d_v_pages of the cache may be
- * the key table.
+ * d_lse.  The new tokens' own positions (the last ones) have no `before`; a
+ * sequence without new tokens has keep * before.  Entries from d_lens[s] on are
+ * left as they were.  A row whose log-sum is -infinity adds nothing; a row adds
+ * nothing to keys that it does not see, whatever its bits and theirs.  FP32
+ * throughout; the order of additions is fixed by the call's sizes.  Only keys
+ * are read: d_v_pages of the cache may be the key table.
  *   q, d_lse   as sz_attend_pages took and left them (d_lse float[n_tokens]
  *              [q heads]); limits of q's heads and tokens as there
  *   d_before   optional device float[n_seqs][kv_heads][weights_pitch]; not read
@@ -751,8 +751,9 @@ sz_status sz_weigh_pages(const sz_heads *q, const float *d_lse, const float *d_b
  *   d_status      optional device i32[n_seqs]: SZ_OK, or
  *                 SZ_ERR_INVALID_ARGUMENT for a sequence whose length is
  *                 negative or above max_len (none of its tokens stays), or one
- *                 of whose pages, read or written, is NULL or misaligned (rows
- *                 there are not copied) */
+ *                 of whose pages, up to its length in `from` and up to what
+ *                 stays in `to`, is NULL or misaligned (rows there are not
+ *                 copied) */
 sz_status sz_evict_pages(const float *d_weights, uint64_t weight_heads, uint64_t weights_pitch,
                          const sz_kv_cache *from, const int32_t *d_lens, uint64_t n_seqs,
                          uint64_t max_len, uint64_t budget, uint64_t first, uint64_t recent,

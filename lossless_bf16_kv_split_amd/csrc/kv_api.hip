@@ -204,6 +204,12 @@ bool attend_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t q_heads, uint64_t 
            n_tokens * q_heads / 128 + 2 * n_seqs * kv_heads < uint64_t{1} << 24;
 }
 
+// (a tile of 128 rows of latent attention is two workgroups', in groups of eight)
+bool latent_fits(uint64_t n_seqs, uint64_t n_tokens, uint64_t heads) {
+    return 2 * n_tokens * heads <= kMaxTokens &&
+           n_tokens * heads / 64 + 2 * n_seqs < (uint64_t{1} << 24) - 16;
+}
+
 bool expanded_dim_ok(uint64_t d) { return d >= 8 && d <= 128 && d % 8 == 0; }
 
 bool spans_meet(Span a, Span b) {
@@ -443,7 +449,7 @@ uint64_t sz_attend_latent_workspace_size(uint64_t heads, const sz_latent_cache* 
         !latent_dims_ok(cache->latent_dim, cache->rotary_dim) || heads == 0 || heads > kMaxHeads ||
         !table_ok(cache->pages_per_seq, cache->table_pitch, cache->page_tokens) ||
         batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxTokens ||
-        !attend_fits(batch->n_seqs, batch->n_tokens, heads, 1) || batch->n_seqs == 0 ||
+        !latent_fits(batch->n_seqs, batch->n_tokens, heads) || batch->n_seqs == 0 ||
         batch->n_tokens == 0)
         return 0;
     const sz_kv_cache rows = rows_of(*cache);
@@ -463,7 +469,7 @@ sz_status sz_attend_latent(const sz_heads* q, const sz_heads* out, float* d_lse,
     const uint32_t dim = rows.head_dim, value = cache->latent_dim;
     if (!heads_ok(q, n, dim, false) || !heads_ok(out, n, value, true) ||
         q->type != SZ_TYPE_BF16 || q->heads != out->heads ||
-        !attend_fits(batch->n_seqs, n, q->heads, 1) || !apart(*q, dim, *out, value, n, false))
+        !latent_fits(batch->n_seqs, n, q->heads) || !apart(*q, dim, *out, value, n, false))
         return SZ_ERR_INVALID_ARGUMENT;
     if (!(scale > 0 && scale < 1e38f) || !aligned(d_lse, 4) || !aligned(d_status, 4))
         return SZ_ERR_INVALID_ARGUMENT;
@@ -476,7 +482,8 @@ sz_status sz_attend_latent(const sz_heads* q, const sz_heads* out, float* d_lse,
     const uint64_t need = sz_attend_latent_workspace_size(q->heads, cache, batch, max_len);
     if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 256) ||
                      workspace_bytes < need || overlap(d_workspace, need, span(*q, n, dim)) ||
-                     overlap(d_workspace, need, span(*out, n, value))))
+                     overlap(d_workspace, need, span(*out, n, value)) ||
+                     spans_meet(span_of(d_workspace, need), span_of(d_lse, lse_bytes))))
         return SZ_ERR_INVALID_ARGUMENT;
     if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
     if (sz_status s = check_stream(stream)) return s;
@@ -566,8 +573,7 @@ sz_status sz_attend_expanded(const sz_heads* q, const sz_heads* out, float* d_ls
 
 uint64_t sz_weigh_workspace_size(uint64_t q_heads, const sz_kv_cache* cache,
                                  const sz_batch* batch, uint64_t max_len) {
-    if (!weigh_sizes_ok(q_heads, cache, batch) || batch->n_seqs == 0 || batch->n_tokens == 0)
-        return 0;
+    if (!weigh_sizes_ok(q_heads, cache, batch) || batch->n_seqs == 0) return 0;
     const uint64_t most = most_len(*cache);
     return sz::weigh_workspace((uint32_t)q_heads, cache_of(*cache), batch->n_seqs,
                                batch->n_tokens, max_len == 0 || max_len > most ? most : max_len);
@@ -595,8 +601,8 @@ sz_status sz_weigh_pages(const sz_heads* q, const float* d_lse, const float* d_b
     if (keep == 0) d_before = nullptr;
     const uint64_t bytes = 4 * batch->n_seqs * cache->kv_heads * weights_pitch;
     const uint64_t need = sz_weigh_workspace_size(q->heads, cache, batch, max_len);
-    if (batch->n_seqs > 0 && n > 0) {
-        if (d_lse == nullptr || d_weights == nullptr) return SZ_ERR_INVALID_ARGUMENT;
+    if (batch->n_seqs > 0) {
+        if ((n > 0 && d_lse == nullptr) || d_weights == nullptr) return SZ_ERR_INVALID_ARGUMENT;
         if (overlap(d_weights, bytes, span(*q, n, dim)) ||
             overlap(d_weights, bytes, span_of(d_lse, 4 * n * q->heads)) ||
             (d_before != d_weights && overlap(d_weights, bytes, span_of(d_before, bytes))))
@@ -612,14 +618,13 @@ sz_status sz_weigh_pages(const sz_heads* q, const float* d_lse, const float* d_b
             uint64_t{1} << 24)
             return SZ_ERR_INVALID_ARGUMENT;
     }
-    if (batch->n_seqs == 0 || (n == 0 && d_status == nullptr)) return SZ_OK;
+    if (batch->n_seqs == 0) return SZ_OK;
     if (sz_status s = check_stream(stream)) return s;
     sz::Cache c = cache_of(*cache);
     c.v_pages = c.k_pages;
     const sz::Weigh a{rows_of(q), d_lse, d_before, d_weights, weights_pitch, keep, c,
                       batch_of(*batch), (int64_t)max_len, scale, softcap, causal != 0, window};
-    sz_status st = SZ_OK;
-    if (n > 0) st = hip_status(sz::launch_weigh(a, static_cast<float*>(d_workspace), stream));
+    sz_status st = hip_status(sz::launch_weigh(a, static_cast<float*>(d_workspace), stream));
     if (st == SZ_OK && d_status != nullptr)
         st = hip_status(sz::launch_check_seqs(
             sz::SeqCheck{c, a.batch, a.max_len, 0, a.causal, window, d_status}, stream));
