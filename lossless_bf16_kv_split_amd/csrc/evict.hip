@@ -577,7 +577,7 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
 // Bound by the vector instructions of one CU, about thirty for 64 weights.
 constexpr uint32_t kPickThreads = 1024;
 constexpr uint32_t kPickWaves = kPickThreads / kWave;
-constexpr uint32_t kDigit = 11, kBins = 1u << kDigit, kCopies = 2;
+constexpr uint32_t kDigit = 11, kBins = 1u << kDigit, kCopies = 4;
 constexpr uint32_t kHold = 32;  // weights of a thread
 constexpr uint32_t kPiece = kHold * kPickThreads;
 
@@ -620,7 +620,7 @@ struct Before {
 __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
     __shared__ uint32_t bins[kCopies][kBins];
     __shared__ __attribute__((aligned(16))) uint32_t sums[2][kPickWaves];
-    __shared__ uint32_t chosen[2];
+    __shared__ uint32_t chosen[3];
     const uint32_t s = blockIdx.x / a.weight_heads, t = threadIdx.x, lane = t % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t / kWave);
     const int32_t len = a.lens[s];
@@ -702,11 +702,18 @@ __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
             const bool first = above + own[0] >= take;
             chosen[0] = kBins - 1 - 2 * t - (first ? 0 : 1);
             chosen[1] = take - above - (first ? 0 : own[0]);
+            chosen[2] = own[first ? 0 : 1];
         }
         lds_barrier();
         prefix = above_digit >= 32 ? chosen[0] << low
                                    : (prefix >> above_digit << above_digit) | chosen[0] << low;
         take = chosen[1];
+        // (all that begin like this stay, as distinct weights do after two digits)
+        if (take == chosen[2] && prefix != 0) {
+            prefix--;
+            take = 0;
+            break;
+        }
     }
     // every key above `prefix` stays, and of those equal to it the first `take`
     uint32_t base_sure = 0, base_ties = 0;
