@@ -563,10 +563,10 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
     // With the rotary part there is room for two workgroups only if V has two
     // buffers.  A step's values are then asked for when it begins, into those
     // of the step before the last, and waited for in its middle, a barrier more
-    // (four chunks of 20 heads, 128 rows: 98.7 us, 113 with three buffers and
-    // one workgroup; a prompt of 8192 tokens of 32 heads 618, 753, and 638 with
-    // 256 rows).  Shared out, a tile takes more registers than half of them.
-    constexpr bool kLate = kRotary && !SHARED;
+    // (a prompt of 8192 tokens of 32 heads 618 us, 753 with three buffers and one
+    // workgroup, 638 with 256 rows; shared out, 1024 tokens of 16 heads on 8192
+    // keys 102, 123 with one workgroup).
+    constexpr bool kLate = kRotary;
     constexpr uint32_t kVs = kLate ? 2 : 3;
     constexpr int kKeys = 64;
     constexpr uint32_t kRow = 2 * DP;             // bytes of a row in LDS
@@ -986,10 +986,12 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
         Half even, uneven;
         uint32_t va = v_lane + vb * kBuffer;
         begin_step();
-        if (works) {  // (every wave, where values are late)
+        if (works) {
             ahead(even, k_lane + (x & 1) * kBuffer);
             values_here();
             inner(even, uneven, k_lane + (x & 1) * kBuffer + 32 * kRow, va, std::true_type{});
+        } else {
+            values_here();
         }
         end_step();
         while (x < in1) {
@@ -1000,6 +1002,8 @@ __device__ __forceinline__ void chunk_part(const Attend& a, const AttendPlan& p,
                 values_here();
                 va = v_lane + vb * kBuffer;
                 inner(even, uneven, ka + 32 * kRow, va, std::true_type{});
+            } else {
+                values_here();
             }
             end_step();
         }
@@ -1069,10 +1073,10 @@ __global__ __launch_bounds__(kThreads, QB == 1 && DP <= 128 ? 2 : 1) void k_atte
 // The same over keys and values expanded from latents: 192 elements of keys,
 // 128 of values.
 template <bool SHARED>
-__global__ __launch_bounds__(kThreads, SHARED ? 1 : 2) void k_attend_expanded(
+__global__ __launch_bounds__(kThreads, 2) void k_attend_expanded(
     Attend a, Expanded e, AttendPlan p, Score score, uint8_t* ws) {
     const uint32_t head = blockIdx.x % a.cache.kv_heads, index = blockIdx.x / a.cache.kv_heads;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<128, true, SHARED ? 3 : 2>];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kChunkLds<128, true, 2>];
     Walk<SHARED> walk(a, p);
     Part part;
     if (!walk.first(a, p, SHARED ? index : p.tiles - 1 - index, part)) return;
@@ -1220,9 +1224,12 @@ uint64_t attend_workspace(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uin
 }
 
 // Keys and values expanded from latents: a head is a KV head of its own.
-// Tiles of 128 rows, whole where there is one for each CU (1024 tokens of 16
-// heads on 8192 keys, 128 tiles: 159 us whole, 123 shared out) or with few keys
-// (1024 of 16 heads on as many keys: 28 and 34; 512 of 5 on 2048: 46 and 28).
+// Tiles of 128 rows, whole where there is one for each CU (four chunks of 20
+// heads, 340 tiles: 112 us whole, 129 shared out), or where the CUs without one
+// would take too few keys off the others to pay for the join.  Whole and shared
+// out, us: 1024 tokens of 16 heads (128 tiles) on 1024 keys 29 and 35, on 2048
+// 50 and 42, on 8192 159 and 102; 1500 of 16 as a prompt (176) 40 and 47; on
+// 1024 keys 512 of 5 (20) 27.3 and 24.7, 128 of 16 (16) 27.5 and 22.5.
 AttendPlan plan_expanded(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint64_t max_len) {
     AttendPlan p{};
     p.group = 1;
@@ -1231,8 +1238,9 @@ AttendPlan plan_expanded(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uin
     const uint64_t full = n_tokens >> p.tile_log2;
     const uint64_t groups = (full > n_seqs ? full : n_seqs) * heads;
     const bool whole = n_seqs > kShareSeqs || heads > kCus || groups >= kCus ||
-                       p.tiles * (max_len / kStep + 2) >= kMostSteps || max_len <= 1024;
-    p.shares = whole ? 0 : (uint32_t)(kCus / heads);
+                       p.tiles * (max_len / kStep + 2) >= kMostSteps ||
+                       max_len * (kCus - groups) <= 768 * kCus;
+    p.shares = whole ? 0 : (uint32_t)(2 * kCus / heads);
     return p;
 }
 
