@@ -671,7 +671,8 @@ sz_status sz_attend_latent(const sz_heads *q, const sz_heads *out, float *d_lse,
  *   d_key_starts  device i32[n_seqs]; any order, rows may be shared
  *   n_keys    < 2^31
  *   max_len   a host-side bound of d_lens (longer sequences are refused); 0, or
- *             anything past it, means n_keys
+ *             anything past it, means n_keys.  The workspace's size goes by
+ *             that bound; asked for with 0 it is enough for any
  *   n_tokens * heads < 2^31, n_tokens * heads / 128 + 2 * n_seqs * heads < 2^24
  *   d_status  SZ_ERR_INVALID_ARGUMENT also for a sequence whose rows do not
  *             lie in 0 .. n_keys */

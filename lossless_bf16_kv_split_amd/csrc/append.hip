@@ -318,9 +318,11 @@ hipError_t launch(const TurnRows& a, const Cache& cache, const Batch& batch, hip
 
 // A new token's latent (normed with a weight) and its key's rotary part go to
 // its row of a latent page, side by side; the rotary parts of its queries are
-// turned beside them.  The latent row lies across a wave, 8 elements a lane; of
-// rotary rows (the key's first, then the queries') a wave holds as many as it
-// has LANES.  Slices as in k_turn; the first one has the latent.
+// turned beside them.  The latent row lies across a wave, 8 elements a lane, so
+// that the norm's sum needs no LDS; a rotary row (the key's first, then the
+// queries') lies across LANES of them.  Slices as in k_turn; the first one has
+// the latent.  A prompt of 8192 tokens (32 heads, from 32 bits): 26.9 us, 4.8
+// TB/s, the rate of memory; 40 tokens of 128 heads 4.4, the chain of lookups.
 template <int LANES, int VEC, int MODE>
 __global__ __launch_bounds__(kThreads) void k_latent_append(LatentRows a, Cache cache, Batch batch,
                                                             uint32_t slices, uint32_t first) {

@@ -1246,7 +1246,9 @@ AttendPlan plan_expanded(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uin
 
 uint64_t attend_expanded_workspace(uint32_t heads, uint32_t value_dim, uint64_t n_seqs,
                                    uint64_t n_tokens, uint64_t max_len) {
-    const AttendPlan p = plan_expanded(heads, n_seqs, n_tokens, max_len);
+    // (0, of any length: one that is shared out if any is)
+    const AttendPlan p =
+        plan_expanded(heads, n_seqs, n_tokens, max_len == 0 ? uint64_t{1} << 18 : max_len);
     if (p.shares == 0) return 0;
     const uint64_t rows = heads * partial_slots(p) << p.tile_log2;
     return (rows * (value_dim + 2) * 4 + 255) / 256 * 256;

@@ -128,6 +128,9 @@ __device__ __forceinline__ float weight_of(const Score& score, float z, float mi
 }
 
 // ---- few rows ----------------------------------------------------------------
+//
+// Bound by the reads of keys: 48 tokens of 32/8 heads on 130 to 8192 keys, 432 MB,
+// 93 us, 4.7 TB/s.
 template <int DP, bool CAPPED>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh a, WeighPlan p,
                                                                           Score score) {
@@ -273,7 +276,10 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
 // Rows pass in steps of 32 through LDS: each wave fetches eight of them while
 // the step before is worked on, one barrier a step.  LDS rows are cut into
 // 16-byte pieces, piece c of row r at c ^ (r & 15) (r >> 1 & 7 with 64
-// elements), so that 16 rows' same piece lies in 16 places.
+// elements), so that 16 rows' same piece lies in 16 places.  Bound by the vector
+// instructions, an exponential and two more for every score (63% of the cycles,
+// the products 33%): a prompt of 4096 tokens, 32/8 heads of 128, 82 to 86 us with
+// the join's 4.7.
 template <int DP, bool CAPPED>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p, Score score,
                                                             float* ws) {
@@ -574,7 +580,9 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
 // weights and keys stay in registers over the passes, every load under way at
 // once; more are read again in pieces of so many for each.  A wave has
 // consecutive weights, 64 at a time, so that ballots give each token its place.
-// Bound by the vector instructions of one CU, about thirty for 64 weights.
+// Bound by the vector instructions and LDS of one CU: 32768 weights 26 us, 24 x 8
+// rows of up to 8192 17.6; four copies of the counts, by lane, keep equal digits
+// apart (one row 41.8 us with the copying, with two 42.7, with one 43.6).
 constexpr uint32_t kPickThreads = 1024;
 constexpr uint32_t kPickWaves = kPickThreads / kWave;
 constexpr uint32_t kDigit = 11, kBins = 1u << kDigit, kCopies = 4;
@@ -757,7 +765,7 @@ __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
 }
 
 // Copies kept rows, 16 destination tokens and all heads a workgroup: LANES
-// lanes a row, 16 bytes each.
+// lanes a row, 16 bytes each.  At the rate of memory: 206 MB in 37.8 us, 5.4 TB/s.
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_evict_copy(Evict a, uint32_t blocks) {
     constexpr uint32_t kRows = kThreads / LANES;  // of a round

@@ -505,8 +505,7 @@ uint64_t sz_attend_expanded_workspace_size(uint64_t heads, uint32_t value_dim,
         batch->n_tokens == 0)
         return 0;
     return sz::attend_expanded_workspace((uint32_t)heads, value_dim, batch->n_seqs,
-                                         batch->n_tokens,
-                                         max_len == 0 || max_len > kMaxLen ? kMaxLen : max_len);
+                                         batch->n_tokens, max_len > kMaxLen ? kMaxLen : max_len);
 }
 
 sz_status sz_attend_expanded(const sz_heads* q, const sz_heads* out, float* d_lse,

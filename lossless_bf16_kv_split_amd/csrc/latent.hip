@@ -10,6 +10,15 @@
 // Both products run on the matrix cores, S^T = C Q^T and O^T = C^T P^T, from
 // the same copy of the keys in LDS: what is loaded once is read as keys and,
 // transposed by the LDS reads, as values.
+//
+// 48 tokens of 128 heads on 100 to 8192 keys (196 MB of rows): 91 to 96 us, of
+// which the join 10.  A step of 64 keys takes about 4800 cycles: 1900 for the
+// scores, bound by LDS (their reads 1152, the next step's rows arriving 576),
+// 1060 for the output, 1200 for the softmax and its barrier, 600 waiting for the
+// rows.  LDS holds two steps' keys and one workgroup a CU, so nothing runs
+// beside a wave's wait.
+//
+// What beginning a tile costs, in steps, so that it is shared out with them
 // (48 tokens of 128 heads: 104 us with 0, 96 with 2, 94 with 3; drafts of 3 tokens
 // 37, 31, 31; 32 tokens of one sequence on 8192 keys 89, 101, 94)
 #define SZ_TILE_EXTRA 3
@@ -389,7 +398,10 @@ __device__ __forceinline__ void latent_part(const Attend& a, const AttendPlan& p
 
 // HALVES workgroups have a tile's rows between them and read the same keys at
 // the same time: numbers that differ by eight, which share an L2, so that the
-// keys come from memory once.
+// keys come from memory once (246 MB for the 48 tokens above; tiles of 64 rows
+// read 460).  Tiles of 64 rows, pairs of them: 48 tokens 99 and 97 us, drafts of
+// 3 tokens of 64 heads 32.9 and 31.3, 32 tokens of one sequence 108 and 100, 128 of
+// one 151 and 152.
 template <int DL, int DT, int RW, int HALVES, bool SHARED>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_latent(Attend a, AttendPlan p, float by,
                                                                uint8_t* ws) {
@@ -410,7 +422,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_latent(Attend a, AttendP
 // Joins the parts of the tiles that were cut, eight elements a lane; the parts'
 // maxima and sums 64 at a time, one a lane.  A row is one wave's, or (TOGETHER,
 // where tiles have many parts) the four waves of a workgroup take a quarter
-// of its parts each.
+// of its parts each (one token of 16 heads on 32768 keys 29 us in all, 63 by
+// one wave).  Latency bound: 4 us of a short call, 10 of the 48 tokens'.
 template <bool TOGETHER>
 __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p, uint8_t* ws) {
     constexpr uint32_t kRows = TOGETHER ? 1 : kWaves;

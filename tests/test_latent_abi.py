@@ -194,6 +194,10 @@ def test_expanded_workspace(sz):
         sz._lib.sz_attend_expanded_workspace_size(h, v, at(b), m)
     need = size()
     assert need > 0 and size(m=0) == size(m=1 << 40)
+    for tokens in (1, 100, 1024, 2000):     # with 0: enough for any length
+        b = batch(seqs=1, tokens=tokens)
+        lengths = [1 << i for i in range(31)] + [777, 1500, 200000]
+        assert size(b=b, m=0) == max(size(b=b, m=m) for m in lengths)
     assert size(h=0) == 0 and size(v=12) == 0 and size(v=136) == 0 and size(b=None) == 0
     assert size(b=batch(tokens=0)) == 0 and size(b=batch(seqs=0)) == 0
     one = dict(b=batch(seqs=1, tokens=100), n_keys=8192)
