@@ -422,8 +422,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_latent(Attend a, AttendP
 // Joins the parts of the tiles that were cut, eight elements a lane; the parts'
 // maxima and sums 64 at a time, one a lane.  A row is one wave's, or (TOGETHER,
 // where tiles have many parts) the four waves of a workgroup take a quarter
-// of its parts each (one token of 16 heads on 32768 keys 29 us in all, 63 by
-// one wave).  Latency bound: 4 us of a short call, 10 of the 48 tokens'.
+// of its parts each.  Latency bound: 4 us of a short call, 10 of the 48 tokens'.
 template <bool TOGETHER>
 __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p, uint8_t* ws) {
     constexpr uint32_t kRows = TOGETHER ? 1 : kWaves;
@@ -525,13 +524,21 @@ __global__ __launch_bounds__(kThreads) void k_latent_join(Attend a, AttendPlan p
         a.lse[(uint64_t)w.token * a.q.heads + w.head] = log_sum(top, total);
 }
 
-// Tiles of 32, 64 or 128 rows by what sequences have on average; whole where
-// they fill the chip or have few keys, shared out among one workgroup a CU
-// otherwise (attend_parts.h).
-constexpr uint64_t kManyTiles = 1024;
-constexpr uint64_t kWholeKeys = 256;
-constexpr uint32_t kTogether = 8;  // shares a tile from which on four waves join a row
-constexpr uint64_t kShareSeqs = 1024;
+// Tiles of 32, 64 or 128 rows by what sequences have on average; whole, or shared
+// out among one workgroup a CU (attend_parts.h).  Whole ones take as long as the
+// longest sequence; of two workgroups for each CU, or of one with lengths that
+// differ, about half would wait for it.  Sharing them out costs what 400 keys do
+// and two for each workgroup (parts to store and to join).  Whole and shared
+// out, us: one token of 16 heads on 256 keys 12.7 and 16.4, on 512 18.5 and 16.0;
+// 8 on 700 23.6 and 16.0; 48 of 128 heads on 512 28 and 36, on 1024 42 and 45, on
+// 2048 71 and 62, on 100 to 2048 69 and 47; 128 on 100 to 8192 493 and 242; 256
+// of 32 heads on 100 to 2048 138 and 114; 300 of 16 on 100 to 1024 55 and 63, to
+// 8192 372 and 297; 512 of 16 to 1024 93 and 182, to 8192 546 and 528; 1000 of 16
+// to 1024 167 and 506; 256 tokens of one sequence, 128 heads, on 4096 271 and 283.
+// Shares a tile from which on four waves join a row: one token of 16 heads on 32768
+// keys, 256 shares, 26 us, by one wave 40; 32 tokens of 128 heads, four shares, 104
+// and 98.
+constexpr uint32_t kTogether = 8;
 constexpr uint64_t kMostSteps = uint64_t{1} << 30;
 
 uint32_t halves(const AttendPlan& p) { return p.tile_log2 == 7 ? 2 : 1; }
@@ -543,8 +550,10 @@ AttendPlan plan_latent(uint32_t heads, uint64_t n_seqs, uint64_t n_tokens, uint6
     p.tile_log2 = rows <= 32 * n_seqs ? 5 : rows <= 64 * n_seqs ? 6 : 7;
     p.tiles = (uint32_t)((rows >> p.tile_log2) + n_seqs);
     const uint64_t full = rows >> p.tile_log2;
-    const bool whole = n_seqs > kShareSeqs || (full > n_seqs ? full : n_seqs) >= kManyTiles ||
-                       p.tiles * (max_len / kStep + 2 + kExtra) >= kMostSteps || max_len <= kWholeKeys;
+    const uint64_t units = (full > n_seqs ? full : n_seqs) * halves(p);
+    const bool whole = units >= 2 * kCus ||
+                       p.tiles * (max_len / kStep + 2 + kExtra) >= kMostSteps ||
+                       max_len * (2 * kCus - units) <= 2 * kCus * (400 + 2 * units);
     p.shares = whole ? 0 : (uint32_t)(kCus / halves(p));
     p.alone = p.shares;
     return p;
