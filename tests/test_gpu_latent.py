@@ -415,3 +415,26 @@ def test_nothing_to_do(torch, sz):
     x = torch.zeros(0, 1, 576, dtype=torch.bfloat16, device="cuda")
     assert sz.latent_append(x[..., :512], S.cache, S.batch, x[..., 512:]) is None
     torch.cuda.synchronize()
+
+
+# ---- both ways of cutting the work up ------------------------------------------
+
+@pytest.mark.parametrize("heads,n,shape", [(16, 600, (512, 64)), (40, 530, (64, 16)),
+                                           (128, 260, (512, 64)), (128, 270, (200, 8))], ids=str)
+def test_whole_tiles(torch, sz, heads, n, shape):
+    """More tiles than two for each CU, of 32, 64 and 128 rows: every one whole."""
+    pairs = [(1, 1 + 37 * s % 150) for s in range(n)]
+    S = Setup(torch, sz, pairs, heads, *shape, 16, seed=40)
+    assert sz.sz_attend_latent_workspace_size(heads, S.cache, S.batch, 0) == 0
+    check(torch, sz, S, f"whole {heads} {n}")
+
+
+@pytest.mark.parametrize("heads,n,shape", [(16, 200, (512, 64)), (40, 130, (64, 16)),
+                                           (128, 70, (512, 64))], ids=str)
+def test_many_sequences_share_the_chip(torch, sz, heads, n, shape):
+    """More sequences than a wave has lanes, one of them long: shared out."""
+    pairs = [(1, 1 + 37 * s % 150) for s in range(n)]
+    pairs[n // 3] = (1, 5000)
+    S = Setup(torch, sz, pairs, heads, *shape, 64, seed=41)
+    assert sz.sz_attend_latent_workspace_size(heads, S.cache, S.batch, 5000) > 0
+    check(torch, sz, S, f"shared {heads} {n}", max_len=5000)
