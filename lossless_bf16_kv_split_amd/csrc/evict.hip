@@ -187,8 +187,9 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
         float before;
     };
     const uint32_t piece = lane % kLanes;
-    const uint32_t off0 = 8 * piece < dim ? lane / kLanes * 2 * (uint32_t)a.cache.token_stride + 16 * piece
-                                          : 0x80000000u;
+    const uint32_t row_bytes = 2 * (uint32_t)a.cache.token_stride;
+    const uint32_t off0 =
+        8 * piece < dim ? lane / kLanes * row_bytes + 16 * piece : 0x80000000u;
     // Keys of a block of 32, and what the lane's key had before.  Lane (n, h)
     // ends with the sum of key 16 (n / 4 % 2) + 4 h + n % 4.
     const int32_t mine = 16 * (int32_t)(n / 4 % 2) + 4 * (int32_t)h + (int32_t)(n % 4);
@@ -209,8 +210,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
 #pragma unroll
             for (int i = 0; i < kLoads / 2; i++)
                 x.k[kLoads / 2 * b + i] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rows,
-                    off0 + i * ((int)kWave / kLanes) * 2 * (uint32_t)a.cache.token_stride, 0, 0);
+                    rows, off0 + i * ((int)kWave / kLanes) * row_bytes, 0, 0);
         }
         x.before = 0;
         if (a.before != nullptr && j + mine < past && j + mine < c0)
@@ -281,8 +281,9 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
 // the products 33%): a prompt of 4096 tokens, 32/8 heads of 128, 82 to 86 us with
 // the join's 4.7.
 template <int DP, bool CAPPED>
-__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p, Score score,
-                                                            float* ws) {
+__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p,
+                                                                           Score score,
+                                                                           float* ws) {
     constexpr int kSlices = DP / 32;
     constexpr uint32_t kStepRows = 32, kRowBytes = 2 * DP;
     constexpr int kLoads = DP / 64;  // 16-byte pieces of a lane, eight lanes a row

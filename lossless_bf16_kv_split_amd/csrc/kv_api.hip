@@ -527,7 +527,8 @@ sz_status sz_attend_expanded(const sz_heads* q, const sz_heads* out, float* d_ls
         return SZ_ERR_INVALID_ARGUMENT;
     const auto keys_ok = [&](const sz_heads* x, uint32_t d) {
         return heads_ok(x, n_keys, d, false) && x->type == SZ_TYPE_BF16 &&
-               x->token_stride < kMaxPageStride && !spans_meet(span(*x, n_keys, d), span(*out, n, value_dim));
+               x->token_stride < kMaxPageStride &&
+               !spans_meet(span(*x, n_keys, d), span(*out, n, value_dim));
     };
     if (!keys_ok(k, key_dim) || !keys_ok(v, value_dim) || k->heads != q->heads ||
         v->heads != q->heads || (k_rotary == nullptr) != (rotary_dim == 0))

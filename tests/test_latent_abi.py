@@ -167,7 +167,8 @@ def test_expanded_refuses(sz):
         dict(out=heads(A + GB, n=16, type=3)), dict(out=heads(A, n=16)),
         dict(k=heads(A + 2 * GB, n=8)), dict(k=heads(A + 2 * GB, n=16, type=2)),
         dict(k=heads(0, n=16)), dict(k=heads(A + 2 * GB + 8, n=16)),
-        dict(k=heads(big, n=16, token_stride=1 << 26)), dict(v=heads(big, n=16, token_stride=1 << 26)),
+        dict(k=heads(big, n=16, token_stride=1 << 26)),
+        dict(v=heads(big, n=16, token_stride=1 << 26)),
         dict(v=heads(A + 3 * GB, n=15)), dict(v=heads(A + 3 * GB, n=16, type=2)),
         dict(k=heads(A + GB + 256, n=16)), dict(v=heads(A + GB, n=16)),   # written by the call
         dict(r=heads(A + GB, n=1, dim=64)), dict(r=heads(A + 4 * GB, n=2, dim=64)),
