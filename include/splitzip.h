@@ -761,6 +761,18 @@ sz_status sz_evict_pages(const float *d_weights, uint64_t weight_heads, uint64_t
                          const sz_kv_cache *to, float *d_weights_to, int32_t *d_kept,
                          int32_t *d_lens_to, int32_t *d_status, hipStream_t stream);
 
+/* The same with the rows of d_weights_to weights_to_pitch floats apart (>=
+ * budget, < 2^31) instead of budget: with a pitch that holds the tokens to
+ * come, what stays is the next sz_weigh_pages' d_before as it is.  Entries
+ * between the rows are left as they were. */
+sz_status sz_evict_pages_pitched(const float *d_weights, uint64_t weight_heads,
+                                 uint64_t weights_pitch, const sz_kv_cache *from,
+                                 const int32_t *d_lens, uint64_t n_seqs, uint64_t max_len,
+                                 uint64_t budget, uint64_t first, uint64_t recent,
+                                 const sz_kv_cache *to, float *d_weights_to,
+                                 uint64_t weights_to_pitch, int32_t *d_kept, int32_t *d_lens_to,
+                                 int32_t *d_status, hipStream_t stream);
+
 /* ---- compressed transfer to and from host memory ----------------------
  * The explainers present the codec as a way to shrink the KV transfer
  * between prefill and decode servers (introduction and "Les Resultats").

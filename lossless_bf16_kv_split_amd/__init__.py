@@ -36,7 +36,8 @@ __all__ = [
     "sz_latent_append", "sz_attend_latent_workspace_size", "sz_attend_latent", "LatentCache",
     "latent_cache", "latent_append", "attend_latent",
     "sz_attend_expanded_workspace_size", "sz_attend_expanded", "attend_expanded",
-    "sz_weigh_workspace_size", "sz_weigh_pages", "sz_evict_pages", "weigh_pages", "evict_pages",
+    "sz_weigh_workspace_size", "sz_weigh_pages", "sz_evict_pages",
+    "sz_evict_pages_pitched", "weigh_pages", "evict_pages",
     "sz_status_string", "encode",
     "decode", "encode_blocks", "decode_blocks", "BlockContainers",
     "PREFIX_BYTES", "MAX_ELEMENTS", "NOALLOC_WORKSPACE_BYTES",
@@ -141,8 +142,10 @@ def _load() -> ctypes.CDLL:
     L.sz_weigh_workspace_size.restype = u64
     L.sz_weigh_pages.argtypes = [p, p, p, p, u64, f32, p, p, u64, f32, f32, i32, u64, p, u64, p, p]
     L.sz_evict_pages.argtypes = [p, u64, u64, p, p, u64, u64, u64, u64, u64, p, p, p, p, p, p]
+    L.sz_evict_pages_pitched.argtypes = [p, u64, u64, p, p, u64, u64, u64, u64, u64, p, p, u64, p,
+                                         p, p, p]
     for name in ("sz_latent_append", "sz_attend_latent", "sz_attend_expanded",
-                 "sz_weigh_pages", "sz_evict_pages",
+                 "sz_weigh_pages", "sz_evict_pages", "sz_evict_pages_pitched",
                  "sz_rope_frequencies", "sz_rope_phases", "sz_qk_norm_rope", "sz_kv_append",
                  "sz_attend_pages", "sz_encode", "sz_decode", "sz_encode_noalloc", "sz_encode_histogram", "sz_encode_codebook",
                  "sz_encode_pack", "sz_encode_pack_ranked", "sz_encode_sample",
@@ -784,24 +787,44 @@ def sz_evict_pages(weights, weights_to, from_cache, to_cache, lens, lens_to, max
     """weights: a float32 tensor [sequences, weight heads, pitch]; weights_to
     and kept: float32 and int32 tensors [sequences, weight heads, budget]; lens
     and lens_to: int32 tensors [sequences]; from_cache, to_cache: KVCaches."""
+    _evict("sz_evict_pages", weights, weights_to, None, from_cache, to_cache, lens, lens_to,
+           max_len, budget, first, recent, kept, d_status, stream)
+
+
+def sz_evict_pages_pitched(weights, weights_to, weights_to_pitch: int, from_cache, to_cache, lens,
+                           lens_to, max_len: int, budget: int, first: int, recent: int, kept,
+                           d_status=None, stream=None) -> None:
+    """As sz_evict_pages, weights_to a tensor [sequences, weight heads,
+    weights_to_pitch]."""
+    _evict("sz_evict_pages_pitched", weights, weights_to, weights_to_pitch, from_cache, to_cache,
+           lens, lens_to, max_len, budget, first, recent, kept, d_status, stream)
+
+
+def _evict(call, weights, weights_to, to_pitch, from_cache, to_cache, lens, lens_to, max_len,
+           budget, first, recent, kept, d_status, stream) -> None:
     if weights.dim() != 3:
         raise ValueError("weights must have 3 dimensions")
     n, heads, pitch = weights.shape
     if not (0 <= max_len < _U64 and 0 <= budget < _U64 and 0 <= first < _U64 and
             0 <= recent < _U64):
         _fits(_U64, max_len, budget, first, recent)
+    pitched = () if to_pitch is None else (to_pitch,)
+    _fits(_U64, *pitched)
     stream = _call_stream(stream, from_cache, to_cache)
     index = from_cache._index
     if n > from_cache.rows or n > to_cache.rows:
         raise ValueError(f"{n} sequences, {from_cache.rows} and {to_cache.rows} rows in the page "
                          "tables")
-    _check(_lib.sz_evict_pages(
+    size = n * heads * budget
+    to_size = size
+    if to_pitch is not None and size > 0:
+        to_size = (n * heads - 1) * to_pitch + budget
+    _check(getattr(_lib, call)(
         _array(weights, "float32", n * heads * pitch, index, "weights"), heads, pitch,
         from_cache._at, _array(lens, "int32", n, index, "lens"), n, max_len, budget, first, recent,
-        to_cache._at, _array(weights_to, "float32", n * heads * budget, index, "weights_to"),
-        _array(kept, "int32", n * heads * budget, index, "kept"),
-        _array(lens_to, "int32", n, index, "lens_to"),
-        _array(d_status, "int32", n, index, "d_status"), stream), "sz_evict_pages")
+        to_cache._at, _array(weights_to, "float32", to_size, index, "weights_to"), *pitched,
+        _array(kept, "int32", size, index, "kept"), _array(lens_to, "int32", n, index, "lens_to"),
+        _array(d_status, "int32", n, index, "d_status"), stream), call)
 
 
 # ---- conveniences (torch allocates; the library computes) -----------------
@@ -1110,19 +1133,25 @@ def weigh_pages(q, lse, cache, batch, weights=None, keep: float = 1.0, max_len: 
 
 
 def evict_pages(weights, from_cache, to_cache, lens, budget: int, first: int = 0,
-                recent: int = 0, max_len: int = 0, check: bool = True):
+                recent: int = 0, max_len: int = 0, check: bool = True, room: int | None = None):
     """Keep at most ``budget`` tokens of each sequence, in the pages of
     to_cache (sz_evict_pages); returns the kept old positions (int32
     [sequences, weight heads, budget], -1 past those that stay), their weights
-    (zero there) and the new lengths.  ``check`` as in kv_append."""
+    (zero there) and the new lengths.  The weights have ``budget`` columns, or
+    ``room`` (at least budget): weigh_pages goes on with them in place where they
+    have room for the tokens that to_cache will hold (its pages' or max_len).
+    ``check`` as in kv_append."""
     import torch
     shape = (*weights.shape[:2], budget)
     kept = torch.empty(shape, dtype=torch.int32, device=weights.device)
-    weights_to = torch.zeros(shape, dtype=torch.float32, device=weights.device)
+    pitch = budget if room is None else room
+    if pitch < budget:
+        raise ValueError(f"room for {room} weights, {budget} tokens stay")
+    weights_to = torch.zeros((*shape[:2], pitch), dtype=torch.float32, device=weights.device)
     lens_to = torch.empty_like(lens)
     status = torch.zeros(lens.shape, dtype=torch.int32, device=lens.device) if check else None
-    sz_evict_pages(weights, weights_to, from_cache, to_cache, lens, lens_to, max_len, budget,
-                   first, recent, kept, status)
+    sz_evict_pages_pitched(weights, weights_to, pitch, from_cache, to_cache, lens, lens_to,
+                           max_len, budget, first, recent, kept, status)
     if check:
         _raise_on(status, "sz_evict_pages")
     return kept, weights_to, lens_to

@@ -638,7 +638,7 @@ __global__ __launch_bounds__(kPickThreads) void k_evict_pick(Evict a) {
     const uint32_t stay = n < a.budget ? n : a.budget;
     const float* w = a.weights + blockIdx.x * a.pitch;
     int32_t* kept = a.kept + blockIdx.x * (uint64_t)a.budget;
-    float* out = a.weights_to + blockIdx.x * (uint64_t)a.budget;
+    float* out = a.weights_to + blockIdx.x * a.to_pitch;
     if (blockIdx.x % a.weight_heads == 0 && t == 0) a.lens_to[s] = (int32_t)stay;
     for (uint32_t i = stay + t; i < a.budget; i += kPickThreads) kept[i] = -1;
     if (n <= a.budget) {

@@ -636,11 +636,24 @@ sz_status sz_evict_pages(const float* d_weights, uint64_t weight_heads, uint64_t
                          uint64_t max_len, uint64_t budget, uint64_t first, uint64_t recent,
                          const sz_kv_cache* to, float* d_weights_to, int32_t* d_kept,
                          int32_t* d_lens_to, int32_t* d_status, hipStream_t stream) {
+    return sz_evict_pages_pitched(d_weights, weight_heads, weights_pitch, from, d_lens, n_seqs,
+                                  max_len, budget, first, recent, to, d_weights_to, budget,
+                                  d_kept, d_lens_to, d_status, stream);
+}
+
+sz_status sz_evict_pages_pitched(const float* d_weights, uint64_t weight_heads,
+                                 uint64_t weights_pitch, const sz_kv_cache* from,
+                                 const int32_t* d_lens, uint64_t n_seqs, uint64_t max_len,
+                                 uint64_t budget, uint64_t first, uint64_t recent,
+                                 const sz_kv_cache* to, float* d_weights_to,
+                                 uint64_t weights_to_pitch, int32_t* d_kept, int32_t* d_lens_to,
+                                 int32_t* d_status, hipStream_t stream) {
     if (!cache_ok(from) || !cache_ok(to) || from->kv_heads != to->kv_heads ||
         from->head_dim != to->head_dim || n_seqs > kMaxSeqs)
         return SZ_ERR_INVALID_ARGUMENT;
     if ((weight_heads != 1 && weight_heads != from->kv_heads) || budget == 0 || budget > kMaxLen ||
-        first > budget || recent > budget - first || weights_pitch > kMaxTokens)
+        first > budget || recent > budget - first || weights_pitch > kMaxTokens ||
+        weights_to_pitch < budget || weights_to_pitch > kMaxTokens)
         return SZ_ERR_INVALID_ARGUMENT;
     const uint64_t most = most_len(*from);
     if (max_len == 0 || max_len > most) max_len = most;
@@ -659,7 +672,8 @@ sz_status sz_evict_pages(const float* d_weights, uint64_t weight_heads, uint64_t
     // what is read and what is written, apart
     const uint64_t lines = 4 * n_seqs * weight_heads, lens = 4 * n_seqs;
     const Span read[2] = {span_of(d_weights, lines * weights_pitch), span_of(d_lens, lens)};
-    const Span written[4] = {span_of(d_weights_to, lines * budget), span_of(d_kept, lines * budget),
+    const uint64_t to_bytes = (lines - 4) * weights_to_pitch + 4 * budget;
+    const Span written[4] = {span_of(d_weights_to, to_bytes), span_of(d_kept, lines * budget),
                              span_of(d_lens_to, lens),
                              span_of(d_status, d_status == nullptr ? 0 : lens)};
     for (int i = 0; i < 4; i++) {
@@ -671,7 +685,7 @@ sz_status sz_evict_pages(const float* d_weights, uint64_t weight_heads, uint64_t
     if (sz_status s = check_stream(stream)) return s;
     const sz::Evict a{d_weights, weights_pitch, (uint32_t)weight_heads, (uint32_t)budget,
                       (uint32_t)first, (uint32_t)recent, cache_of(*from), cache_of(*to), d_lens,
-                      (int64_t)max_len, d_weights_to, d_kept, d_lens_to};
+                      (int64_t)max_len, d_weights_to, weights_to_pitch, d_kept, d_lens_to};
     sz_status st = hip_status(sz::launch_evict(a, (uint32_t)n_seqs, stream));
     if (st == SZ_OK && d_status != nullptr)
         st = hip_status(sz::launch_evict_check(a, (uint32_t)n_seqs, d_status, stream));

@@ -175,8 +175,9 @@ struct Evict {
     Cache from, to;
     const int32_t* lens;
     int64_t max_len;
-    float* weights_to;     // [sequence][weight_heads][budget]
-    int32_t* kept;         // the same
+    float* weights_to;     // [sequence][weight_heads][to_pitch]
+    uint64_t to_pitch;
+    int32_t* kept;         // [sequence][weight_heads][budget]
     int32_t* lens_to;
 };
 hipError_t launch_evict(const Evict& a, uint32_t n_seqs, hipStream_t stream);
