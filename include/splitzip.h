@@ -763,8 +763,10 @@ sz_status sz_evict_pages(const float *d_weights, uint64_t weight_heads, uint64_t
 
 /* The same with the rows of d_weights_to weights_to_pitch floats apart (>=
  * budget, < 2^31) instead of budget: with a pitch that holds the tokens to
- * come, what stays is the next sz_weigh_pages' d_before as it is.  Entries
- * between the rows are left as they were. */
+ * come, what stays is the next sz_weigh_pages' d_before as it is.  With
+ * weight_heads = 1 that has kv_heads such rows a sequence: at kv_heads times
+ * the distance what stays lies in the first, and the heads' sum goes on if the
+ * others are zero.  Entries between the rows are left as they were. */
 sz_status sz_evict_pages_pitched(const float *d_weights, uint64_t weight_heads,
                                  uint64_t weights_pitch, const sz_kv_cache *from,
                                  const int32_t *d_lens, uint64_t n_seqs, uint64_t max_len,

@@ -1137,17 +1137,21 @@ def evict_pages(weights, from_cache, to_cache, lens, budget: int, first: int = 0
     """Keep at most ``budget`` tokens of each sequence, in the pages of
     to_cache (sz_evict_pages); returns the kept old positions (int32
     [sequences, weight heads, budget], -1 past those that stay), their weights
-    (zero there) and the new lengths.  The weights have ``budget`` columns, or
-    ``room`` (at least budget): weigh_pages goes on with them in place where they
-    have room for the tokens that to_cache will hold (its pages' or max_len).
-    ``check`` as in kv_append."""
+    (zero there) and the new lengths.  With ``room`` (at least budget) the
+    weights are a tensor [sequences, KV heads, room] that weigh_pages goes on
+    with in place, where there is room for the tokens that to_cache will hold
+    (its pages' or max_len); one choice for all heads leaves what stays in the
+    first head's row, for the heads' sum to go on.  ``check`` as in kv_append."""
     import torch
     shape = (*weights.shape[:2], budget)
     kept = torch.empty(shape, dtype=torch.int32, device=weights.device)
     pitch = budget if room is None else room
     if pitch < budget:
         raise ValueError(f"room for {room} weights, {budget} tokens stay")
-    weights_to = torch.zeros((*shape[:2], pitch), dtype=torch.float32, device=weights.device)
+    rows = shape[1] if room is None else from_cache.kv_heads
+    weights_to = torch.zeros((shape[0], rows, pitch), dtype=torch.float32, device=weights.device)
+    if rows > shape[1]:
+        pitch *= rows
     lens_to = torch.empty_like(lens)
     status = torch.zeros(lens.shape, dtype=torch.int32, device=lens.device) if check else None
     sz_evict_pages_pitched(weights, weights_to, pitch, from_cache, to_cache, lens, lens_to,

@@ -172,3 +172,60 @@ def test_heads_with_tokens_of_their_own(torch, sz):
             want = pick(full[s, h, :n].tolist(), n, 64, 2, 8)
             assert kept[s, h].tolist() == want
             assert torch.equal(weights[s, h, :64], full[s, h, want])
+
+
+@pytest.mark.gpu
+def test_one_choice_for_all_heads(torch, sz):
+    """The same with one choice by the heads' sum: what stays stands in the
+    first head's row, so that the heads' sum goes on."""
+    H, KH, D, page, budget, keep = 6, 3, 64, 16, 50, 0.75
+    pairs = [(2, 200), (1, 40), (30, 131)]
+    S = Setup(torch, sz, pairs, H, KH, D, page, seed=50)
+    T = Setup(torch, sz, [(1, min(n, budget) + 3) for _, n in pairs], H, KH, D, page, seed=51,
+              fill=0.0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    room = T.cache.pages_per_seq * page
+    _, lse = sz.attend_pages(S.q.cuda(), S.cache, S.batch)
+    weights = sz.weigh_pages(S.q.cuda(), lse, S.cache, S.batch)
+    full = weights.sum(1, keepdim=True)
+    lens = torch.tensor([n for _, n in pairs], **i32)
+    kept, weights, lens = sz.evict_pages(full, S.cache, T.cache, lens, budget, 2, 8, room=room)
+    assert kept.shape == (3, 1, budget) and weights.shape == (3, KH, room)
+    for s, (_, n) in enumerate(pairs):
+        want = pick(full[s, 0, :n].tolist(), n, budget, 2, 8)
+        assert kept[s, 0].tolist() == want + [-1] * (budget - len(want))
+        assert torch.equal(weights[s, 0, :len(want)], full[s, 0, want])
+        assert bool((weights[s, 0, len(want):] == 0).all())
+    assert bool((weights[:, 1:] == 0).all())
+    g = torch.Generator().manual_seed(52)
+    rope = sz.rope(D)
+    total = torch.zeros(3, room, dtype=torch.float64)     # over the heads, in 64 bits
+    slack = torch.zeros_like(total)
+    total[:] = weights[:, 0].cpu()
+    for step in range(3):
+        k, v, q = (torch.randn(3, h, D, generator=g).bfloat16() for h in (KH, KH, H))
+        lens = lens + 1
+        batch = sz.Batch(torch.arange(4, **i32), lens, 3)
+        places = torch.tensor([n + step for _, n in pairs], **i32)
+        q = sz.kv_append(k.cuda(), v.cuda(), T.cache, batch, rope, q.cuda(), positions=places)
+        _, lse = sz.attend_pages(q, T.cache, batch)
+        weights = sz.weigh_pages(q, lse, T.cache, batch, weights, keep)
+        T.pairs = [(1, n) for n in lens.tolist()]
+        for s, n in enumerate(lens.tolist()):
+            want, tol = weights_of(q[s:s + 1].cpu(), lse[s:s + 1].cpu(),
+                                   T.rows(T.kd.cpu(), s), n, D ** -0.5)
+            total[s, :n - 1] *= keep
+            # (each step's product and sum round once)
+            slack[s] = slack[s] * keep + 2 * ref.U32 * total[s]
+            total[s, :n] += want.sum(0)
+            slack[s, :n] += tol.sum(0) + 2 * ref.U32 * total[s, :n]
+        got = weights.cpu().double().sum(1)
+        assert bool(((got - total).abs() <= slack).all()), step
+        say("one choice", step)
+    full = weights.sum(1, keepdim=True)
+    kept, weights, lens_to = sz.evict_pages(full, T.cache, S.cache, lens, 30, 2, 8)
+    assert weights.shape == (3, 1, 30)                # as ever without room
+    for s, n in enumerate(lens.tolist()):
+        want = pick(full[s, 0, :n].tolist(), n, 30, 2, 8)
+        assert kept[s, 0].tolist() == want
+        assert torch.equal(weights[s, 0], full[s, 0, want])
