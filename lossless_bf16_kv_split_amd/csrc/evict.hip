@@ -21,11 +21,25 @@ constexpr uint64_t kCus = 256;
 // the four waves of a workgroup; up to `splits` workgroups share a tile's rows,
 // as many as the sequence has kSplitRows of them (the sums then meet in the
 // workspace).
+//
+// A call goes by its sequences' average, but a sequence with more than kFewRows
+// rows among few (a chunk of a prompt beside single tokens) goes through the
+// tile's loop in the first kernel as well, unsplit: streaming reads and places
+// every row again for each 32 keys.  Streamed and so, 128 elements, us: 16
+// single tokens and 500 new ones, group 1, 150 and 56; 255 and 1700, group 4,
+// 1700 and 460; 32 and 128 136 and 64; 32 and 64 (256 rows) 81 and 46; 63 idle
+// sequences and 256 new tokens 340 and 114.  With 64, 128 or 256 for kFewRows
+// all of these but the last border take the same.  (Workgroups of 256 keys
+// where that can be would give 41, 300 and 85, but uniform drafts, 64 of 5
+// tokens, 70.9 for 68.3.)  The kernel that has both loops takes more
+// registers, so calls of as many tokens as sequences, a decode step's, have one
+// without: such a call's chunk beside idle sequences is streamed.
+constexpr uint64_t kFewRows = 128;
 constexpr uint64_t kSplitRows = 256;
 constexpr uint64_t kSplitBytes = uint64_t{1} << 28;  // of workspace, no more
 struct WeighPlan {
     uint32_t group;   // G
-    bool few;
+    bool few, uneven;  // uneven: few, and some may have many
     uint32_t keys;    // of a workgroup
     uint32_t chunks;  // of so many keys up to max_len
     uint32_t splits;
@@ -127,150 +141,6 @@ __device__ __forceinline__ float weight_of(const Score& score, float z, float mi
     return __builtin_amdgcn_exp2f(x);
 }
 
-// ---- few rows ----------------------------------------------------------------
-//
-// Bound by the reads of keys: 48 tokens of 32/8 heads on 130 to 8192 keys, 432 MB,
-// 93 us, 4.7 TB/s.
-template <int DP, bool CAPPED>
-__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh a, WeighPlan p,
-                                                                          Score score) {
-    constexpr int kSlices = DP / 32;
-    const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const Work w(a, p);
-    const Seq seq = load_seq(a.batch, w.s, a.max_len);
-    if (!seq.good || w.tile >= seq.len) return;
-    const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
-    const int32_t past = seq.len - w.tile < (int32_t)p.keys ? seq.len : w.tile + (int32_t)p.keys;
-    const uint32_t dim = a.cache.head_dim;
-    const uint64_t line = ((uint64_t)w.s * a.cache.kv_heads + w.kv) * a.pitch;
-
-    // 16 rows from r0 on: the lane's own, its log-sum and what it sees
-    struct RowBlock {
-        bf16x8 q[kSlices];
-        float minus;
-        int32_t low, high, least;  // least: of its tokens' positions
-    };
-    const uint32_t rows = (uint32_t)count * p.group;
-    const auto load_rows = [&](uint32_t r0, RowBlock& b) {
-        const uint32_t row = r0 + n;
-        const bool on = row < rows;
-        const uint32_t token = on ? row / p.group : 0, head = on ? row % p.group : 0;
-        const uint64_t t = (uint32_t)seq.begin + token;
-        const uint32_t at = w.kv * p.group + head;
-        float lse = -INFINITY;
-        if (on) lse = *(const SZ_GLOBAL float*)(a.lse + t * a.q.heads + at);
-        const uint16_t* x = static_cast<const uint16_t*>(a.q.data) + t * a.q.token_stride +
-                            at * a.q.head_stride;
-#pragma unroll
-        for (int u = 0; u < kSlices; u++) {
-            u32x4 v = {0, 0, 0, 0};
-            if (on && 32 * u + 8 * h < dim) v = *(const SZ_GLOBAL u32x4*)(x + 32 * u + 8 * h);
-            b.q[u] = __builtin_bit_cast(bf16x8, v);
-        }
-        seen_keys(a, seq.len, c0 + (int32_t)token, b.low, b.high);
-        // (a row whose log-sum is -infinity has seen nothing)
-        if (lse == -INFINITY) b.high = b.low;
-        b.minus = -lse * kLog2e;
-    };
-    RowBlock row;
-    const uint32_t blocks = (rows + 15) / 16;
-    // 32 keys as they are loaded, DP / 8 lanes a row, which LDS turns into
-    // operands (asked for in the operands' order, 16 rows at a time, they keep
-    // the address units busy four times as long: 48 tokens 103 us, now 94.5).
-    constexpr int kLanes = DP / 8, kLoads = 32 * kLanes / (int)kWave;
-    constexpr uint32_t kRowBytes = 2 * DP, kMixMask = DP == 64 ? 7 : 15;
-    __shared__ __attribute__((aligned(256))) uint8_t turned[kWaves][32 * kRowBytes];
-    const auto mix = [](uint32_t r) { return (DP == 64 ? r >> 1 : r) & kMixMask; };
-    struct Keys {
-        u32x4 k[kLoads];
-        float before;
-    };
-    const uint32_t piece = lane % kLanes;
-    const uint32_t row_bytes = 2 * (uint32_t)a.cache.token_stride;
-    const uint32_t off0 =
-        8 * piece < dim ? lane / kLanes * row_bytes + 16 * piece : 0x80000000u;
-    // Keys of a block of 32, and what the lane's key had before.  Lane (n, h)
-    // ends with the sum of key 16 (n / 4 % 2) + 4 h + n % 4.
-    const int32_t mine = 16 * (int32_t)(n / 4 % 2) + 4 * (int32_t)h + (int32_t)(n % 4);
-    const auto load = [&](Keys& x, int32_t j) {
-        // (keys that no row sees are not read)
-        const Tokens t(a, count, c0, j, 32);
-        const int32_t upto = t.lo < t.hi ? past : j;
-#pragma unroll
-        for (int b = 0; b < 2; b++) {
-            const int32_t jb = j + 16 * b;
-            uint64_t page = 0;
-            if (jb < upto)
-                page = page_address(a.cache.k_pages, (uint64_t)w.s * a.cache.table_pitch +
-                                                         ((uint32_t)jb >> a.cache.page_log2));
-            const auto rows =
-                block_rows(a.cache, page, (uint32_t)jb & ((1u << a.cache.page_log2) - 1), w.kv,
-                           upto - jb);
-#pragma unroll
-            for (int i = 0; i < kLoads / 2; i++)
-                x.k[kLoads / 2 * b + i] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rows, off0 + i * ((int)kWave / kLanes) * row_bytes, 0, 0);
-        }
-        x.before = 0;
-        if (a.before != nullptr && j + mine < past && j + mine < c0)
-            x.before = *(const SZ_GLOBAL float*)(a.before + line + (uint32_t)(j + mine));
-    };
-    const auto compute = [&](const Keys& x, int32_t j) {
-        bf16x8 k[2][kSlices];
-        {
-            uint8_t* lds = turned[wave];
-#pragma unroll
-            for (int i = 0; i < kLoads; i++) {
-                const uint32_t r = i * (kWave / kLanes) + lane / kLanes;
-                *reinterpret_cast<u32x4*>(lds + r * kRowBytes + (piece ^ mix(r)) * 16) = x.k[i];
-            }
-            __builtin_amdgcn_wave_barrier();  // (the wave's own: in order)
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-#pragma unroll
-                for (int u = 0; u < kSlices; u++)
-                    k[i][u] = *reinterpret_cast<const bf16x8*>(
-                        lds + (16 * i + n) * kRowBytes + ((4 * u + h) ^ mix(n)) * 16);
-        }
-        float acc[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) acc[i] = 0;
-        for (uint32_t b = 0; b < blocks; b++) {
-            if (blocks > 1) load_rows(16 * b, row);
-            f32x4 z[2];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                z[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int u = 0; u < kSlices; u++)
-                    z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[i][u], row.q[u], z[i], 0, 0,
-                                                                   0);
-            }
-            const Sees sees(row.low, row.high, j + 4 * (int32_t)h);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float e = weight_of<CAPPED>(score, z[i / 4][i % 4], row.minus);
-                acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
-            }
-        }
-        const float sum = sum_lanes<8>(acc, n);
-        if (n < 8 && j + mine < past)
-            a.weights[line + (uint32_t)(j + mine)] = fmaf(a.keep, x.before, sum);
-    };
-    constexpr int32_t kStride = 32 * kWaves;
-    int32_t j = w.tile + 32 * (int32_t)wave;
-    Keys even, odd;
-    load(even, j);
-    if (blocks == 1) load_rows(0, row);
-    for (; j < past; j += 2 * kStride) {
-        load(odd, j + kStride);
-        compute(even, j);
-        load(even, j + 2 * kStride);
-        if (j + kStride < past) compute(odd, j + kStride);
-    }
-}
-
 // ---- many rows ---------------------------------------------------------------
 //
 // Rows pass in steps of 32 through LDS: each wave fetches eight of them while
@@ -280,26 +150,31 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
 // instructions, an exponential and two more for every score (63% of the cycles,
 // the products 33%): a prompt of 4096 tokens, 32/8 heads of 128, 82 to 86 us with
 // the join's 4.7.
+constexpr uint32_t kStepRows = 32;
+template <int DP>
+struct TileLds {
+    uint8_t rows[2][kStepRows * 2 * DP];
+    float minus[2][kStepRows];
+    int32_t place[2][kStepRows];  // positions; none: INT32_MIN
+};
+
+// The sums of this lane's key over the rows of split w.split of `splits`, keys
+// from w.tile on and before `past`.  All waves of the workgroup.
 template <int DP, bool CAPPED>
-__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p,
-                                                                           Score score,
-                                                                           float* ws) {
+__device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, const Score& score,
+                                           const Work& w, const Seq& seq, int32_t past,
+                                           uint32_t splits, TileLds<DP>& lds) {
     constexpr int kSlices = DP / 32;
-    constexpr uint32_t kStepRows = 32, kRowBytes = 2 * DP;
+    constexpr uint32_t kRowBytes = 2 * DP;
     constexpr int kLoads = DP / 64;  // 16-byte pieces of a lane, eight lanes a row
     constexpr uint32_t kMixMask = DP == 64 ? 7 : 15;
-    __shared__ __attribute__((aligned(256))) uint8_t staged[2][kStepRows * kRowBytes];
-    __shared__ float minus_of[2][kStepRows];
-    __shared__ int32_t place_of[2][kStepRows];  // positions; none: INT32_MIN
+    auto& staged = lds.rows;
+    auto& minus_of = lds.minus;
+    auto& place_of = lds.place;
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const Work w(a, p);
-    const Seq seq = load_seq(a.batch, w.s, a.max_len);
-    if (!seq.good || w.tile >= seq.len) return;
     const int32_t key0 = w.tile + kWaveKeys * (int32_t)wave;
     const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
-    const uint32_t splits = p.splits_of((uint64_t)count * p.group);
-    if (w.split >= splits) return;
     const uint32_t dim = a.cache.head_dim;
 
     // the rows of the tokens that see any of the workgroup's keys, in steps
@@ -382,10 +257,10 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
             return (uint32_t)(x < 0 ? 0 : x > steps ? steps : x);
         };
         const int64_t group = p.group;
-        uint32_t none = key0 < seq.len ? 0 : steps, full0 = 0, full1 = step_of(row_hi, false);
+        uint32_t none = key0 < past ? 0 : steps, full0 = 0, full1 = step_of(row_hi, false);
         if (a.causal) {
             const int64_t first = key0 - (int64_t)c0;  // the token that stands at key0
-            if (key0 < seq.len && first > 0)
+            if (key0 < past && first > 0)
                 none = first * group >= row_hi ? steps : step_of(first * group, false);
             full0 = step_of((first + kWaveKeys - 1) * group, true);
             if (a.window != 0) {
@@ -398,7 +273,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
         bf16x8 k[kBlocks][kSlices];
 #pragma unroll
         for (int b = 0; b < kBlocks; b++)
-            load_keys<kSlices>(a, w.s, w.kv, key0 + 16 * b, seq.len, lane, k[b]);
+            load_keys<kSlices>(a, w.s, w.kv, key0 + 16 * b, past, lane, k[b]);
         put(next, 0);
         // (here, or every step waits for them again, and for the rows behind)
 #pragma unroll
@@ -488,9 +363,30 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
         edges(steps);
     }
 
-    // lane (n, h) gets the sum of key 16 (n / 4) + 4 h + n % 4
-    const float sum = sum_lanes<16>(acc, n);
-    const int32_t j = key0 + 16 * (int32_t)(n / 4) + 4 * (int32_t)h + (int32_t)(n % 4);
+    return sum_lanes<16>(acc, n);
+}
+
+// The key whose sum a lane gets, of a tile's from `tile` on
+__device__ __forceinline__ int32_t tile_key(int32_t tile) {
+    const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    return tile + kWaveKeys * (int32_t)wave + 16 * (int32_t)(n / 4) + 4 * (int32_t)h +
+           (int32_t)(n % 4);
+}
+
+template <int DP, bool CAPPED>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh a, WeighPlan p,
+                                                                           Score score,
+                                                                           float* ws) {
+    __shared__ __attribute__((aligned(256))) TileLds<DP> lds;
+    const Work w(a, p);
+    const Seq seq = load_seq(a.batch, w.s, a.max_len);
+    if (!seq.good || w.tile >= seq.len) return;
+    const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
+    const uint32_t splits = p.splits_of((uint64_t)count * p.group);
+    if (w.split >= splits) return;
+    const float sum = tile_sums<DP, CAPPED>(a, p, score, w, seq, seq.len, splits, lds);
+    const int32_t j = tile_key(w.tile);
     if (j >= seq.len) return;
     const uint64_t line = (uint64_t)w.s * a.cache.kv_heads + w.kv;
     if (splits > 1) {
@@ -499,6 +395,167 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
     } else {
         const uint64_t at = line * a.pitch + (uint32_t)j;
         a.weights[at] = a.before != nullptr && j < c0 ? fmaf(a.keep, a.before[at], sum) : sum;
+    }
+}
+
+// ---- few rows ----------------------------------------------------------------
+//
+// Bound by the reads of keys: 48 tokens of 32/8 heads on 130 to 8192 keys, 432 MB,
+// 93 us, 4.7 TB/s.
+template <int DP, bool CAPPED, bool UNEVEN>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh a, WeighPlan p,
+                                                                          Score score) {
+    constexpr int kSlices = DP / 32;
+    constexpr uint32_t kRowBytes = 2 * DP;
+    __shared__ __attribute__((aligned(256))) union {
+        uint8_t turned[kWaves][32 * kRowBytes];
+        TileLds<DP> tile;
+    } lds;
+    const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    Work w(a, p);
+    const Seq seq = load_seq(a.batch, w.s, a.max_len);
+    if (!seq.good || w.tile >= seq.len) return;
+    const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
+    const int32_t past = seq.len - w.tile < (int32_t)p.keys ? seq.len : w.tile + (int32_t)p.keys;
+    const uint32_t dim = a.cache.head_dim;
+    const uint64_t line = ((uint64_t)w.s * a.cache.kv_heads + w.kv) * a.pitch;
+    if (UNEVEN && (uint64_t)count * p.group > kFewRows) {
+        w.split = 0;
+        for (; w.tile < past; w.tile += (int32_t)kTileKeys) {
+            const float sum = tile_sums<DP, CAPPED>(a, p, score, w, seq, past, 1, lds.tile);
+            const int32_t j = tile_key(w.tile);
+            if (j < past)
+                a.weights[line + (uint32_t)j] =
+                    a.before != nullptr && j < c0
+                        ? fmaf(a.keep, a.before[line + (uint32_t)j], sum) : sum;
+            lds_barrier();  // (every wave is done with the rows)
+        }
+        return;
+    }
+
+    // 16 rows from r0 on: the lane's own, its log-sum and what it sees
+    struct RowBlock {
+        bf16x8 q[kSlices];
+        float minus;
+        int32_t low, high, least;  // least: of its tokens' positions
+    };
+    const uint32_t rows = (uint32_t)count * p.group;
+    const auto load_rows = [&](uint32_t r0, RowBlock& b) {
+        const uint32_t row = r0 + n;
+        const bool on = row < rows;
+        const uint32_t token = on ? row / p.group : 0, head = on ? row % p.group : 0;
+        const uint64_t t = (uint32_t)seq.begin + token;
+        const uint32_t at = w.kv * p.group + head;
+        float lse = -INFINITY;
+        if (on) lse = *(const SZ_GLOBAL float*)(a.lse + t * a.q.heads + at);
+        const uint16_t* x = static_cast<const uint16_t*>(a.q.data) + t * a.q.token_stride +
+                            at * a.q.head_stride;
+#pragma unroll
+        for (int u = 0; u < kSlices; u++) {
+            u32x4 v = {0, 0, 0, 0};
+            if (on && 32 * u + 8 * h < dim) v = *(const SZ_GLOBAL u32x4*)(x + 32 * u + 8 * h);
+            b.q[u] = __builtin_bit_cast(bf16x8, v);
+        }
+        seen_keys(a, seq.len, c0 + (int32_t)token, b.low, b.high);
+        // (a row whose log-sum is -infinity has seen nothing)
+        if (lse == -INFINITY) b.high = b.low;
+        b.minus = -lse * kLog2e;
+    };
+    RowBlock row;
+    const uint32_t blocks = (rows + 15) / 16;
+    // 32 keys as they are loaded, DP / 8 lanes a row, which LDS turns into
+    // operands (asked for in the operands' order, 16 rows at a time, they keep
+    // the address units busy four times as long: 48 tokens 103 us, now 94.5).
+    constexpr int kLanes = DP / 8, kLoads = 32 * kLanes / (int)kWave;
+    constexpr uint32_t kMixMask = DP == 64 ? 7 : 15;
+    const auto mix = [](uint32_t r) { return (DP == 64 ? r >> 1 : r) & kMixMask; };
+    struct Keys {
+        u32x4 k[kLoads];
+        float before;
+    };
+    const uint32_t piece = lane % kLanes;
+    const uint32_t row_bytes = 2 * (uint32_t)a.cache.token_stride;
+    const uint32_t off0 =
+        8 * piece < dim ? lane / kLanes * row_bytes + 16 * piece : 0x80000000u;
+    // Keys of a block of 32, and what the lane's key had before.  Lane (n, h)
+    // ends with the sum of key 16 (n / 4 % 2) + 4 h + n % 4.
+    const int32_t mine = 16 * (int32_t)(n / 4 % 2) + 4 * (int32_t)h + (int32_t)(n % 4);
+    const auto load = [&](Keys& x, int32_t j) {
+        // (keys that no row sees are not read)
+        const Tokens t(a, count, c0, j, 32);
+        const int32_t upto = t.lo < t.hi ? past : j;
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            const int32_t jb = j + 16 * b;
+            uint64_t page = 0;
+            if (jb < upto)
+                page = page_address(a.cache.k_pages, (uint64_t)w.s * a.cache.table_pitch +
+                                                         ((uint32_t)jb >> a.cache.page_log2));
+            const auto rows =
+                block_rows(a.cache, page, (uint32_t)jb & ((1u << a.cache.page_log2) - 1), w.kv,
+                           upto - jb);
+#pragma unroll
+            for (int i = 0; i < kLoads / 2; i++)
+                x.k[kLoads / 2 * b + i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rows, off0 + i * ((int)kWave / kLanes) * row_bytes, 0, 0);
+        }
+        x.before = 0;
+        if (a.before != nullptr && j + mine < past && j + mine < c0)
+            x.before = *(const SZ_GLOBAL float*)(a.before + line + (uint32_t)(j + mine));
+    };
+    const auto compute = [&](const Keys& x, int32_t j) {
+        bf16x8 k[2][kSlices];
+        {
+            uint8_t* const to = lds.turned[wave];
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) {
+                const uint32_t r = i * (kWave / kLanes) + lane / kLanes;
+                *reinterpret_cast<u32x4*>(to + r * kRowBytes + (piece ^ mix(r)) * 16) = x.k[i];
+            }
+            __builtin_amdgcn_wave_barrier();  // (the wave's own: in order)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int u = 0; u < kSlices; u++)
+                    k[i][u] = *reinterpret_cast<const bf16x8*>(
+                        to + (16 * i + n) * kRowBytes + ((4 * u + h) ^ mix(n)) * 16);
+        }
+        float acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] = 0;
+        for (uint32_t b = 0; b < blocks; b++) {
+            if (blocks > 1) load_rows(16 * b, row);
+            f32x4 z[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                z[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int u = 0; u < kSlices; u++)
+                    z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[i][u], row.q[u], z[i], 0, 0,
+                                                                   0);
+            }
+            const Sees sees(row.low, row.high, j + 4 * (int32_t)h);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float e = weight_of<CAPPED>(score, z[i / 4][i % 4], row.minus);
+                acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
+            }
+        }
+        const float sum = sum_lanes<8>(acc, n);
+        if (n < 8 && j + mine < past)
+            a.weights[line + (uint32_t)(j + mine)] = fmaf(a.keep, x.before, sum);
+    };
+    constexpr int32_t kStride = 32 * kWaves;
+    int32_t j = w.tile + 32 * (int32_t)wave;
+    Keys even, odd;
+    load(even, j);
+    if (blocks == 1) load_rows(0, row);
+    for (; j < past; j += 2 * kStride) {
+        load(odd, j + kStride);
+        compute(even, j);
+        load(even, j + 2 * kStride);
+        if (j + kStride < past) compute(odd, j + kStride);
     }
 }
 
@@ -528,6 +585,7 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group, lines = n_seqs * c.kv_heads;
     p.few = rows <= 32 * n_seqs;
+    p.uneven = n_tokens != n_seqs && rows > kFewRows;
     p.splits = 1;
     if (p.few) {
         // as many keys a workgroup as leave four of them to a CU, 128 (a block a
@@ -567,7 +625,8 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
         x.softcap = a.softcap;
         score = score_of(x);
     }
-    if (p.few) k_weigh_few<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score);
+    if (p.few && p.uneven) k_weigh_few<DP, CAPPED, true><<<grid, block, 0, stream>>>(a, p, score);
+    else if (p.few) k_weigh_few<DP, CAPPED, false><<<grid, block, 0, stream>>>(a, p, score);
     else k_weigh_tile<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score, ws);
 }
 
