@@ -23,23 +23,21 @@ constexpr uint64_t kCus = 256;
 // workspace).
 //
 // A call goes by its sequences' average, but a sequence with more than kFewRows
-// rows among few (a chunk of a prompt beside single tokens) goes through the
-// tile's loop in the first kernel as well, unsplit: streaming reads and places
-// every row again for each 32 keys.  Streamed and so, 128 elements, us: 16
-// single tokens and 500 new ones, group 1, 150 and 56; 255 and 1700, group 4,
-// 1700 and 460; 32 and 128 136 and 64; 32 and 64 (256 rows) 81 and 46; 63 idle
-// sequences and 256 new tokens 340 and 114.  With 64, 128 or 256 for kFewRows
-// all of these but the last border take the same.  (Workgroups of 256 keys
-// where that can be would give 41, 300 and 85, but uniform drafts, 64 of 5
-// tokens, 70.9 for 68.3.)  The kernel that has both loops takes more
-// registers, so calls of as many tokens as sequences, a decode step's, have one
-// without: such a call's chunk beside idle sequences is streamed.
+// rows among few (a chunk of a prompt beside single tokens, or idle sequences)
+// goes through the tile's loop in the first kernel as well, unsplit: streaming
+// reads and places every row again for each 32 keys.  Streamed and so, 128
+// elements, us: 16 single tokens and 500 new ones, group 1, 149 and 70; 255 and
+// 1700, group 4, 1738 and 597; 32 and 128 136 and 75; 32 and 64 (256 rows) 78 and
+// 53; 63 idle sequences and 256 new tokens 345 and 130; 24 and 500, 256 elements,
+// 57 and 34.  With 64 or 256 for kFewRows they take the same, but for the 256
+// rows, streamed with 256.  (Workgroups of 256 keys where that can be took a
+// third off some, but cost uniform drafts, 64 of 5 tokens, 70.9 for 68.3.)
 constexpr uint64_t kFewRows = 128;
 constexpr uint64_t kSplitRows = 256;
 constexpr uint64_t kSplitBytes = uint64_t{1} << 28;  // of workspace, no more
 struct WeighPlan {
     uint32_t group;   // G
-    bool few, uneven;  // uneven: few, and some may have many
+    bool few;
     uint32_t keys;    // of a workgroup
     uint32_t chunks;  // of so many keys up to max_len
     uint32_t splits;
@@ -48,9 +46,12 @@ struct WeighPlan {
         return most < 1 ? 1 : most < splits ? (uint32_t)most : splits;
     }
 };
-constexpr int kBlocks = 4;  // of 16 keys, a wave's of a tile
-constexpr int kWaveKeys = 16 * kBlocks;
-constexpr uint32_t kTileKeys = kWaves * kWaveKeys;
+// Blocks of 16 keys that a wave has of a tile, and a tile's keys.  Within
+// k_weigh_few half of them, for which its registers are enough: four take 20%
+// off such chunks, but cost all batches of few rows a wave or two a SIMD with 64
+// elements (64 drafts of 5 tokens 44 us, not 36.5) and spills with 128 and 256.
+constexpr int kBlocks = 4, kBlocksFew = 2;
+constexpr uint32_t tile_keys(int blocks) { return kWaves * 16 * blocks; }
 
 // What a workgroup works on
 struct Work {
@@ -147,9 +148,9 @@ __device__ __forceinline__ float weight_of(const Score& score, float z, float mi
 // the step before is worked on, one barrier a step.  LDS rows are cut into
 // 16-byte pieces, piece c of row r at c ^ (r & 15) (r >> 1 & 7 with 64
 // elements), so that 16 rows' same piece lies in 16 places.  Bound by the vector
-// instructions, an exponential and two more for every score (63% of the cycles,
-// the products 33%): a prompt of 4096 tokens, 32/8 heads of 128, 82 to 86 us with
-// the join's 4.7.
+// instructions, an exponential and two more for every score (62% of the cycles,
+// the products 33%): a prompt of 4096 tokens, 32/8 heads of 128, 81 to 98 us by
+// card with the join's 4.7.
 constexpr uint32_t kStepRows = 32;
 template <int DP>
 struct TileLds {
@@ -160,7 +161,7 @@ struct TileLds {
 
 // The sums of this lane's key over the rows of split w.split of `splits`, keys
 // from w.tile on and before `past`.  All waves of the workgroup.
-template <int DP, bool CAPPED>
+template <int DP, bool CAPPED, int BLOCKS>
 __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, const Score& score,
                                            const Work& w, const Seq& seq, int32_t past,
                                            uint32_t splits, TileLds<DP>& lds) {
@@ -173,20 +174,21 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
     auto& place_of = lds.place;
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    constexpr int kWaveKeys = 16 * BLOCKS;
     const int32_t key0 = w.tile + kWaveKeys * (int32_t)wave;
     const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
     const uint32_t dim = a.cache.head_dim;
 
     // the rows of the tokens that see any of the workgroup's keys, in steps
-    const Tokens t(a, count, c0, w.tile, (int32_t)kTileKeys);
+    const Tokens t(a, count, c0, w.tile, (int32_t)tile_keys(BLOCKS));
     const uint32_t row_lo = (uint32_t)t.lo * p.group, row_hi = (uint32_t)t.hi * p.group;
     const uint64_t all = (row_hi - row_lo + kStepRows - 1) / kStepRows;
     const uint32_t step0 = (uint32_t)(all * w.split / splits);
     const uint32_t steps = (uint32_t)(all * (w.split + 1) / splits) - step0;
 
-    float acc[16];  // keys 16 b + 4 h + i of key0
+    float acc[4 * BLOCKS];  // keys 16 b + 4 h + i of key0
 #pragma unroll
-    for (int i = 0; i < 16; i++) acc[i] = 0;
+    for (int i = 0; i < 4 * BLOCKS; i++) acc[i] = 0;
     if (steps > 0) {
         // the row that this lane fetches a part of: its address and its
         // log-sum's move on by a step's tokens and heads, with or without a
@@ -270,14 +272,14 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
         }
         Fetch next;
         fetch(next);
-        bf16x8 k[kBlocks][kSlices];
+        bf16x8 k[BLOCKS][kSlices];
 #pragma unroll
-        for (int b = 0; b < kBlocks; b++)
+        for (int b = 0; b < BLOCKS; b++)
             load_keys<kSlices>(a, w.s, w.kv, key0 + 16 * b, past, lane, k[b]);
         put(next, 0);
         // (here, or every step waits for them again, and for the rows behind)
 #pragma unroll
-        for (int b = 0; b < kBlocks; b++)
+        for (int b = 0; b < BLOCKS; b++)
 #pragma unroll
             for (int u = 0; u < kSlices; u++) asm volatile("" : "+v"(k[b][u]));
         fetch(next);
@@ -285,7 +287,7 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
         uint32_t step = 0;
         // 16 of a step's rows: the lane's, its products with the keys
         struct Products {
-            f32x4 z[kBlocks];
+            f32x4 z[BLOCKS];
             float minus;
             int32_t place;
         };
@@ -299,7 +301,7 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
                 q[u] = *reinterpret_cast<const bf16x8*>(
                     &staged[buffer][(16 * r + n) * kRowBytes + ((4 * u + h) ^ q_mix) * 16]);
 #pragma unroll
-            for (int b = 0; b < kBlocks; b++) {
+            for (int b = 0; b < BLOCKS; b++) {
                 x.z[b] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int u = 0; u < kSlices; u++)
@@ -325,7 +327,7 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
                     if (x.place == INT32_MIN) high = low;
                     const Sees sees(low, high, key0 + 4 * (int32_t)h);
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
+                    for (int i = 0; i < 4 * BLOCKS; i++) {
                         const float e = weight_of<CAPPED>(score, x.z[i / 4][i % 4], x.minus);
                         acc[i] += sees(16 * (i / 4) + i % 4) ? e : 0.0f;
                     }
@@ -349,13 +351,13 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
                 const bool nothing = x.place == INT32_MIN;
                 if (__ballot(nothing) != 0) {
 #pragma unroll
-                    for (int b = 0; b < kBlocks; b++)
+                    for (int b = 0; b < BLOCKS; b++)
 #pragma unroll
                         for (int i = 0; i < 4; i++) x.z[b][i] = nothing ? 0 : x.z[b][i];
                     x.minus = nothing ? -INFINITY : x.minus;
                 }
 #pragma unroll
-                for (int i = 0; i < 16; i++)
+                for (int i = 0; i < 4 * BLOCKS; i++)
                     acc[i] += weight_of<CAPPED>(score, x.z[i / 4][i % 4], x.minus);
             }
             end_step();
@@ -363,14 +365,17 @@ __device__ __forceinline__ float tile_sums(const Weigh& a, const WeighPlan& p, c
         edges(steps);
     }
 
-    return sum_lanes<16>(acc, n);
+    return sum_lanes<4 * BLOCKS>(acc, n);
 }
 
-// The key whose sum a lane gets, of a tile's from `tile` on
+// The key whose sum a lane gets, of a tile's from `tile` on (past every key where
+// another lane has it too)
+template <int BLOCKS>
 __device__ __forceinline__ int32_t tile_key(int32_t tile) {
     const uint32_t lane = threadIdx.x % kWave, n = lane % 16, h = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    return tile + kWaveKeys * (int32_t)wave + 16 * (int32_t)(n / 4) + 4 * (int32_t)h +
+    if (n >= 4 * BLOCKS) return INT32_MAX;
+    return tile + 16 * BLOCKS * (int32_t)wave + 16 * (int32_t)(n / 4) + 4 * (int32_t)h +
            (int32_t)(n % 4);
 }
 
@@ -385,8 +390,8 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
     const int32_t count = seq.end - seq.begin, c0 = seq.len - count;
     const uint32_t splits = p.splits_of((uint64_t)count * p.group);
     if (w.split >= splits) return;
-    const float sum = tile_sums<DP, CAPPED>(a, p, score, w, seq, seq.len, splits, lds);
-    const int32_t j = tile_key(w.tile);
+    const float sum = tile_sums<DP, CAPPED, kBlocks>(a, p, score, w, seq, seq.len, splits, lds);
+    const int32_t j = tile_key<kBlocks>(w.tile);
     if (j >= seq.len) return;
     const uint64_t line = (uint64_t)w.s * a.cache.kv_heads + w.kv;
     if (splits > 1) {
@@ -401,8 +406,8 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_tile(Weigh
 // ---- few rows ----------------------------------------------------------------
 //
 // Bound by the reads of keys: 48 tokens of 32/8 heads on 130 to 8192 keys, 432 MB,
-// 93 us, 4.7 TB/s.
-template <int DP, bool CAPPED, bool UNEVEN>
+// 86 to 95 us by card, 4.5 to 5.0 TB/s.
+template <int DP, bool CAPPED>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh a, WeighPlan p,
                                                                           Score score) {
     constexpr int kSlices = DP / 32;
@@ -420,11 +425,12 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 2 : 3) void k_weigh_few(Weigh 
     const int32_t past = seq.len - w.tile < (int32_t)p.keys ? seq.len : w.tile + (int32_t)p.keys;
     const uint32_t dim = a.cache.head_dim;
     const uint64_t line = ((uint64_t)w.s * a.cache.kv_heads + w.kv) * a.pitch;
-    if (UNEVEN && (uint64_t)count * p.group > kFewRows) {
+    if ((uint64_t)count * p.group > kFewRows) {
         w.split = 0;
-        for (; w.tile < past; w.tile += (int32_t)kTileKeys) {
-            const float sum = tile_sums<DP, CAPPED>(a, p, score, w, seq, past, 1, lds.tile);
-            const int32_t j = tile_key(w.tile);
+        for (; w.tile < past; w.tile += (int32_t)tile_keys(kBlocksFew)) {
+            const float sum =
+                tile_sums<DP, CAPPED, kBlocksFew>(a, p, score, w, seq, past, 1, lds.tile);
+            const int32_t j = tile_key<kBlocksFew>(w.tile);
             if (j < past)
                 a.weights[line + (uint32_t)j] =
                     a.before != nullptr && j < c0
@@ -585,7 +591,6 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
     p.group = q_heads / c.kv_heads;
     const uint64_t rows = n_tokens * p.group, lines = n_seqs * c.kv_heads;
     p.few = rows <= 32 * n_seqs;
-    p.uneven = n_tokens != n_seqs && rows > kFewRows;
     p.splits = 1;
     if (p.few) {
         // as many keys a workgroup as leave four of them to a CU, 128 (a block a
@@ -594,14 +599,14 @@ WeighPlan plan_weigh(uint32_t q_heads, const Cache& c, uint64_t n_seqs, uint64_t
         while (keys > 128 && (max_len + keys - 1) / keys * lines < 4 * kCus) keys /= 2;
         p.keys = (uint32_t)keys;
     } else {
-        p.keys = kTileKeys;
+        p.keys = tile_keys(kBlocks);
     }
     p.chunks = (uint32_t)((max_len + p.keys - 1) / p.keys);
     if (!p.few) {
         // Rows among so many workgroups that the causal ones' uneven shares even
         // out, or one long sequence among short ones fills the chip: by the
         // tiles of those sequences that can have 2048 rows (a prompt of 4096
-        // tokens, 128 tiles: 96 us in 12 parts each, 95 in 16, 100 in 24; 500
+        // tokens, 128 tiles: 93 us in 12 parts each, 92 in 16, 98 in 24; 500
         // tokens beside 24 single ones, 256 elements, capped: 193 us whole).
         const uint64_t long_seqs = rows / 2048 < 1 ? 1 : rows / 2048 < n_seqs ? rows / 2048 : n_seqs;
         uint64_t splits = 8 * kCus / (uint64_t{p.chunks} * c.kv_heads * long_seqs);
@@ -625,8 +630,7 @@ void go(const Weigh& a, const WeighPlan& p, float* ws, hipStream_t stream) {
         x.softcap = a.softcap;
         score = score_of(x);
     }
-    if (p.few && p.uneven) k_weigh_few<DP, CAPPED, true><<<grid, block, 0, stream>>>(a, p, score);
-    else if (p.few) k_weigh_few<DP, CAPPED, false><<<grid, block, 0, stream>>>(a, p, score);
+    if (p.few) k_weigh_few<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score);
     else k_weigh_tile<DP, CAPPED><<<grid, block, 0, stream>>>(a, p, score, ws);
 }
 
