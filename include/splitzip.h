@@ -701,8 +701,8 @@ sz_status sz_attend_expanded(const sz_heads *q, const sz_heads *out, float *d_ls
  * sequence without new tokens has keep * before.  Entries from d_lens[s] on are
  * left as they were.  A row whose log-sum is -infinity adds nothing; a row adds
  * nothing to keys that it does not see, whatever its bits and theirs.  FP32
- * throughout; the order of additions is fixed by the call's sizes.  Only keys
- * are read: d_v_pages of the cache may be the key table.
+ * throughout; the order of additions is fixed by the call's sizes and starts.
+ * Only keys are read: d_v_pages of the cache may be the key table.
  *   q, d_lse   as sz_attend_pages took and left them (d_lse float[n_tokens]
  *              [q heads]); limits of q's heads and tokens as there
  *   d_before   optional device float[n_seqs][kv_heads][weights_pitch]; not read

@@ -1,5 +1,6 @@
 // kv_internal.h -- shared by the operators on a paged cache (append.hip,
-// attend.hip) and their entry points (kv_api.hip); not installed.
+// attend.hip, latent.hip, evict.hip) and their entry points (kv_api.hip); not
+// installed.
 #pragma once
 
 #include "sz_internal.h"

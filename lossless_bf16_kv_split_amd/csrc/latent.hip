@@ -11,11 +11,11 @@
 // the same copy of the keys in LDS: what is loaded once is read as keys and,
 // transposed by the LDS reads, as values.
 //
-// 48 tokens of 128 heads on 100 to 8192 keys (196 MB of rows): 91 to 96 us, of
-// which the join 10.  A step of 64 keys takes about 4800 cycles: 1900 for the
-// scores, bound by LDS (their reads 1152, the next step's rows arriving 576),
-// 1060 for the output, 1200 for the softmax and its barrier, 600 waiting for the
-// rows.  LDS holds two steps' keys and one workgroup a CU, so nothing runs
+// 48 tokens of 128 heads on 100 to 8192 keys (196 MB of rows): 86 to 103 us
+// by card, of which the join 10 to 12.  A step of 64 keys takes about 4800
+// cycles: 1900 for the scores, bound by LDS (their reads 1152, the next step's
+// rows arriving 576), 1060 for the output, 1200 for the softmax and its barrier,
+// 600 waiting for the rows.  LDS holds two steps' keys and one workgroup a CU, so nothing runs
 // beside a wave's wait.
 //
 // What beginning a tile costs, in steps, so that it is shared out with them
